@@ -63,6 +63,8 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_LENGTH 4 /* a context length or cu_seqlens span outside its contract
                               (negative, longer than the block table covers, k_len < q_len,
                               q_len > max_seqlen_q): the sequence's output rows are zero */
+#define PA_DEVERR_POSITION 16 /* a token's position lies outside the cosine/sine table: the token
+                              is skipped */
 #define PA_DEVERR_TIMEOUT 8 /* an internal wait (on an asynchronous copy or on another warp)
                                gave up after about half a second: the kernel stopped early and
                                its outputs are incomplete */
@@ -88,6 +90,49 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 pa_status pa_store_kv(const void *k, const void *v, void *k_cache, void *v_cache,
                       const int32_t *slot_mapping, int T, int num_blocks, int block_size, int Hkv,
                       int D, pa_dtype dtype, int32_t *err, cudaStream_t stream);
+
+/*
+ * pa_rope_store_kv: rotate a step's queries and keys at their positions and append the keys and
+ * values to the pools, in one launch (the step before pa_decode, pa_chunk_attn or pool-path
+ * pa_prefill_varlen).
+ *
+ * Source: as pa_store_kv; the rotation is the position embedding of the engines' Qwen models
+ * ("mini-vLLM": a Qwen2 engine; smzdm deep dive "模型实现细节": Qwen3), with its multi-axis form.
+ *
+ *   for t in [0, T): s = slot_mapping[t]; if s < 0 skip the token: none of its rows is read or
+ *       written (padding)
+ *       for pair i in [0, rot_dim / 2): pos = positions[pair_axis[i]][t]
+ *           (x0, x1) -> (x0 * cos - x1 * sin, x1 * cos + x0 * sin),
+ *           cos = cos_sin[pos][i], sin = cos_sin[pos][rot_dim / 2 + i]
+ *       q_out[t] = rotated q[t];  k_cache row s = rotated k[t];  v_cache row s = v[t] (bit copy)
+ *
+ * Pair i of a head row is elements i and rot_dim / 2 + i, or, with `interleaved`, 2i and 2i + 1.
+ * Elements from rot_dim on are copied. Products and sums in fp32, rounded once.
+ *
+ * q, q_out      [T, Hq, D], k, v [T, Hkv, D]; the heads of a token contiguous, tokens
+ *               q_stride, q_out_stride, k_stride, v_stride elements apart (slices of one
+ *               projection's output, for instance). Strides are multiples of 8, at least Hq * D or
+ *               Hkv * D. q_out may be q itself (same pointer and stride); any other overlap of
+ *               q_out's span with the spans of q, k or v is PA_ERR_UNSUPPORTED.
+ * slot_mapping  int32 [T], as pa_store_kv.
+ * positions     int32 [n_axes, T], 1 <= n_axes <= 4. A position outside [0, max_pos) on any axis
+ *               sets PA_DEVERR_POSITION and the token is skipped.
+ * pair_axis     HOST pointer, rot_dim / 2 bytes < n_axes (read during the call): the axis of each
+ *               pair. NULL: every pair takes axis 0.
+ * cos_sin       fp32 [max_pos, rot_dim], each row the cosines, then the sines, of a position's
+ *               rot_dim / 2 angles (any scaling of frequencies or amplitude included), 16-byte
+ *               aligned. Compute the angles in 64 bits: at position 10^5 fp32 products are off
+ *               by up to 4e-3 radians.
+ * Supported: D % 8 == 0; rot_dim a multiple of 16, 16 <= rot_dim <= min(D, 256).
+ * T == 0 is a no-op. Bytes moved: T * D * 2 * (2 * Hq + 4 * Hkv), and the table rows.
+ */
+pa_status pa_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                           const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           void *k_cache, void *v_cache, const int32_t *slot_mapping,
+                           const int32_t *positions, int n_axes, const uint8_t *pair_axis,
+                           const float *cos_sin, int max_pos, int rot_dim, int interleaved, int T,
+                           int num_blocks, int block_size, int Hq, int Hkv, int D, pa_dtype dtype,
+                           int32_t *err, cudaStream_t stream);
 
 /*
  * pa_decode_workspace_size: bytes of scratch pa_decode needs for these sizes on the current

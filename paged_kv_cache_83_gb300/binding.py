@@ -16,8 +16,8 @@ PKG = Path(__file__).resolve().parent
 LIB_PATH = PKG / "_build" / "libpagedattn.so"
 
 PA_F16, PA_BF16 = 0, 1
-PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT = 1, 2, 4, 8
-EXPORTS = ("pa_store_kv", "pa_decode_workspace_size", "pa_decode", "pa_store_decode",
+PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION = 1, 2, 4, 8, 16
+EXPORTS = ("pa_store_kv", "pa_rope_store_kv", "pa_decode_workspace_size", "pa_decode", "pa_store_decode",
            "pa_store_decode_host", "pa_store_decode_host_workspace_size", "pa_store_decode_host_layout",
            "pa_prefill_varlen", "pa_decode_noalloc", "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
            "pa_bm_destroy", "pa_bm_allocate", "pa_bm_can_allocate", "pa_bm_append",
@@ -46,6 +46,10 @@ def load(path: Path | str = LIB_PATH) -> ctypes.CDLL:
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     lib.pa_store_kv.argtypes = [P, P, P, P, P, I, I, I, I, I, I, P, P]
     lib.pa_store_kv.restype = I
+    L = ctypes.c_int64
+    lib.pa_rope_store_kv.argtypes = [P, L, P, L, P, L, P, L, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, I,
+                                     P, P]
+    lib.pa_rope_store_kv.restype = I
     lib.pa_decode_workspace_size.argtypes = [I, I, I, I, I, I]
     lib.pa_decode_workspace_size.restype = Z
     lib.pa_decode.argtypes = [P, P, P, P, P, I, P, I, I, I, I, I, I, F, I, P, Z, P, P]
@@ -65,7 +69,6 @@ def load(path: Path | str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_decode_noalloc.restype = I
     lib.pa_decode_debug_tail_units.argtypes = [P, I, I, I, I, I, I]
     lib.pa_decode_debug_tail_units.restype = I
-    L = ctypes.c_int64
     lib.pa_bm_create.argtypes = [I, I, I]
     lib.pa_bm_create.restype = P
     lib.pa_bm_destroy.argtypes = [P]
@@ -136,6 +139,16 @@ def _stream(stream, ref: torch.Tensor) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _elsewhere(ref: torch.Tensor, *others) -> bool:
+    """Whether the call's device, ref's, is not the current one (the caller then makes it current
+    for the call). Raises when the tensors (None: not given) are on different devices."""
+    dev = ref.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on one CUDA device")
+    return dev >= 0 and dev != torch._C._cuda_getDevice()
+
+
 def _check(fn: str, status: int) -> None:
     if status != 0:
         raise PagedAttnError(fn, status)
@@ -155,6 +168,69 @@ def pa_store_kv(k, v, k_cache, v_cache, slot_mapping, err=None, stream=None) -> 
     _check("pa_store_kv", load().pa_store_kv(
         _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _i32(slot_mapping, "slot_mapping"), T, NB,
         bs, Hkv, D, dt, _i32(err, "err"), _stream(stream, k)))
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """The elements between tokens of a [T, heads, D] tensor whose tokens may lie apart."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    T, H, D = t.shape
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return stride[0] if T > 1 else H * D
+
+
+def rope_pair_axis(sections, interleaved: bool = False) -> bytes:
+    """The axis of each rotated pair, as pa_rope_store_kv takes it: `sections[a]` pairs for axis a,
+    one section after the other; interleaved: the axes in turns (0, 1, 2, 0, 1, 2, ...) until
+    sections[a] pairs have gone to each axis a > 0, axis 0 for all others."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4 or min(sections) < 0:
+        raise ValueError("one to four sections of at least 0 pairs")
+    if not interleaved:
+        return b"".join(bytes([a]) * n for a, n in enumerate(sections))
+    A, total = len(sections), sum(sections)
+    if any(n and a + A * (n - 1) >= total for a, n in enumerate(sections) if a):
+        raise ValueError("the sections do not fit in turns")
+    return bytes(i % A if i < A * sections[i % A] else 0 for i in range(total))
+
+
+def pa_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, pair_axis=None,
+                     interleaved: bool = False, err=None, stream=None) -> None:
+    """Rotate q [T, Hq, D] (into q_out) and k [T, Hkv, D] at positions [T] or [axes, T] with the
+    table cos_sin [max_pos, rot_dim] (cosines, then sines) and append k, v to the pools at
+    slot_mapping [T]. q, q_out, k and v may be views whose tokens lie apart (slices of one
+    projection's output); q_out may be q itself. pair_axis: bytes, the axis of each rotated pair
+    (rope_pair_axis)."""
+    NB, bs, Hkv, D = k_cache.shape
+    T, Hq, _ = q.shape
+    if q.shape[2] != D or q_out.shape != q.shape or k.shape != (T, Hkv, D) or v.shape != k.shape or \
+            v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    n_axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.shape[-1] != T or positions.dim() > 2:
+        raise ValueError("positions must be [T] or [axes, T]")
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise TypeError("cos_sin must be a float32 [max_pos, rot_dim] table")
+    max_pos, rot = cos_sin.shape
+    if pair_axis is not None and (type(pair_axis) is not bytes or len(pair_axis) != rot // 2):
+        raise ValueError("pair_axis must be rot_dim / 2 bytes")
+    if _elsewhere(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, err):
+        with torch.cuda.device(q.device):
+            return pa_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, pair_axis,
+                                    interleaved, err, stream)
+    dtype = k_cache.dtype
+    dt = _dtype(k_cache)
+    if q.dtype != dtype or q_out.dtype != dtype or k.dtype != dtype or v.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("q, q_out, k, v and the pools must share a dtype")
+    _check("pa_rope_store_kv", load().pa_rope_store_kv(
+        q_out.data_ptr(), _token_stride(q_out, "q_out"), q.data_ptr(), _token_stride(q, "q"), k.data_ptr(),
+        _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"), _ptr(k_cache), _ptr(v_cache),
+        _i32(slot_mapping, "slot_mapping"), _i32(positions, "positions"), n_axes, pair_axis, _ptr(cos_sin),
+        max_pos, rot, int(bool(interleaved)), T, NB, bs, Hq, Hkv, D, dt, _i32(err, "err"), _stream(stream, q)))
 
 
 def pa_decode_workspace_size(B: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,

@@ -95,6 +95,74 @@ pa_status pa_store_kv(const void *k, const void *v, void *k_cache, void *v_cache
     return from_cuda(pa::launch_store_kv(a, stream));
 }
 
+pa_status pa_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                           const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           void *k_cache, void *v_cache, const int32_t *slot_mapping,
+                           const int32_t *positions, int n_axes, const uint8_t *pair_axis,
+                           const float *cos_sin, int max_pos, int rot_dim, int interleaved, int T,
+                           int num_blocks, int block_size, int Hq, int Hkv, int D, pa_dtype dtype,
+                           int32_t *err, cudaStream_t stream) {
+    if (!dtype_ok(dtype)) return PA_ERR_DTYPE;
+    if (T < 0 || num_blocks < 0 || block_size < 1 || Hq < 1 || Hkv < 1 || D < 1 || n_axes < 1 || max_pos < 0 ||
+        rot_dim < 0 || (interleaved != 0 && interleaved != 1))
+        return PA_ERR_SHAPE;
+    if (D % 8 || rot_dim % 16 || rot_dim < 16 || rot_dim > 256 || n_axes > 4) return PA_ERR_UNSUPPORTED;
+    if (rot_dim > D) return PA_ERR_SHAPE;
+    const int64_t qw = static_cast<int64_t>(Hq) * D, kw = static_cast<int64_t>(Hkv) * D;
+    // 2^24 elements a token and 2^40 a stride keep every byte offset below in 64 bits
+    if (Hq > 65535 || Hkv > 65535 || qw > (1 << 24) || kw > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    if (T == 0) return PA_OK;
+    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions || !cos_sin)
+        return PA_ERR_NULL;
+    if (q_stride < qw || q_out_stride < qw || k_stride < kw || v_stride < kw) return PA_ERR_SHAPE;
+    if ((q_stride | q_out_stride | k_stride | v_stride) % 8) return PA_ERR_UNSUPPORTED;
+    const int64_t most = int64_t{1} << 40;
+    if (q_stride > most / T || q_out_stride > most / T || k_stride > most / T || v_stride > most / T)
+        return PA_ERR_UNSUPPORTED;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(cos_sin))
+        return PA_ERR_UNSUPPORTED;
+    for (int i = 0; pair_axis && i < rot_dim / 2; ++i)
+        if (pair_axis[i] >= n_axes) return PA_ERR_SHAPE;
+    if (static_cast<long long>(T) * (Hq + 2ll * Hkv) * ((D + 15) / 16 + 1) / 256 > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
+    // q_out is q itself or lies clear of everything that is read
+    auto span_meets = [&](const void *p, int64_t stride, int64_t width) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q_out), b = reinterpret_cast<uintptr_t>(p);
+        return a < b + 2 * ((T - 1) * stride + width) && b < a + 2 * ((T - 1) * q_out_stride + qw);
+    };
+    if (!(q_out == q && q_out_stride == q_stride) &&
+        (span_meets(q, q_stride, qw) || span_meets(k, k_stride, kw) || span_meets(v, v_stride, kw)))
+        return PA_ERR_UNSUPPORTED;
+    pa::RopeStoreArgs a{};
+    a.q_out = q_out;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out_stride = q_out_stride;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.slot_mapping = slot_mapping;
+    a.positions = positions;
+    a.pair_axis = pair_axis;
+    a.cos_sin = cos_sin;
+    a.n_axes = n_axes;
+    a.max_pos = max_pos;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.T = T;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.dtype = dtype;
+    a.err = err;
+    return from_cuda(pa::launch_rope_store_kv(a, stream));
+}
+
 size_t pa_decode_workspace_size(int B, int Hq, int Hkv, int D, int max_blocks_per_seq,
                                 int block_size) {
     if (B <= 0 || check_heads(Hq, Hkv, D) != PA_OK || max_blocks_per_seq < 0 || block_size < 1)

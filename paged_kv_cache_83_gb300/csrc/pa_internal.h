@@ -33,6 +33,24 @@ struct StoreArgs {
 cudaError_t launch_store_kv(const StoreArgs &a, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------------------
+// Rotation + append (rope_store_kv.cu). Strides in elements; pair_axis: host bytes or nullptr.
+struct RopeStoreArgs {
+    void *q_out;
+    const void *q, *k, *v;
+    long long q_out_stride, q_stride, k_stride, v_stride;
+    void *k_cache, *v_cache;
+    const int32_t *slot_mapping, *positions;
+    const uint8_t *pair_axis;
+    const float *cos_sin;
+    int n_axes, max_pos, rot_dim;
+    bool interleaved;
+    int T, num_blocks, block_size, Hq, Hkv, D;
+    pa_dtype dtype;
+    int32_t *err;
+};
+cudaError_t launch_rope_store_kv(const RopeStoreArgs &a, cudaStream_t stream);
+
+// ------------------------------------------------------------------------------------------
 // Decode: one persistent CTA per SM streams an equal share of the (sequence, kv head, tile)
 // space; pieces of a context shared by two CTAs are combined by a small merge kernel.
 struct DecodePlan {

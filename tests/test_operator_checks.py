@@ -1,0 +1,104 @@
+"""What the layer-step and sampling operators refuse, without a GPU: the status codes of the C entry
+points and the exceptions of the binding. Every call here fails a host-side check or is an empty
+no-op, so nothing is launched."""
+import pytest
+import torch
+
+import paged_kv_cache_83_gb300 as pa
+from paged_kv_cache_83_gb300 import binding
+
+NULL, SHAPE, DTYPE, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4, 5
+FAKE = 1 << 20  # a non-null, 16-byte aligned address that no launch ever sees
+FAR = 1 << 30   # another, clear of FAKE's spans
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not binding.LIB_PATH.exists():
+        from paged_kv_cache_83_gb300 import build
+        build.build()
+    return pa.load()
+
+
+def _rope(lib, **kw):
+    a = dict(qo=FAR, qos=256, q=FAKE, qs=256, k=FAKE, ks=128, v=FAKE, vs=128, kc=FAKE, vc=FAKE, sm=FAKE, pos=FAKE,
+             axes=1, pair=None, table=FAKE, max_pos=100, rot=64, inter=0, T=4, nb=8, bs=16, Hq=4, Hkv=2, D=64, dt=0,
+             err=None, stream=None)
+    a.update(kw)
+    return lib.pa_rope_store_kv(*a.values())
+
+
+def test_rope_store_refusals(lib):
+    assert _rope(lib, dt=2) == DTYPE
+    assert _rope(lib, T=-1) == SHAPE
+    assert _rope(lib, bs=0) == SHAPE
+    assert _rope(lib, Hq=0) == SHAPE
+    assert _rope(lib, axes=0) == SHAPE
+    assert _rope(lib, inter=2) == SHAPE
+    assert _rope(lib, rot=80) == SHAPE               # wider than a head
+    assert _rope(lib, D=60) == UNSUPPORTED
+    assert _rope(lib, rot=24) == UNSUPPORTED
+    assert _rope(lib, rot=0) == UNSUPPORTED
+    assert _rope(lib, D=512, rot=272, qs=2048, qos=2048, ks=1024, vs=1024) == UNSUPPORTED
+    assert _rope(lib, axes=5) == UNSUPPORTED
+    assert _rope(lib, T=0) == 0                      # empty: no-op
+    for name in ("qo", "q", "k", "v", "kc", "vc", "sm", "pos", "table"):
+        assert _rope(lib, **{name: None}) == NULL
+    assert _rope(lib, qs=248) == SHAPE               # tokens that run into each other
+    assert _rope(lib, ks=0) == SHAPE
+    assert _rope(lib, vs=132) == UNSUPPORTED         # tokens off the 16-byte grid
+    assert _rope(lib, qos=1 << 41) == UNSUPPORTED
+    assert _rope(lib, k=FAKE + 2) == UNSUPPORTED
+    assert _rope(lib, table=FAKE + 4) == UNSUPPORTED
+    assert _rope(lib, pair=bytes([0] * 31 + [1])) == SHAPE   # an axis that is not there
+
+
+def test_rope_store_refuses_overlap(lib):
+    # q_out starts inside q, covers k, or is q with another stride
+    assert _rope(lib, qo=FAKE + 512) == UNSUPPORTED
+    assert _rope(lib, qo=FAKE, qos=264) == UNSUPPORTED
+    assert _rope(lib, q=1 << 25, k=FAR + 1024) == UNSUPPORTED
+    assert _rope(lib, q=1 << 25, v=FAR - 1024 + 16) == UNSUPPORTED
+
+
+def test_pair_axis_of_sections():
+    assert list(pa.rope_pair_axis([2, 3, 1])) == [0, 0, 1, 1, 1, 2]
+    assert list(pa.rope_pair_axis([4, 2, 2], interleaved=True)) == [0, 1, 2, 0, 1, 2, 0, 0]
+    assert list(pa.rope_pair_axis([4, 2, 1], interleaved=True)) == [0, 1, 2, 0, 1, 0, 0]
+    assert list(pa.rope_pair_axis([3])) == [0, 0, 0]
+    for bad in ([], [1, 1, 1, 1, 1], [4, -1]):
+        with pytest.raises(ValueError):
+            pa.rope_pair_axis(bad)
+    with pytest.raises(ValueError):
+        pa.rope_pair_axis([1, 4, 4], interleaved=True)
+
+
+def test_rope_store_binding_refusals():
+    q, k = torch.zeros(3, 4, 64, dtype=torch.float16), torch.zeros(3, 2, 64, dtype=torch.float16)
+    pool = torch.zeros(2, 16, 2, 64, dtype=torch.float16)
+    idx = torch.zeros(3, dtype=torch.int32)
+    table = torch.zeros(8, 64)
+
+    def call(q_out=q, q=q, k=k, v=k, kc=pool, vc=pool, slots=idx, pos=idx, table=table, **kw):
+        pa.pa_rope_store_kv(q_out, q, k, v, kc, vc, slots, pos, table, **kw)
+
+    with pytest.raises(ValueError):                  # not on a CUDA device
+        call()
+    with pytest.raises(ValueError):
+        call(q_out=q[:2])
+    with pytest.raises(ValueError):
+        call(v=k[:, :1])
+    with pytest.raises(ValueError):
+        call(slots=idx[:2])
+    with pytest.raises(ValueError):
+        call(pos=torch.zeros(2, 2, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        call(table=table.half())
+    with pytest.raises(ValueError):
+        call(pair_axis=b"\0" * 31)
+    with pytest.raises(ValueError):
+        call(pair_axis=[0] * 32)
+    with pytest.raises(TypeError):
+        call(q=q.bfloat16())
+    with pytest.raises(TypeError):
+        call(kc=pool.float())
