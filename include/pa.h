@@ -304,6 +304,57 @@ pa_status pa_prefill_varlen(void *out, const void *q, const void *k, const void 
                             pa_dtype dtype, int32_t *err, cudaStream_t stream);
 
 /*
+ * pa_chunk_attn: causal attention of a chunk of new tokens of each sequence over its paged cache,
+ * optionally within a sliding window: drafts to verify (a few tokens a sequence), pieces of long
+ * prompts, and batches that mix them with single decode tokens.
+ *
+ * Source: "nano-vLLM Part 4" section 3 and smzdm deep dive "模型实现细节" (attention over cached
+ * history through a block table, the new tokens stored first).
+ *
+ *   for sequence s: q_len = cu_seqlens_q[s+1] - cu_seqlens_q[s], n = context_lens[s] >= q_len
+ *   new token r (0 <= r < q_len) sits at position p = n - q_len + r and sees keys
+ *   max(0, p - window + 1) .. p (window == 0: keys 0 .. p):
+ *       out[cu_seqlens_q[s] + r, h, :] = sum_j softmax_j(scale * q . K_j) V_j
+ *
+ * The new tokens' rows must already be in the pool (pa_rope_store_kv or pa_store_kv first) and are
+ * counted in n. It differs from pool-path pa_prefill_varlen in that the keys of a sequence are split over
+ * the GPU as the lengths ask, so that few query rows with long contexts use the whole machine, in the
+ * window, and in the lengths, which are pa_decode's.
+ *
+ * out           [total_q, Hq, D], written; rows outside every sequence (padding before
+ *               cu_seqlens_q[0] or from cu_seqlens_q[S] on) are left as they were.
+ * q             [total_q, Hq, D].
+ * block_tables  int32 [S, max_blocks_per_seq]. Entries of blocks that end before the first visible
+ *               key of the chunk are not read (they may hold anything once a window has passed).
+ *               An entry that must be read and lies outside [0, num_blocks) sets PA_DEVERR_TABLE;
+ *               the rows of the tokens that the kernel computes together with one that needs the
+ *               block (up to 256 / (Hq / Hkv) tokens of the sequence) are then zero, for
+ *               the query heads of one kv head or of all.
+ * cu_seqlens_q  int32 [S+1], non-decreasing, from >= 0 to <= total_q.
+ * context_lens  int32 [S]; q_len <= n <= max_blocks_per_seq * block_size, and q_len <=
+ *               max_seqlen_q, else PA_DEVERR_LENGTH and the sequence's rows are zero. A sequence
+ *               with q_len == 0 is skipped; its n is not looked at.
+ * total_q       host int: rows of q and out.
+ * max_seqlen_q  host int >= every q_len.
+ * window        host int >= 0.
+ * scale         positive: from FLT_MIN to FLT_MAX / 2 (masked scores are -infinity times it).
+ * workspace     device scratch of at least pa_chunk_attn_workspace_size(S, Hq, Hkv, D) bytes (up to
+ *               82 MB, by the SM count and D, not the lengths). Its contents on entry do not
+ *               matter; calls that share a workspace must not overlap on the GPU.
+ * Keys and values that no row of the chunk sees may hold anything, NaN included. Those that some
+ * rows see and others do not have to be finite for the result of the others to be.
+ * S == 0, max_seqlen_q == 0 or total_q == 0 is a no-op.
+ */
+size_t pa_chunk_attn_workspace_size(int S, int Hq, int Hkv, int D);
+pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const void *v_cache,
+                        const int32_t *block_tables, int max_blocks_per_seq,
+                        const int32_t *cu_seqlens_q, const int32_t *context_lens, int S,
+                        int total_q, int max_seqlen_q, int window, int Hq, int Hkv, int D,
+                        int block_size, int num_blocks, float scale, pa_dtype dtype,
+                        void *workspace, size_t workspace_bytes, int32_t *err,
+                        cudaStream_t stream);
+
+/*
  * pa_decode_noalloc: pa_decode for callers that cannot allocate device memory.
  *
  * The pages have no counterpart to this call; it exists for users of the library that cannot

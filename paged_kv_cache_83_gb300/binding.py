@@ -19,7 +19,7 @@ PA_F16, PA_BF16 = 0, 1
 PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION = 1, 2, 4, 8, 16
 EXPORTS = ("pa_store_kv", "pa_rope_store_kv", "pa_decode_workspace_size", "pa_decode", "pa_store_decode",
            "pa_store_decode_host", "pa_store_decode_host_workspace_size", "pa_store_decode_host_layout",
-           "pa_prefill_varlen", "pa_decode_noalloc", "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
+           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_decode_noalloc", "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
            "pa_bm_destroy", "pa_bm_allocate", "pa_bm_can_allocate", "pa_bm_append",
            "pa_bm_release", "pa_bm_block_table", "pa_bm_num_tokens", "pa_bm_num_free",
            "pa_bm_refcount")
@@ -65,6 +65,10 @@ def load(path: Path | str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_prefill_varlen.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P, I, I, I, I, I, I,
                                       F, I, I, P, P]
     lib.pa_prefill_varlen.restype = I
+    lib.pa_chunk_attn_workspace_size.argtypes = [I, I, I, I]
+    lib.pa_chunk_attn_workspace_size.restype = Z
+    lib.pa_chunk_attn.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, F, I, P, Z, P, P]
+    lib.pa_chunk_attn.restype = I
     lib.pa_decode_noalloc.argtypes = [P, P, P, P, P, I, P, I, I, I, I, I, I, F, I, P, P]
     lib.pa_decode_noalloc.restype = I
     lib.pa_decode_debug_tail_units.argtypes = [P, I, I, I, I, I, I]
@@ -375,6 +379,38 @@ def pa_prefill_varlen(out, q, k, v, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k
         _i32(cu_seqlens_q, "cu_seqlens_q"), _i32(cu_seqlens_k, "cu_seqlens_k"), S, Tq, total_k,
         int(max_seqlen_q), int(max_seqlen_k), _i32(block_tables, "block_tables"), maxb, Hq, Hkv, D,
         bs, NB, float(scale), int(bool(causal)), dt, _i32(err, "err"), _stream(stream, q)))
+
+
+def pa_chunk_attn_workspace_size(S: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of scratch pa_chunk_attn needs on the current device for these sizes."""
+    return int(load().pa_chunk_attn_workspace_size(int(S), int(Hq), int(Hkv), int(D)))
+
+
+def pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_seqlen_q: int,
+                  scale: float, window: int = 0, workspace=None, err=None, stream=None) -> None:
+    """Causal attention of a chunk of new tokens of each sequence over its paged cache: out, q
+    [Tq, Hq, D]; sequence s has rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] at the last positions of its
+    context_lens[s] keys. window > 0: a token sees its last `window` keys only."""
+    NB, bs, Hkv, D = k_cache.shape
+    Tq, Hq, Dq = q.shape
+    S = context_lens.shape[0]
+    if Dq != D or out.shape != q.shape or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != S or context_lens.dim() != 1 or cu_seqlens_q.shape != (S + 1,):
+        raise ValueError("shape mismatch")
+    if _elsewhere(q, out, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, workspace, err):
+        with torch.cuda.device(q.device):
+            return pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_seqlen_q,
+                                 scale, window, workspace, err, stream)
+    dtype = q.dtype
+    dt = _dtype(q)
+    if out.dtype != dtype or k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("q, out and the pools must share a dtype")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("pa_chunk_attn", load().pa_chunk_attn(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _i32(block_tables, "block_tables"), block_tables.shape[1],
+        _i32(cu_seqlens_q, "cu_seqlens_q"), _i32(context_lens, "context_lens"), S, Tq, int(max_seqlen_q),
+        int(window), Hq, Hkv, D, bs, NB, float(scale), dt, _ptr(workspace), ws_bytes, _i32(err, "err"),
+        _stream(stream, q)))
 
 
 # ---------------------------------------------------------------------------------------------

@@ -1,4 +1,5 @@
 // pa_api.cu: the C ABI declared in include/pa.h: argument checks, then the kernel launchers.
+#include <float.h>
 #include <limits.h>
 
 #include "pa_internal.h"
@@ -385,6 +386,60 @@ pa_status pa_prefill_varlen(void *out, const void *q, const void *k, const void 
     a.dtype = dtype;
     a.err = err;
     return from_cuda(pa::launch_prefill(a, stream));
+}
+
+size_t pa_chunk_attn_workspace_size(int S, int Hq, int Hkv, int D) {
+    if (S <= 0 || check_heads(Hq, Hkv, D) != PA_OK) return 0;
+    return pa::chunk_attn_workspace(D);
+}
+
+pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const void *v_cache,
+                        const int32_t *block_tables, int max_blocks_per_seq,
+                        const int32_t *cu_seqlens_q, const int32_t *context_lens, int S,
+                        int total_q, int max_seqlen_q, int window, int Hq, int Hkv, int D,
+                        int block_size, int num_blocks, float scale, pa_dtype dtype,
+                        void *workspace, size_t workspace_bytes, int32_t *err,
+                        cudaStream_t stream) {
+    if (!dtype_ok(dtype)) return PA_ERR_DTYPE;
+    if (S < 0 || total_q < 0 || max_seqlen_q < 0 || window < 0 || block_size < 1 || num_blocks < 0 ||
+        max_blocks_per_seq < 0 || !(scale >= FLT_MIN && scale <= FLT_MAX / 2))
+        return PA_ERR_SHAPE;
+    const pa_status st = check_heads(Hq, Hkv, D);
+    if (st != PA_OK) return st;
+    if (static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX) return PA_ERR_SHAPE;
+    // positions and tile bounds stay below 2^31 - 256 in 32 bits
+    if (S > 65535 || static_cast<long long>(num_blocks) * block_size > INT_MAX ||
+        static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX - 1024 || total_q > INT_MAX - 1024)
+        return PA_ERR_UNSUPPORTED;
+    if (S == 0 || max_seqlen_q == 0 || total_q == 0) return PA_OK;
+    if (max_blocks_per_seq < 1 || num_blocks < 1) return PA_ERR_SHAPE;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !context_lens) return PA_ERR_NULL;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < pa::chunk_attn_workspace(D) || !aligned16(workspace))
+        return PA_ERR_WORKSPACE;
+    pa::ChunkArgs a{};
+    a.out = out;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.cu_q = cu_seqlens_q;
+    a.ctx = context_lens;
+    a.block_tables = block_tables;
+    a.S = S;
+    a.total_q = total_q;
+    a.max_seqlen_q = max_seqlen_q;
+    a.max_blocks = max_blocks_per_seq;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.window = window;
+    a.scale = scale;
+    a.dtype = dtype;
+    a.workspace = workspace;
+    a.err = err;
+    return from_cuda(pa::launch_chunk_attn(a, stream));
 }
 
 }  // extern "C"

@@ -107,6 +107,21 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 bool tc_prefill_supported(const PrefillArgs &a);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);
 
+// ------------------------------------------------------------------------------------------
+// Attention of a chunk of new tokens over the paged cache (chunk_attn.cu).
+struct ChunkArgs {
+    void *out;
+    const void *q, *k_cache, *v_cache;
+    const int32_t *cu_q, *ctx, *block_tables;
+    int S, total_q, max_seqlen_q, max_blocks, Hq, Hkv, D, block_size, num_blocks, window;
+    float scale;
+    pa_dtype dtype;
+    void *workspace;
+    int32_t *err;
+};
+size_t chunk_attn_workspace(int D);
+cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream);
+
 inline int log2_if_pow2(int x) {
     if (x <= 0 || (x & (x - 1))) return -1;
     int s = 0;

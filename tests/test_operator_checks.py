@@ -102,3 +102,52 @@ def test_rope_store_binding_refusals():
         call(q=q.bfloat16())
     with pytest.raises(TypeError):
         call(kc=pool.float())
+
+
+def _chunk(lib, **kw):
+    a = dict(out=FAKE, q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, maxb=4, cu=FAKE, ctx=FAKE, S=2, tq=8, mq=4, window=0, Hq=4,
+             Hkv=2, D=64, bs=16, nb=8, scale=0.125, dt=0, ws=None, wsb=0, err=None, stream=None)
+    a.update(kw)
+    return lib.pa_chunk_attn(*a.values())
+
+
+def test_chunk_attn_refusals(lib):
+    assert _chunk(lib, dt=2) == DTYPE
+    for bad in (dict(S=-1), dict(tq=-1), dict(mq=-1), dict(window=-1), dict(bs=0), dict(nb=-1), dict(maxb=-1), dict(Hq=5),
+                dict(Hkv=0), dict(scale=-0.1), dict(scale=0.0), dict(scale=1e-40), dict(scale=3e38), dict(scale=float("nan")), dict(scale=float("inf")), dict(maxb=0), dict(nb=0),
+                dict(maxb=1 << 30, bs=4)):
+        assert _chunk(lib, **bad) == SHAPE, bad
+    for bad in (dict(Hq=18), dict(D=96), dict(S=65536), dict(nb=1 << 30), dict(maxb=(1 << 27) - 1)):
+        assert _chunk(lib, **bad) == UNSUPPORTED, bad
+    for empty in (dict(S=0), dict(tq=0), dict(mq=0)):
+        assert _chunk(lib, **empty) == 0
+    for name in ("out", "q", "kc", "vc", "bt", "cu", "ctx"):
+        assert _chunk(lib, **{name: None}) == NULL, name
+    for name in ("out", "q", "kc", "vc"):
+        assert _chunk(lib, **{name: FAKE + 8}) == UNSUPPORTED, name
+    need = lib.pa_chunk_attn_workspace_size(2, 4, 2, 64)
+    assert need > 0
+    assert _chunk(lib) == WORKSPACE
+    assert _chunk(lib, ws=FAKE, wsb=need - 1) == WORKSPACE
+    assert _chunk(lib, ws=FAKE + 8, wsb=need) == WORKSPACE
+    assert lib.pa_chunk_attn_workspace_size(0, 4, 2, 64) == 0
+    assert lib.pa_chunk_attn_workspace_size(2, 5, 2, 64) == 0
+    assert lib.pa_chunk_attn_workspace_size(2, 4, 2, 96) == 0
+
+
+def test_chunk_attn_binding_refusals():
+    q = torch.zeros(6, 4, 64, dtype=torch.float16)
+    pool = torch.zeros(2, 16, 2, 64, dtype=torch.float16)
+    bt, cu, ctx = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+
+    def call(out=q, q=q, kc=pool, vc=pool, bt=bt, cu=cu, ctx=ctx):
+        pa.pa_chunk_attn(out, q, kc, vc, bt, cu, ctx, 3, 0.125)
+
+    with pytest.raises(ValueError):                  # not on a CUDA device
+        call()
+    for bad in (dict(out=q[:5]), dict(vc=pool[:1]), dict(bt=bt[:1]), dict(cu=cu[:2]), dict(ctx=ctx[None])):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for bad in (dict(out=q.float()), dict(kc=pool.bfloat16())):
+        with pytest.raises(TypeError):
+            call(**bad)
