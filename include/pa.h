@@ -48,13 +48,13 @@ typedef enum {
     PA_OK = 0,
     PA_ERR_NULL = 1,        /* a required pointer is NULL */
     PA_ERR_SHAPE = 2,       /* a size is negative, zero where it must not be, or inconsistent */
-    PA_ERR_DTYPE = 3,       /* dtype is not PA_F16 or PA_BF16 */
+    PA_ERR_DTYPE = 3,       /* a dtype the call does not take */
     PA_ERR_UNSUPPORTED = 4, /* a shape outside the supported set (D, group size, alignment) */
     PA_ERR_WORKSPACE = 5,   /* workspace missing or smaller than pa_decode_workspace_size() */
     PA_ERR_CUDA = 6         /* a CUDA runtime call failed (e.g. the launch) */
 } pa_status;
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
+typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 /* pa_sample's logits only */ } pa_dtype;
 
 /* Bits OR-ed into *err by the kernels. */
 #define PA_DEVERR_SLOT 1   /* slot_mapping entry >= num_blocks * block_size: token not stored */
@@ -65,6 +65,7 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
                               q_len > max_seqlen_q): the sequence's output rows are zero */
 #define PA_DEVERR_POSITION 16 /* a token's position lies outside the cosine/sine table: the token
                               is skipped */
+#define PA_DEVERR_ROW 32 /* a row of logits holds nothing above -infinity: its token is -1 */
 #define PA_DEVERR_TIMEOUT 8 /* an internal wait (on an asynchronous copy or on another warp)
                                gave up after about half a second: the kernel stopped early and
                                its outputs are incomplete */
@@ -353,6 +354,39 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
                         int block_size, int num_blocks, float scale, pa_dtype dtype,
                         void *workspace, size_t workspace_bytes, int32_t *err,
                         cudaStream_t stream);
+
+/*
+ * pa_sample: one token per row of logits, from a given random number per row.
+ *
+ * Source: smzdm nano-vLLM deep dive (the sampler with each request's temperature); "nano-vLLM Part 4"
+ * section 3 (step 3: the next tokens are sampled from the logits).
+ *
+ *   for row b, logits x, T = temperature[b]:
+ *       T <= 0 or NaN: tokens[b] = the lowest index of the largest logit; u and the rest are not looked at
+ *       else w_j = exp((x_j - max x) / T);  order the tokens by descending logit, lowest index first
+ *       1. top-k: the first top_k[b] of the order stay (top_k <= 0 or >= V: all)
+ *       2. top-p: of these, each before which less than top_p[b] of their sum lies stays, the first
+ *          one in any case (top_p >= 1 or NaN: all)
+ *       3. min-p: of these, those with w_j >= min(min_p[b], 1) stay (min_p <= 0 or NaN: all)
+ *       tokens[b] = the first index, in the order of the vocabulary, at which the running sum of the
+ *       kept weights exceeds u[b] times their whole sum
+ *
+ * tokens        int32 [B], written.
+ * logits        [B, V] fp16, bf16 or fp32 (`dtype`), rows row_stride elements apart, row_stride >= V; any
+ *               alignment that the element type has. NaN counts as -infinity, which is never chosen;
+ *               +infinity leaves the other tokens without weight. A row without any logit above
+ *               -infinity gives token -1 and PA_DEVERR_ROW.
+ * u             fp32 [B], uniform in [0, 1); NaN and values below 0 count as 0, values from 1 on
+ *               choose the last kept token with weight. May be NULL where every row is greedy (0).
+ * temperature, top_k, top_p, min_p  [B] each (top_k int32, the others fp32); NULL: 1, none, none, none.
+ * Weights are exact to about 2^-31 of themselves and held as multiples of 2^-44 of the largest
+ * (smaller ones count as zero); their sums are integers, so the tokens do not depend on how the
+ * work is divided. Supported: 1 <= V <= 262144. B == 0 is a no-op. Reads the logits once.
+ */
+pa_status pa_sample(int32_t *tokens, const void *logits, int64_t row_stride, int B, int V,
+                    pa_dtype dtype, const float *u, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, int32_t *err,
+                    cudaStream_t stream);
 
 /*
  * pa_decode_noalloc: pa_decode for callers that cannot allocate device memory.

@@ -15,11 +15,11 @@ import torch
 PKG = Path(__file__).resolve().parent
 LIB_PATH = PKG / "_build" / "libpagedattn.so"
 
-PA_F16, PA_BF16 = 0, 1
-PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION = 1, 2, 4, 8, 16
+PA_F16, PA_BF16, PA_F32 = 0, 1, 2
+PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION, PA_DEVERR_ROW = 1, 2, 4, 8, 16, 32
 EXPORTS = ("pa_store_kv", "pa_rope_store_kv", "pa_decode_workspace_size", "pa_decode", "pa_store_decode",
            "pa_store_decode_host", "pa_store_decode_host_workspace_size", "pa_store_decode_host_layout",
-           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_decode_noalloc", "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
+           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample", "pa_decode_noalloc", "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
            "pa_bm_destroy", "pa_bm_allocate", "pa_bm_can_allocate", "pa_bm_append",
            "pa_bm_release", "pa_bm_block_table", "pa_bm_num_tokens", "pa_bm_num_free",
            "pa_bm_refcount")
@@ -69,6 +69,8 @@ def load(path: Path | str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_chunk_attn_workspace_size.restype = Z
     lib.pa_chunk_attn.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, F, I, P, Z, P, P]
     lib.pa_chunk_attn.restype = I
+    lib.pa_sample.argtypes = [P, P, L, I, I, I, P, P, P, P, P, P, P]
+    lib.pa_sample.restype = I
     lib.pa_decode_noalloc.argtypes = [P, P, P, P, P, I, P, I, I, I, I, I, I, F, I, P, P]
     lib.pa_decode_noalloc.restype = I
     lib.pa_decode_debug_tail_units.argtypes = [P, I, I, I, I, I, I]
@@ -411,6 +413,44 @@ def pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_
         _i32(cu_seqlens_q, "cu_seqlens_q"), _i32(context_lens, "context_lens"), S, Tq, int(max_seqlen_q),
         int(window), Hq, Hkv, D, bs, NB, float(scale), dt, _ptr(workspace), ws_bytes, _i32(err, "err"),
         _stream(stream, q)))
+
+
+def _per_row(t: torch.Tensor | None, B: int, dtype, name: str):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != (B,):
+        raise TypeError(f"{name} must be {dtype} [B]")
+    return _ptr(t)
+
+
+_LOGITS = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
+
+
+def pa_sample(tokens, logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None, err=None,
+              stream=None) -> None:
+    """One token per row of logits [B, V] (rows may lie apart) into tokens [B] int32, from the given
+    uniform numbers u [B]; temperature, top_k (int32), top_p, min_p: one per row, or None for 1 and
+    no truncation. A row with temperature 0 takes its largest logit; u may be None when all do."""
+    B, V = logits.shape
+    if tokens.shape != (B,):
+        raise ValueError("tokens must be [B]")
+    if _elsewhere(logits, tokens, u, temperature, top_k, top_p, min_p, err):
+        with torch.cuda.device(logits.device):
+            return pa_sample(tokens, logits, u, temperature, top_k, top_p, min_p, err, stream)
+    dt = _LOGITS.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {logits.dtype}")
+    if not logits.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    s0, s1 = logits.stride()
+    if s1 != 1 and V > 1:
+        raise ValueError("a row of logits must be contiguous")
+    f32 = torch.float32
+    _check("pa_sample", load().pa_sample(
+        _i32(tokens, "tokens"), logits.data_ptr(), s0 if B > 1 else V, B, V, dt, _per_row(u, B, f32, "u"),
+        _per_row(temperature, B, f32, "temperature"), _per_row(top_k, B, torch.int32, "top_k"),
+        _per_row(top_p, B, f32, "top_p"), _per_row(min_p, B, f32, "min_p"), _i32(err, "err"),
+        _stream(stream, logits)))
 
 
 # ---------------------------------------------------------------------------------------------

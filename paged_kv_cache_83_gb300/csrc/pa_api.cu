@@ -442,4 +442,19 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
     return from_cuda(pa::launch_chunk_attn(a, stream));
 }
 
+pa_status pa_sample(int32_t *tokens, const void *logits, int64_t row_stride, int B, int V,
+                    pa_dtype dtype, const float *u, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, int32_t *err,
+                    cudaStream_t stream) {
+    if (!dtype_ok(dtype) && dtype != PA_F32) return PA_ERR_DTYPE;
+    if (B < 0 || V < 1 || row_stride < V) return PA_ERR_SHAPE;
+    if (V > pa::kSampleMaxVocab || B > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    if (B == 0) return PA_OK;
+    if (row_stride > (int64_t{1} << 40) / B) return PA_ERR_UNSUPPORTED;
+    if (!tokens || !logits) return PA_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == PA_F32 ? 4 : 2)) return PA_ERR_UNSUPPORTED;
+    pa::SampleArgs a{tokens, logits, row_stride, B, V, dtype, u, temperature, top_k, top_p, min_p, err};
+    return from_cuda(pa::launch_sample(a, stream));
+}
+
 }  // extern "C"

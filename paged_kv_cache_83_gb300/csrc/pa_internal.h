@@ -122,6 +122,22 @@ struct ChunkArgs {
 size_t chunk_attn_workspace(int D);
 cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream);
 
+// ------------------------------------------------------------------------------------------
+// Sampling (sample.cu).
+struct SampleArgs {
+    int32_t *tokens;
+    const void *logits;
+    long long row_stride;  // elements
+    int B, V;
+    pa_dtype dtype;  // PA_F16, PA_BF16 or PA_F32
+    const float *u, *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int32_t *err;
+};
+constexpr int kSampleMaxVocab = 1 << 18;
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
+
 inline int log2_if_pow2(int x) {
     if (x <= 0 || (x & (x - 1))) return -1;
     int s = 0;

@@ -151,3 +151,32 @@ def test_chunk_attn_binding_refusals():
     for bad in (dict(out=q.float()), dict(kc=pool.bfloat16())):
         with pytest.raises(TypeError):
             call(**bad)
+
+
+def _sample(lib, **kw):
+    a = dict(tokens=FAKE, logits=FAKE, stride=1000, B=2, V=1000, dt=2, u=FAKE, t=FAKE, k=FAKE, p=FAKE, m=FAKE, err=None,
+             stream=None)
+    a.update(kw)
+    return lib.pa_sample(*a.values())
+
+
+def test_sample_refusals(lib):
+    assert _sample(lib, dt=3) == DTYPE
+    for bad in (dict(B=-1), dict(V=0), dict(stride=999)):
+        assert _sample(lib, **bad) == SHAPE, bad
+    for bad in (dict(V=262145, stride=262145), dict(B=(1 << 24) + 1), dict(stride=1 << 40), dict(logits=FAKE + 2),
+                dict(dt=0, logits=FAKE + 1)):
+        assert _sample(lib, **bad) == UNSUPPORTED, bad
+    assert _sample(lib, B=0) == 0
+    assert _sample(lib, tokens=None) == NULL
+    assert _sample(lib, logits=None) == NULL
+
+
+def test_sample_binding_refusals():
+    x, t = torch.zeros(3, 50), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):                  # not on a CUDA device
+        pa.pa_sample(t, x)
+    with pytest.raises(ValueError):
+        pa.pa_sample(t[:2], x)
+    with pytest.raises(TypeError):
+        pa.pa_sample(t, x.double())
