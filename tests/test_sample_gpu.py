@@ -145,7 +145,7 @@ def test_masked_and_odd_logits():
     x[4, :-7] = low
     x[5, 17] = nan
     x[6, 4000] = inf                                     # all of the weight
-    x[7, [5, 4999]] = inf
+    x[7, [5, 17, 900, 901, 4999]] = inf
     x[8, :] = -inf
     x[8, 4321] = -3e38
     x[9, ::2] = -inf
