@@ -29,24 +29,18 @@
 //               is released for the next key tile's QK; O is rescaled only when the row's maximum
 //               grew by more than 2^8. Warps without rows only keep the barriers going.
 // Every wait is bounded (PA_DEVERR_TIMEOUT); on a timeout every role drains what it started.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <math.h>
-
 #include <type_traits>
 
-#include "pa_internal.h"
+#include "chunk_common.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int BM = 128, BN = 128;
-constexpr int kThreads = 384;
-constexpr int kHalf = BM * 64 * 2;   // one 128-row x 64-column half tile: 16 KB
+using namespace chunk;
+
 constexpr int kPTile = BM * BN * 2;  // P, and the output stage
 constexpr int kRing = 3;
-constexpr unsigned kFull = 0xffffffffu;
 enum {
     B_QFULL = 0,               // the segment's Q tiles landed
     B_QEMPTY,                  // both issuers are past the segment's last QK
@@ -64,20 +58,6 @@ enum {
     B_IEMPTY = B_IFULL + 2,    // + k: every role has read it
     NBAR = B_IEMPTY + 2
 };
-constexpr int kItemReaders = 11;
-constexpr int kBadRing = 8;  // segments whose table entries were bad, by segment number
-
-// A segment: key tiles [j0, j1) of an item. tok0: its first token's row of q; tok: its tokens;
-// p0: position of its first token; [n_lo, n_end): the keys that any of its rows sees.
-// part: -1 the whole item, else the CTA's workspace slot. j1 == j0 marks the end of the work.
-struct SegInfo {
-    int s, g, tok0, tok, p0, n_lo, n_end, j0, j1, part;
-};
-// What the joining kernel needs about the item whose first piece a CTA holds (in slot 1).
-struct PieceRec {
-    int valid, tok0, tok, g, last_cta, pad[3];
-};
-
 template <int HD>
 struct Layout {
     static constexpr int kHalves = HD / 64;
@@ -88,92 +68,19 @@ struct Layout {
                          OFF_RING = OFF_PB + kPTile, OFF_BAR = OFF_RING + kRing * kKV;
     static constexpr int OFF_ITEMS = OFF_BAR + NBAR * 8;
     static constexpr int OFF_BAD = OFF_ITEMS + 2 * static_cast<int>(sizeof(SegInfo));
-    static constexpr int OFF_PLAN = (OFF_BAD + kBadRing * 4 + 15) / 16 * 16;  // 12 warp sums, then the start
-    static constexpr int OFF_MISC = OFF_PLAN + 16 * 8;
+    static constexpr int OFF_PLAN = (OFF_BAD + kBadRing * 4 + 15) / 16 * 16;  // 12 warp sums, then the share
+    static constexpr int OFF_MISC = OFF_PLAN + 12 * 8 + static_cast<int>(sizeof(Share));
     static constexpr int kSmem = OFF_MISC + 16 + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
     // one piece in the workspace: m[256], l[256], O[HD][256], fp32 (rows fastest: lanes = rows)
     static constexpr size_t kPieceFloats = 256 * (HD + 2);
 };
 
-struct ChunkParams {
-    CUtensorMap tm_q, tm_k, tm_v;  // q: [total_q, Hq, D], boxes of `tt` tokens x G heads x 64
-    const int32_t *cu_q, *ctx, *block_tables;
-    const void *k_cache, *v_cache;
-    void *out;
-    int32_t *err;
-    float *pieces;
-    PieceRec *recs;
-    int S, Hq, Hkv, G, tt, max_blocks, num_blocks, total_q, max_seqlen_q, window, box_rows;
-    BlockGeom geom;
-    float scale_log2;
-};
-
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    const bool ok = mbar_wait(bar, parity) && !*abort_flag;
-    const bool all = __all_sync(kFull, ok);
-    __syncwarp();
-    return all;
-}
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b),
                  "r"(c), "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ void give_up(int32_t *err, volatile int *abort_flag) {
-    raise_err(err, PA_DEVERR_TIMEOUT);
-    *abort_flag = 1;
-}
-
-// ------------------------------------------------------------------------------------------
-// the shares
-// ------------------------------------------------------------------------------------------
-
-struct SeqShape {
-    int q0, ql, kl;
-    bool bad;  // lengths outside the contract: the rows are zero, no work
-};
-__device__ __forceinline__ SeqShape seq_shape(const ChunkParams &p, int s) {
-    SeqShape r;
-    r.q0 = __ldg(p.cu_q + s);
-    const int q1 = __ldg(p.cu_q + s + 1);
-    r.kl = __ldg(p.ctx + s);
-    r.bad = r.q0 < 0 || q1 < r.q0 || q1 > p.total_q;
-    r.ql = r.bad ? 0 : q1 - r.q0;
-    if (r.ql > 0 && (r.ql > p.max_seqlen_q || r.kl < r.ql ||
-                     static_cast<long long>(r.kl) > static_cast<long long>(p.max_blocks) * p.geom.block_size))
-        r.bad = true;
-    return r;
-}
-// first key and key tiles of item i (2 * tt tokens) of a sequence
-__device__ __forceinline__ int item_tiles(const ChunkParams &p, const SeqShape &q, int i) {
-    const int t0 = i * 2 * p.tt, t1 = min(t0 + 2 * p.tt, q.ql), p0 = q.kl - q.ql;
-    const int lo = p.window > 0 ? max(0, p0 + t0 - p.window + 1) : 0;
-    return (p0 + t1 + BN - 1) / BN - lo / BN;
-}
-// key tiles of all the sequence's items of one kv head
-__device__ __forceinline__ long long head_tiles(const ChunkParams &p, const SeqShape &q) {
-    if (q.bad || q.ql <= 0) return 0;
-    long long n = 0;
-    for (int i = 0; i * 2 * p.tt < q.ql; ++i) n += item_tiles(p, q, i);
-    return n;
-}
-__device__ __forceinline__ long long warp_sum(long long v) {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
-
-// joins warps' sums through shared memory: every thread gets the sum over the block
-__device__ __forceinline__ long long block_sum(long long v, long long *sm) {
-    v = warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-    __syncthreads();
-    long long t = 0;
-    for (int i = 0; i < kThreads / 32; ++i) t += sm[i];
-    return t;
-}
-
 template <class E, int HD, bool kGather>
 __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkParams p) {
     using T = typename E::T;
@@ -188,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     SegInfo *items = reinterpret_cast<SegInfo *>(smem + Lay::OFF_ITEMS);
     volatile int *bad_seg = reinterpret_cast<volatile int *>(smem + Lay::OFF_BAD);
     long long *plan = reinterpret_cast<long long *>(smem + Lay::OFF_PLAN);
+    Share *share = reinterpret_cast<Share *>(plan + 12);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_MISC + 4);
     auto bar = [&](int i) { return sbase + OFF_BAR + 8u * i; };
@@ -209,49 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     }
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
 
-    // this CTA's share [b0, b1) of the line of (item, key tile) pairs, and the sequence it starts in
-    long long mine = 0;
-    for (int s = tid; s < p.S; s += kThreads) mine += head_tiles(p, seq_shape(p, s)) * p.Hkv;
-    const long long N = block_sum(mine, plan);
-    // CTAs 0 .. P - 1 take a share, at least one tile each (no piece of an item is then empty)
-    const long long P = min(static_cast<long long>(gridDim.x), N), me = blockIdx.x;
-    const long long b0 = me < P ? me * N / P : N, b1 = me < P ? (me + 1) * N / P : N;
-    if (b0 < b1) {
-        long long base = 0;
-        for (int sb = 0; sb < p.S; sb += kThreads) {
-            const int s = sb + tid;
-            const long long v = s < p.S ? head_tiles(p, seq_shape(p, s)) * p.Hkv : 0;
-            long long incl = v;
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(kFull, incl, o);
-                if (lane >= o) incl += u;
-            }
-            __syncthreads();
-            if (lane == 31) plan[warp] = incl;
-            __syncthreads();
-            long long before = base;
-            for (int w = 0; w < kThreads / 32; ++w) {
-                if (w < warp) before += plan[w];
-                base += plan[w];
-            }
-            const long long after = before + incl;
-            if (after - v <= b0 && b0 < after) {  // one thread of the block, once
-                plan[12] = s;
-                plan[13] = after - v;
-            }
-            if (b0 < base) break;  // the same for every thread
-        }
-    }
-    // sequences whose lengths are outside the contract: an error bit and zero rows
-    for (int s = blockIdx.x; s < p.S; s += gridDim.x) {
-        const SeqShape q = seq_shape(p, s);
-        if (!q.bad) continue;
-        if (tid == 0) raise_err(p.err, PA_DEVERR_LENGTH);
-        const int a = max(q.q0, 0), b = min(__ldg(p.cu_q + s + 1), p.total_q);
-        for (long long i = static_cast<long long>(a) * p.Hq * HD + tid; i < static_cast<long long>(b) * p.Hq * HD;
-             i += kThreads)
-            out[i] = T(0.f);
-    }
+    plan_share(p, plan, share);
+    zero_bad_sequences<T, HD>(p);
     if (tid == 0) p.recs[blockIdx.x].valid = 0;
     tc_fence_before();
     __syncthreads();
@@ -271,7 +138,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     if (warp == 3) {
         // ================================== scheduler ==================================
         int published = 0;
-        bool ok = true;
         auto publish = [&](const SegInfo &it) {
             if (!warp_wait(bar(B_IEMPTY + (published & 1)), ((published >> 1) & 1) ^ 1, abort_flag)) return false;
             if (lane == 0) {
@@ -282,48 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             ++published;
             return true;
         };
-        if (b0 < b1) {
-            int s = static_cast<int>(plan[12]);
-            long long at = b0;                // position on the line
-            long long off = b0 - plan[13];    // position in the sequence
-            while (ok && at < b1) {
-                const SeqShape q = seq_shape(p, s);
-                const long long per_head = head_tiles(p, q);
-                // order within a sequence: kv head, then item: a CTA's next item reads the same keys
-                int g = per_head > 0 ? static_cast<int>(off / per_head) : p.Hkv;
-                long long in_head = per_head > 0 ? off - g * per_head : 0;
-                int i = 0;
-                if (g < p.Hkv)
-                    for (int n; in_head >= (n = item_tiles(p, q, i)); ++i) in_head -= n;
-                for (; ok && g < p.Hkv && at < b1; ++g, i = 0)
-                    for (; ok && i * 2 * p.tt < q.ql && at < b1; ++i) {
-                        const int n = item_tiles(p, q, i), t0 = i * 2 * p.tt;
-                        const int first = static_cast<int>(in_head);
-                        const int last = static_cast<int>(min(static_cast<long long>(n), first + (b1 - at)));
-                        in_head = 0;
-                        SegInfo it;
-                        it.s = s, it.g = g, it.tok0 = q.q0 + t0, it.tok = min(2 * p.tt, q.ql - t0);
-                        it.p0 = q.kl - q.ql + t0;
-                        it.n_end = it.p0 + it.tok;
-                        it.n_lo = p.window > 0 ? max(0, it.p0 - p.window + 1) : 0;
-                        it.j0 = it.n_lo / BN + first, it.j1 = it.n_lo / BN + last;
-                        it.part = first > 0 ? 0 : last < n ? 1 : -1;
-                        if (it.part == 1 && lane == 0) {
-                            // the CTA that holds the item's last tile: share c is [c N / P, (c + 1) N / P)
-                            PieceRec r{};
-                            const long long x = at + n - 1;
-                            r.valid = 1, r.tok0 = it.tok0, r.tok = it.tok, r.g = g;
-                            r.last_cta = static_cast<int>(((x + 1) * P - 1) / N);
-                            p.recs[blockIdx.x] = r;
-                        }
-                        ok = publish(it);
-                        at += last - first;
-                    }
-                ++s;
-                off = 0;
-            }
-        }
-        if (ok) ok = publish(SegInfo{});  // the end marker
+        const bool ok = walk_share(p, *share, publish);
         if (!ok && lane == 0) give_up(p.err, abort_flag);
     } else if (warp == 0) {
         // =================================== producer ===================================
@@ -337,18 +162,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         long long L = 0;  // tiles loaded
         int n = 0;        // segments taken
         bool ok = true;
-        // the pool row of key `pos` of the segment's sequence, -1 where none is to be read
-        auto pool_row = [&](const SegInfo &it, int pos, int last, int seg_no) -> long long {
-            // a box that ends before the first key is not read; pos is its first row
-            if (pos >= it.n_end || last < it.n_lo) return -1;
-            const int id = __ldg(p.block_tables + static_cast<size_t>(it.s) * p.max_blocks + p.geom.block_of(pos));
-            if (id < 0 || id >= p.num_blocks) {
-                bad_seg[seg_no & (kBadRing - 1)] = seg_no + 1;
-                raise_err(p.err, PA_DEVERR_TABLE);
-                return -1;
-            }
-            return static_cast<long long>(id) * p.geom.block_size + p.geom.offset_of(pos);
-        };
         constexpr int kRowsLane = kGather ? BN / 32 : 1;
         struct Rows {
             long long r[kRowsLane];
@@ -359,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < kRowsLane; ++i) {
                 const int pos = j * BN + (kGather ? lane + 32 * i : lane * R);
-                w.r[i] = kGather || lane < nbox ? pool_row(it, pos, kGather ? pos : pos + R - 1, seg_no) : -1;
+                w.r[i] = kGather || lane < nbox ? pool_row(p, it, pos, kGather ? pos : pos + R - 1, bad_seg, seg_no) : -1;
             }
             return w;
         };
@@ -375,17 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             const uint32_t base = sbase + OFF_RING + slot * Lay::kKV;
             if (!warp_wait(bar(B_EMPTY + slot), static_cast<uint32_t>((L / kRing) & 1) ^ 1, abort_flag)) return false;
             if constexpr (kGather) {
-                const T *pool = static_cast<const T *>(is_v ? p.v_cache : p.k_cache);
-#pragma unroll
-                for (int i = 0; i < kRowsLane; ++i) {
-                    const int r = lane + 32 * i;
-                    const T *src = pool + (static_cast<size_t>(w.r[i] < 0 ? 0 : w.r[i]) * p.Hkv + it.g) * HD;
-#pragma unroll
-                    for (int c = 0; c < HD / 8; ++c)
-                        cp_async16(base + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4), src + c * 8,
-                                   w.r[i] < 0 ? 0 : 16);
-                }
-                cp_async_commit();
+                gather_tile<T, HD>(base, static_cast<const T *>(is_v ? p.v_cache : p.k_cache), w.r, p.Hkv, it.g);
                 cp_async_wait<1>();
                 announce(L - 1);
             } else {
@@ -537,22 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             if (!(ok = next_load(slot))) break;
             const int z0 = max(cur.n_lo - j * BN, 0), z1 = min(cur.n_end - j * BN, BN);  // rows that hold keys
             if (rows && (z0 > 0 || z1 < BN)) {
-                // rows outside the keys (unwritten slots, blocks given back, an earlier tile's) are
-                // zeroed before any PV reads them: P is zero there, but 0 * NaN is not
                 const bool both = has_b(cur);
                 if (h == 0) {
                     if (both && zt > 0 &&
                         !(ok = warp_wait(bar(B_VZACK), static_cast<uint32_t>((zt - 1) & 1), abort_flag)))
                         break;
-                    unsigned char *vt = smem + OFF_RING + slot * Lay::kKV;
-                    const int nz = z0 + BN - z1;
-                    for (int c = lane; c < nz * (HD / 8); c += 32) {
-                        const int rr = c / (HD / 8), c16 = c % (HD / 8), r = rr < z0 ? rr : rr - z0 + z1;
-                        *reinterpret_cast<uint4 *>(vt + (c16 >> 3) * kHalf + r * 128 + (c16 & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                    zero_rows<HD>(smem + OFF_RING + slot * Lay::kKV, z0, z1);
                     if (both && lane == 0) mbar_arrive(bar(B_VZ));
                 } else {
                     if (!(ok = warp_wait(bar(B_VZ), zt & 1, abort_flag))) break;
@@ -776,39 +569,56 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
 // joining the pieces
 // ------------------------------------------------------------------------------------------
 
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 32, kJoinCols = 32;  // of a block: threads = rows x 4 chunks of 8 columns
+constexpr int kJoinThreads = kJoinRows * (kJoinCols / 8);
 
-// Block (c, y): rows [32 y, 32 y + 32) of the item whose first piece CTA c holds (its slot 1); the
-// pieces after it are slot 0 of the CTAs up to last_cta. Thread = one row and 8 output columns; the
-// reads run along the rows.
+// Block (c, y, z): rows [32 y, 32 y + 32) and columns [32 z, 32 z + 32) of the item whose first piece CTA c
+// holds (its slot 1); the pieces after it are slot 0 of the CTAs up to last_cta. The reads run along
+// the rows, with four pieces' in flight: what bounds it is their latency.
 template <class E, int HD>
-__global__ void __launch_bounds__(kJoinRows * HD / 8) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
     using Lay = Layout<HD>;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PieceRec rec = p.recs[blockIdx.x];
     if (!rec.valid) return;
     const int rt = p.tt * p.G;  // rows of a full row tile
     // row r of the item: tile r / 128, row r % 128 of it
-    const int r = blockIdx.y * kJoinRows + (threadIdx.x & 31), c8 = threadIdx.x >> 5;
+    const int r = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, col = blockIdx.z * kJoinCols + threadIdx.x / kJoinRows * 8;
     const int h = r >> 7, rr = r & 127;
     if (rr >= rt || h * p.tt + rr / p.G >= rec.tok) return;
-    const float *w0 = p.pieces + (static_cast<size_t>(blockIdx.x) * 2 + 1) * Lay::kPieceFloats + r;
-    auto piece = [&](int c) { return c == static_cast<int>(blockIdx.x) ? w0 : p.pieces + static_cast<size_t>(c) * 2 * Lay::kPieceFloats + r; };
-    float m = -INFINITY;
+    const int first = blockIdx.x;
+    float m = -INFINITY, l = 0.f, o[8] = {};
     bool bad = false;
-    for (int c = blockIdx.x; c <= rec.last_cta; ++c) {
-        const float *w = piece(c);
-        bad |= w[256] == -1.f;
-        m = fmaxf(m, w[0]);
-    }
-    const float mu = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[8] = {};
-    for (int c = blockIdx.x; c <= rec.last_cta; ++c) {
-        const float *w = piece(c);
-        const float f = fast_exp2(w[0] - mu);
-        l += f * w[256];
+    for (int c0 = first; c0 <= rec.last_cta; c0 += 4) {
+        float pm[4], pl[4], po[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += f * w[512 + (c8 * 8 + e) * 256];
+        for (int k = 0; k < 4; ++k) {
+            const int c = c0 + k;
+            pm[k] = -INFINITY, pl[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) po[k][e] = 0.f;
+            if (c <= rec.last_cta) {
+                const float *w = p.pieces + (static_cast<size_t>(c) * 2 + (c == first)) * Lay::kPieceFloats + r;
+                pm[k] = __ldg(w);
+                pl[k] = __ldg(w + 256);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) po[k][e] = __ldg(w + 512 + (col + e) * 256);
+            }
+        }
+        const float mn = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
+        const float mu = mn == -INFINITY ? 0.f : mn, f0 = fast_exp2(m - mu);
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float f = fast_exp2(pm[k] - mu);
+            bad |= pl[k] == -1.f;
+            l += f * pl[k];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += f * po[k][e];
+        }
+        m = mn;
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint4 u;
@@ -819,7 +629,7 @@ __global__ void __launch_bounds__(kJoinRows * HD / 8) chunk_join_kernel(const __
     if (bad) u = make_uint4(0, 0, 0, 0);
     using T = typename E::T;
     const int tk = rec.tok0 + h * p.tt + rr / p.G, head = rec.g * p.G + rr % p.G;
-    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (static_cast<size_t>(tk) * p.Hq + head) * HD + c8 * 8) = u;
+    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (static_cast<size_t>(tk) * p.Hq + head) * HD + col) = u;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -876,8 +686,8 @@ cudaError_t launch_typed(const ChunkParams &prm, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     const int rows = prm.max_seqlen_q > prm.tt ? 256 : (prm.max_seqlen_q * prm.G + kJoinRows - 1) / kJoinRows * kJoinRows;
-    cfg.gridDim = dim3(P, rows / kJoinRows);
-    cfg.blockDim = dim3(kJoinRows * HD / 8);
+    cfg.gridDim = dim3(P, rows / kJoinRows, HD / kJoinCols);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -900,6 +710,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream) {
     const bool gather = R < 8;  // less than a swizzle atom of 8 rows
     prm.G = a.Hq / a.Hkv;
     prm.tt = BM / prm.G;
+    prm.item_tok = 2 * prm.tt;
     const long long krows = static_cast<long long>(a.num_blocks) * a.block_size;
     if (!encode(&prm.tm_q, a.q, a.dtype, a.Hq, a.D, a.total_q, prm.G, prm.tt)) return cudaErrorInvalidValue;
     if (!gather && (!encode(&prm.tm_k, a.k_cache, a.dtype, a.Hkv, a.D, krows, 1, R) ||
