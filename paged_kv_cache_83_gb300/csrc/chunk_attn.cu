@@ -710,7 +710,15 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream) {
     const bool gather = R < 8;  // less than a swizzle atom of 8 rows
     prm.G = a.Hq / a.Hkv;
     prm.tt = BM / prm.G;
-    prm.item_tok = 2 * prm.tt;
+    // Chunks of at most 64 query rows a kv head take the form with keys as the rows: an item is a
+    // whole chunk, its Q box as many tokens as the columns hold.
+    const long long rows = static_cast<long long>(a.max_seqlen_q) * prm.G;
+    const bool narrow = rows <= 64;
+    if (narrow) {
+        prm.tt = prm.item_tok = (gather || rows > 32 ? 64 : rows > 16 ? 32 : 16) / prm.G;
+    } else {
+        prm.item_tok = 2 * prm.tt;
+    }
     const long long krows = static_cast<long long>(a.num_blocks) * a.block_size;
     if (!encode(&prm.tm_q, a.q, a.dtype, a.Hq, a.D, a.total_q, prm.G, prm.tt)) return cudaErrorInvalidValue;
     if (!gather && (!encode(&prm.tm_k, a.k_cache, a.dtype, a.Hkv, a.D, krows, 1, R) ||
@@ -733,6 +741,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream) {
     prm.geom.block_size = a.block_size;
     prm.geom.shift = log2_if_pow2(a.block_size);
     prm.scale_log2 = a.scale * kLog2e;
+    if (narrow) return launch_chunk_narrow(prm, a.dtype, a.D, gather, stream);
     auto go = [&](auto e, auto hd) {
         using E = decltype(e);
         constexpr int HD = decltype(hd)::value;

@@ -266,7 +266,6 @@ __device__ __forceinline__ void zero_rows(unsigned char *tile, int z0, int z1) {
 }  // namespace chunk
 
 // chunk_attn_narrow.cu: items of at most 64 query rows
-size_t chunk_narrow_piece_floats(int D);
 cudaError_t launch_chunk_narrow(const chunk::ChunkParams &prm, pa_dtype dtype, int D, bool gather, cudaStream_t stream);
 
 }  // namespace pa

@@ -138,6 +138,33 @@ def test_window(window, Hq, Hkv, D, bs, dt):
     assert int(c.err.item()) == 0
 
 
+@pytest.mark.parametrize("window", [0, 1, 130, 1000])
+@pytest.mark.parametrize("D,bs,dt", [(64, 16, "f16"), (128, 256, "bf16"), (128, 24, "f16"), (64, 3, "bf16"), (128, 2, "bf16")])
+@pytest.mark.parametrize("Hq,Hkv,q", [(2, 2, 16), (8, 8, 17), (14, 2, 9), (8, 2, 4), (8, 1, 8), (3, 1, 1), (5, 1, 12)])
+def test_few_rows(Hq, Hkv, q, D, bs, dt, window):
+    """Chunks of up to 16, 32 and 64 query rows a kv head (and the least that are more), single key
+    tiles, odd and even numbers of them, whole and shared ones."""
+    c = Case([(q, 4000), (1, 1), (min(q, 3), 128), (q, 129), (0, 7), (q, 256), (1, 257), (q, 700), (max(1, q - 1), 384)],
+             Hq, Hkv, D, bs, dt, window=window, seed=q + bs, pad=2)
+    c.check()
+    assert int(c.err.item()) == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,q", [(2, 2, 5), (14, 2, 4), (8, 1, 8)])
+def test_few_rows_growing_scores(Hq, Hkv, q):
+    """Keys that grow along the sequence, so that every tile moves the running maximum, and a column
+    of equal scores; large scores in both directions."""
+    for f in (lambda j: 0.02 * j, lambda j: 40 - 0.02 * j, lambda j: 0 * j):
+        c = Case([(q, 2000), (q, 300)], Hq, Hkv, 128, 16, "bf16", seed=3)
+        for s, (_, n) in enumerate(c.lens):
+            j = torch.arange(n, device="cuda")
+            slot = c.bt[s].long()[j // 16] * 16 + j % 16
+            c.kc.view(-1, Hkv, 128)[slot] = f(j.float())[:, None, None].expand(n, Hkv, 128).bfloat16()
+        c.q[:, 0].fill_(1.0)
+        c.q[:, -1].fill_(-1.0)
+        c.check()
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, single tokens and drafts, empty ones among them."""
     r = np.random.default_rng(5)
