@@ -80,13 +80,23 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t *r) {
               "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
             : "r"(taddr));
 }
-// order-preserving map to integers, NaN below everything
-__device__ __forceinline__ uint32_t rank_of(float x) {
-    const uint32_t b = __float_as_uint(x);
-    return x == x ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u) : 0u;
-}
-__device__ __forceinline__ float ranked(uint32_t k) {
-    return k == 0 ? -INFINITY : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+// Reduces W columns over the warp's lanes: lane c (of 32; c % W) gets column c's result. Halves of the columns
+// change places with the lane W / 2, W / 4, ... away.
+template <int W, class F>
+__device__ __forceinline__ float fold(float (&v)[W], F op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = W / 2; w > 0; w >>= 1) {
+        const bool upper = lane & w;
+#pragma unroll
+        for (int c = 0; c < w; ++c) {
+            const float give = upper ? v[c] : v[c + w], keep = upper ? v[c + w] : v[c];
+            v[c] = op(keep, __shfl_xor_sync(kFull, give, w));
+        }
+    }
+#pragma unroll
+    for (int w = W; w < 32; w <<= 1) v[0] = op(v[0], __shfl_xor_sync(kFull, v[0], w));
+    return v[0];
 }
 constexpr float kUnset = -3e38f;  // the maximum of a column that has seen no key: finite, below every score
 
@@ -109,20 +119,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for this grid itself
+    static_assert(Lay::NBAR <= kThreads);
+    if (tid < Lay::NBAR) {
+        uint32_t count = 1;
+        if (tid >= Lay::B_QEMPTY && tid < Lay::B_KFULL) count = 2;       // both issuers
+        if (tid >= Lay::B_F && tid < Lay::B_O) count = 4;                // F, P, WG: four warps
+        if (tid == Lay::B_OFREE || tid == Lay::B_BOTH) count = 8;
+        if (tid >= Lay::B_IEMPTY) count = kItemReaders;
+        mbar_init(bar(tid), count);
+        fence_mbar_init();
+    }
     if (tid == 0) {
-        for (int i = 0; i < Lay::NBAR; ++i) {
-            uint32_t count = 1;
-            if (i >= Lay::B_QEMPTY && i < Lay::B_KFULL) count = 2;                                 // both issuers
-            if ((i >= Lay::B_F && i < Lay::B_O)) count = 4;                                        // F, P, WG: four warps
-            if (i == Lay::B_OFREE || i == Lay::B_BOTH) count = 8;
-            if (i >= Lay::B_IEMPTY) count = kItemReaders;
-            mbar_init(bar(i), count);
-        }
         *abort_flag = 0;
         for (int i = 0; i < kBadRing; ++i) bad_seg[i] = 0;
         for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(fl + Lay::kFloats)[i] = 0;  // votes
         p.recs[blockIdx.x].valid = 0;
-        fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), Lay::kTmem);
     plan_share(p, plan, share);
@@ -376,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t s_row = tmem + lane_off + h * NT, o_row = tmem + lane_off + (2 + h) * NT;
         unsigned char *prow = smem + Lay::OFF_P + h * Lay::kP + wt * 128;
+        constexpr int CH = NT < 32 ? NT : 32;
         float *red = fl + Lay::kRed + h * 4 * NT, *fac = fl + Lay::kFac + h * NT;
         volatile uint32_t *votes = reinterpret_cast<volatile uint32_t *>(fl + Lay::kFloats) + h * 2;
         uint32_t t = 0;                  // key tiles of this stream before this one
@@ -412,25 +424,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                 const int key = (it.j0 + i) * BN + wt, n0 = (it.j0 + i) * BN;
                 // every row sees every key of the tile?
                 const bool masked = n0 + BN > it.p0 + 1 || (p.window > 0 && n0 < last_pos - p.window + 1);
-                uint32_t sv[NT];
-                auto read_s = [&]() {
+                // CH columns at a time: 64 scores and 64 sums a thread would not fit the registers, so
+                // two halves of 64 columns are read again for the exponentials
+                uint32_t sv[CH];
+                auto read_s = [&](int c0) {
 #pragma unroll
-                    for (int c = 0; c < NT / 16; ++c) tmem_ld<16>(s_row + c * 16, sv + c * 16);
+                    for (int c = 0; c < CH; c += 16) tmem_ld<16>(s_row + c0 + c, sv + c);
                     tmem_wait_ld();
                     if (masked) {
-                        int pos = it.p0, in_tok = 0;
+                        int pos = it.p0 + c0 / p.G, in_tok = c0 % p.G;
 #pragma unroll
-                        for (int c = 0; c < NT; ++c) {
+                        for (int c = 0; c < CH; ++c) {
                             if (key > pos || (p.window > 0 && key <= pos - p.window)) sv[c] = 0xff800000u;  // -inf
                             if (++in_tok == p.G) in_tok = 0, ++pos;
                         }
                     }
                 };
-                read_s();
-                auto shift = [&](float &most) {  // s -> s * scale - maximum, in place
+                auto shift = [&](int c0) {  // s -> s * scale - reference, in place; the largest
+                    float most = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < NT; c += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4 *>(mx + c);
+                    for (int c = 0; c < CH; c += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4 *>(mx + c0 + c);
                         const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -439,24 +453,36 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                             sv[c + e] = __float_as_uint(x);
                         }
                     }
+                    return most;
                 };
-                float most = -INFINITY;
-                shift(most);
-                // A reference moves when some score exceeds it by more than 2^8: the sum uses the same
-                // reference, so the result is exact, and P stays below 2^8.
-                if (!(ok = meet(most > 8.f, any))) break;
-                if (any) {
-                    read_s();
+                any = true;  // the segment's first tile sets the references
+                if (i > h) {
+                    // A reference moves when some score exceeds it by more than 2^8: the sum uses the same
+                    // reference, so the result is exact, and P stays below 2^8.
+                    float most = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        const uint32_t k = __reduce_max_sync(kFull, rank_of(__uint_as_float(sv[c])));
-                        if (lane == (c & 31)) red[quarter * NT + c] = ranked(k);
+                    for (int c0 = 0; c0 < NT; c0 += CH) {
+                        read_s(c0);
+                        most = fmaxf(most, shift(c0));
+                    }
+                    if (!(ok = meet(most > 8.f, any))) break;
+                }
+                const bool moved = any;
+                if (moved) {
+#pragma unroll
+                    for (int c0 = 0; c0 < NT; c0 += CH) {
+                        read_s(c0);
+                        float v[CH];
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) v[c] = __uint_as_float(sv[c]);
+                        const float top = fold(v, [](float a, float b) { return fmaxf(a, b); });
+                        if (lane < CH) red[quarter * NT + c0 + lane] = top;
                     }
                     if (!(ok = meet(false, any))) break;
                     if (wt < NT) {
                         const float x = fmaxf(fmaxf(red[wt], red[NT + wt]), fmaxf(red[2 * NT + wt], red[3 * NT + wt]));
                         const float old = mx[wt], top = x * p.scale_log2;
-                        const bool move = top > old + 8.f;  // never where old is +inf, x -inf or NaN
+                        const bool move = top > old + 8.f;  // never where old is +inf, or x -inf
                         fac[wt] = move ? fast_exp2(old - top) : 1.f;
                         if (move) mx[wt] = top;
                     }
@@ -480,27 +506,38 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                         }
                         tmem_wait_st();
                     }
-                    shift(most);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(Lay::B_F + h));  // S has been read
                 // the stream's previous PV has read P
                 if (t > 0 && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
 #pragma unroll
-                for (int q = 0; q < NT / 8; ++q) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = q * 8 + e * 2;
-                        const float p0 = fast_exp2(__uint_as_float(sv[c])), p1 = fast_exp2(__uint_as_float(sv[c + 1]));
-                        l[c] += p0;
-                        l[c + 1] += p1;
-                        // P is rounded to the storage type (the tensor cores' operand), the sum is not
-                        pk[e] = E::pack2(p0, p1);
+                for (int c0 = 0; c0 < NT; c0 += CH) {
+                    if (moved && CH == NT) {
+                        shift(c0);  // the scores are in registers, as they are where nothing moved
+                    } else if (CH < NT) {
+                        read_s(c0);
+                        shift(c0);
                     }
-                    // 16-byte chunk q of a key's row sits at q ^ (key % 8)
-                    *reinterpret_cast<uint4 *>(prow + ((q ^ (wt & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    if (c0 + CH == NT) {  // S has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(Lay::B_F + h));
+                    }
+#pragma unroll
+                    for (int q = 0; q < CH / 8; ++q) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = q * 8 + e * 2;
+                            const float p0 = fast_exp2(__uint_as_float(sv[c])), p1 = fast_exp2(__uint_as_float(sv[c + 1]));
+                            l[c0 + c] += p0;
+                            l[c0 + c + 1] += p1;
+                            // P is rounded to the storage type (the tensor cores' operand), the sum is not
+                            pk[e] = E::pack2(p0, p1);
+                        }
+                        // 16-byte chunk q of a key's row sits at q ^ (key % 8)
+                        *reinterpret_cast<uint4 *>(prow + (((c0 / 8 + q) ^ (wt & 7)) << 4)) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -508,26 +545,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                 if (lane == 0) mbar_arrive(bar(Lay::B_P + h));
             }
             if (!ok) break;
-            // ---- the segment's end. Sums over the warp's keys, a column a lane: halves of the columns
-            // change places with the lane 16, 8, ... away
+            // ---- the segment's end: sums over the warp's keys
             float *sums = fl + Lay::kSum + ((par * 2 + h) * 4 + quarter) * NT;
 #pragma unroll
-            for (int c0 = 0; c0 < NT; c0 += 32) {
-                constexpr int W = NT < 32 ? NT : 32;
-                float v[W];
+            for (int c0 = 0; c0 < NT; c0 += CH) {
+                float v[CH];
 #pragma unroll
-                for (int c = 0; c < W; ++c) v[c] = l[c0 + c];
-#pragma unroll
-                for (int w = W / 2; w > 0; w >>= 1) {
-                    const bool upper = lane & w;
-#pragma unroll
-                    for (int c = 0; c < w; ++c) {
-                        const float give = upper ? v[c] : v[c + w], keep = upper ? v[c + w] : v[c];
-                        v[c] = keep + __shfl_xor_sync(kFull, give, w);
-                    }
-                }
-                if (NT < 32) v[0] += __shfl_xor_sync(kFull, v[0], 16);
-                if (lane < W) sums[c0 + lane] = v[0];
+                for (int c = 0; c < CH; ++c) v[c] = l[c0 + c];
+                const float sum = fold(v, [](float a, float b) { return a + b; });
+                if (lane < CH) sums[c0 + lane] = sum;
             }
             const int cnt_b = cnt / 2;
             // this stream's products are complete; then both streams', with their maxima and sums
@@ -562,26 +588,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             const uint32_t oa = tmem + lane_off + 2 * NT, ob = oa + NT;
             const int d = wt;  // element of the head
             T *out = static_cast<T *>(p.out);
+            constexpr int W = NT / 2 < 16 ? 8 : 16;
 #pragma unroll 1
-            for (int c0 = h * (NT / 2); c0 < (h + 1) * (NT / 2) && c0 < rows; c0 += 8) {
-                uint32_t a[8], b[8];
-                tmem_ld<8>(oa + c0, a);
-                if (cnt_b > 0) tmem_ld<8>(ob + c0, b);
+            for (int c0 = h * (NT / 2); c0 < (h + 1) * (NT / 2) && c0 < rows; c0 += W) {
+                uint32_t a[W], b[W];
+                tmem_ld<W>(oa + c0, a);
+                if (cnt_b > 0) tmem_ld<W>(ob + c0, b);
                 tmem_wait_ld();
                 if (d < HD) {
+                    int tk = c0 / p.G, in_tok = c0 - tk * p.G;
+                    float *pc = piece + 2 * NT + c0 * HD + d;
+                    T *oc = out + (static_cast<size_t>(it.tok0 + tk) * p.Hq + it.g * p.G + in_tok) * HD + d;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int c = c0 + e;
-                        if (c < rows) {
-                            float o = __uint_as_float(a[e]) * wa[c];
-                            if (cnt_b > 0) o = fmaf(__uint_as_float(b[e]), wb[c], o);
-                            if (piece) {
-                                piece[2 * NT + static_cast<size_t>(c) * HD + d] = o;
-                            } else {
-                                const int tk = it.tok0 + c / p.G, head = it.g * p.G + c % p.G;
-                                out[(static_cast<size_t>(tk) * p.Hq + head) * HD + d] = T(bad ? 0.f : o);
-                            }
+                    for (int e = 0; e < W; ++e) {
+                        if (c0 + e < rows) {
+                            float o = __uint_as_float(a[e]) * wa[c0 + e];
+                            if (cnt_b > 0) o = fmaf(__uint_as_float(b[e]), wb[c0 + e], o);
+                            if (piece)
+                                pc[e * HD] = o;
+                            else
+                                *oc = T(bad ? 0.f : o);
                         }
+                        oc += HD;
+                        if (++in_tok == p.G) in_tok = 0, oc += (p.Hq - p.G) * HD;
                     }
                 }
             }

@@ -139,8 +139,17 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
     // CTAs 0 .. P - 1 take a share, at least one tile each (no piece of an item is then empty)
     r.P = min(static_cast<long long>(gridDim.x), r.N);
     const long long me = blockIdx.x;
-    r.b0 = me < r.P ? me * r.N / r.P : r.N;
-    r.b1 = me < r.P ? (me + 1) * r.N / r.P : r.N;
+    r.b0 = r.b1 = r.N;
+    if (me < r.P) {
+        if (r.N <= 0xffffffffll / gridDim.x) {  // 64-bit divisions cost some hundred cycles
+            const uint32_t n = static_cast<uint32_t>(r.N), c = static_cast<uint32_t>(r.P), i = blockIdx.x;
+            r.b0 = i * n / c;
+            r.b1 = (i + 1) * n / c;
+        } else {
+            r.b0 = me * r.N / r.P;
+            r.b1 = (me + 1) * r.N / r.P;
+        }
+    }
     if (r.b0 < r.b1) {
         long long base = 0, total = first;
         for (int sb = 0;; sb += kThreads) {
@@ -204,6 +213,7 @@ __device__ __forceinline__ bool walk_share(const ChunkParams &p, const Share sh,
                 it.n_lo = p.window > 0 ? max(0, it.p0 - p.window + 1) : 0;
                 it.j0 = it.n_lo / BN + first, it.j1 = it.n_lo / BN + last;
                 it.part = first > 0 ? 0 : last < n ? 1 : -1;
+                if (!publish(it)) return false;
                 if (it.part == 1 && lane == 0) {
                     // the CTA that holds the item's last tile: share c is [c N / P, (c + 1) N / P)
                     PieceRec r{};
@@ -212,7 +222,6 @@ __device__ __forceinline__ bool walk_share(const ChunkParams &p, const Share sh,
                     r.last_cta = static_cast<int>(((x + 1) * sh.P - 1) / sh.N);
                     p.recs[blockIdx.x] = r;
                 }
-                if (!publish(it)) return false;
                 at += last - first;
             }
         ++s;
