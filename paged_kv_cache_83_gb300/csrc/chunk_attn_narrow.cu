@@ -31,23 +31,27 @@ namespace {
 
 using namespace chunk;
 
-template <int HD, int NT>
+// NT columns a stream. kCols: the streams halve the query rows (2 NT of them) and both take every key tile, from
+// rings that they share; else they halve the key tiles, each with rings of its own.
+template <int HD, int NT, bool kCols>
 struct Narrow {
+    static constexpr int kNC = kCols ? 2 * NT : NT;     // query rows
     static constexpr int kKV = BN * HD * 2;
     static constexpr int kHalves = HD / 64;
-    static constexpr int kQHalf = NT * 128;             // 64 columns of NT query rows
+    static constexpr int kQHalf = kNC * 128;            // 64 columns of the query rows
     static constexpr int kQ = kQHalf * kHalves;
     static constexpr int kQStep = (kQ + 1023) / 1024 * 1024;
     static constexpr int kP = BN * 128;                 // P^T: a 128-byte row a key
-    static constexpr int kD = HD == 128 ? 1 : 2;        // slots of each of the four rings (K and V of a stream)
+    static constexpr int kSlots = HD == 128 ? 2 : 4;    // K tiles held, and V tiles
+    static constexpr int kD = kCols ? kSlots : kSlots / 2;  // of a ring
     // barriers; rings, S, F, P, O, WG: + stream
-    static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = B_KFULL + 2 * kD,
-                         B_VFULL = B_KEMPTY + 2 * kD, B_VEMPTY = B_VFULL + 2 * kD, B_S = B_VEMPTY + 2 * kD, B_F = B_S + 2,
-                         B_P = B_F + 2, B_WG = B_P + 2, B_O = B_WG + 2, B_OFREE = B_O + 2, B_BOTH = B_OFREE + 1,
+    static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = B_KFULL + kSlots,
+                         B_VFULL = B_KEMPTY + kSlots, B_VEMPTY = B_VFULL + kSlots, B_S = B_VEMPTY + kSlots, B_F = B_S + 2,
+                         B_P = B_F + 2, B_WG = B_P + 2, B_O = B_WG + 2, B_OFREE = B_O + 2, B_BOTH = B_OFREE + 2,
                          B_END = B_BOTH + 1, B_IFULL = B_END + 2, B_IEMPTY = B_IFULL + 4, NBAR = B_IEMPTY + 4;
     // shared memory: V's rings before K's (at head dim 64 the V operand's unused upper half of rows reads
     // one tile further)
-    static constexpr int OFF_V = 0, OFF_K = 2 * kD * kKV, OFF_Q = OFF_K + 2 * kD * kKV, OFF_P = OFF_Q + 2 * kQStep;
+    static constexpr int OFF_V = 0, OFF_K = kSlots * kKV, OFF_Q = OFF_K + kSlots * kKV, OFF_P = OFF_Q + 2 * kQStep;
     static constexpr int OFF_F = OFF_P + 2 * kP;        // floats below
     // per segment parity and stream: maxima [NT], sums by warp [4][NT], weights [NT]; and scratch
     static constexpr int kMax = 0, kSum = 2 * 2 * NT, kWgt = kSum + 2 * 2 * 4 * NT, kRed = kWgt + 2 * 2 * NT,
@@ -60,7 +64,7 @@ struct Narrow {
     static constexpr int kSmem = OFF_MISC + 16 + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
     static constexpr int kTmem = 4 * NT < 32 ? 32 : 4 * NT;
-    static constexpr size_t kPieceFloats = static_cast<size_t>(NT) * (HD + 2);  // m[NT], l[NT], O[NT][HD]
+    static constexpr size_t kPieceFloats = static_cast<size_t>(kNC) * (HD + 2);  // m[kNC], l[kNC], O[kNC][HD]
 };
 
 // instruction descriptor with A stored with its rows (M) contiguous
@@ -100,10 +104,11 @@ __device__ __forceinline__ float fold(float (&v)[W], F op) {
 }
 constexpr float kUnset = -3e38f;  // the maximum of a column that has seen no key: finite, below every score
 
-template <class E, int HD, int NT, bool kGather>
+template <class E, int HD, int NT, bool kCols, bool kGather>
 __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_constant__ ChunkParams p) {
     using T = typename E::T;
-    using Lay = Narrow<HD, NT>;
+    using Lay = Narrow<HD, NT, kCols>;
+    constexpr int kStep = kCols ? 1 : 2;  // key tiles from one to the next of a stream
     constexpr int kHalves = Lay::kHalves;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -123,8 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     if (tid < Lay::NBAR) {
         uint32_t count = 1;
         if (tid >= Lay::B_QEMPTY && tid < Lay::B_KFULL) count = 2;       // both issuers
+        if (kCols && ((tid >= Lay::B_KEMPTY && tid < Lay::B_VFULL) || (tid >= Lay::B_VEMPTY && tid < Lay::B_S))) count = 2;
         if (tid >= Lay::B_F && tid < Lay::B_O) count = 4;                // F, P, WG: four warps
-        if (tid == Lay::B_OFREE || tid == Lay::B_BOTH) count = 8;
+        if (tid >= Lay::B_OFREE && tid < Lay::B_END) count = 8;
+        if (kCols && tid >= Lay::B_OFREE && tid < Lay::B_BOTH) count = 4;
         if (tid >= Lay::B_IEMPTY) count = kItemReaders;
         mbar_init(bar(tid), count);
         fence_mbar_init();
@@ -273,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                 has[h] = true;
                 return true;
             };
-            for (int j = cur.j0; ok && j < cur.j1; j += 2) ok = tile(j, A{}) && (j + 1 == cur.j1 || tile(j + 1, B{}));
+            for (int j = cur.j0; ok && j < cur.j1; j += kStep)
+                ok = tile(j, A{}) && (kCols || j + 1 == cur.j1 || tile(j + 1, B{}));
             ++n;
         }
         ok = ok && pending(A{}) && pending(B{});
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         if (lane == 0) {
             if (!kGather)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < (kCols ? 1 : 2); ++h)
 #pragma unroll
                     for (uint32_t back = 1; back <= Lay::kD; ++back) {
                         if (nk[h] >= back) {
@@ -306,9 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         const int h = warp - 1;
         constexpr uint32_t IQK = idesc_f16(BM, NT, E::kIsBf16, false);              // A = K rows, B = Q rows, both K-major
         constexpr uint32_t IPV = idesc_a_mn(idesc_f16(BM, NT, E::kIsBf16, true));   // A = V^T, B = P^T, both MN-major
-        const uint64_t dq0 = smem_desc_sw128(sbase + Lay::OFF_Q, 16, 1024);
-        const uint64_t dk0 = smem_desc_sw128(sbase + Lay::OFF_K + h * Lay::kD * Lay::kKV, 16, 1024);
-        const uint64_t dv0 = smem_desc_sw128(sbase + Lay::OFF_V + h * Lay::kD * Lay::kKV, kHalf, 1024);
+        const int ring = kCols ? 0 : h * Lay::kD, first = kCols ? 0 : h;  // the stream's first slot, and key tile
+        const uint64_t dq0 = smem_desc_sw128(sbase + Lay::OFF_Q + (kCols ? h * NT * 128 : 0), 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(sbase + Lay::OFF_K + ring * Lay::kKV, 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(sbase + Lay::OFF_V + ring * Lay::kKV, kHalf, 1024);
         const uint64_t dp = smem_desc_sw128(sbase + Lay::OFF_P + h * Lay::kP, kHalf, 1024);
         const uint32_t s_tm = tmem + h * NT, o_tm = tmem + (2 + h) * NT;
         auto qk = [&](int slot, int q) {  // S^T = K Q^T
@@ -331,12 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         auto issue_qk = [&](int n, bool last) -> bool {
             const int slot = static_cast<int>(t % Lay::kD);
             if (t > 0 && !warp_wait(bar(Lay::B_F + h), (t - 1) & 1, abort_flag)) return false;
-            if (!warp_wait(bar(Lay::B_KFULL + h * Lay::kD + slot), (t / Lay::kD) & 1, abort_flag)) return false;
+            if (!warp_wait(bar(Lay::B_KFULL + ring + slot), (t / Lay::kD) & 1, abort_flag)) return false;
             tc_fence_after();
             if (lane == 0) {
                 qk(slot, n & 1);
                 tc_commit(bar(Lay::B_S + h));
-                tc_commit(bar(Lay::B_KEMPTY + h * Lay::kD + slot));
+                tc_commit(bar(Lay::B_KEMPTY + ring + slot));
                 if (last) tc_commit(bar(Lay::B_QEMPTY + (n & 1)));
             }
             __syncwarp();
@@ -348,28 +357,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             if (!(ok = read_seg(n, it)) || it.j0 == it.j1) break;
             const int cnt = it.j1 - it.j0;
             if (!(ok = warp_wait(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, abort_flag))) break;
-            if (h >= cnt) {  // a segment of one tile has none for stream B
+            if (first >= cnt) {  // a segment of one tile has none for stream B
                 if (lane == 0) mbar_arrive(bar(Lay::B_QEMPTY + (n & 1)));
                 __syncwarp();
                 continue;
             }
-            if (!(ok = issue_qk(n, h + 2 >= cnt))) break;
-            for (int i = h; i < cnt; i += 2, ++done) {
-                if (i + 2 < cnt && !(ok = issue_qk(n, i + 4 >= cnt))) break;
+            if (!(ok = issue_qk(n, first + kStep >= cnt))) break;
+            for (int i = first; i < cnt; i += kStep, ++done) {
+                if (i + kStep < cnt && !(ok = issue_qk(n, i + 2 * kStep >= cnt))) break;
                 const int slot = static_cast<int>(done % Lay::kD);
                 if (!(ok = warp_wait(bar(Lay::B_P + h), done & 1, abort_flag) &&
-                           warp_wait(bar(Lay::B_VFULL + h * Lay::kD + slot), (done / Lay::kD) & 1, abort_flag)))
+                           warp_wait(bar(Lay::B_VFULL + ring + slot), (done / Lay::kD) & 1, abort_flag)))
                     break;
                 const int n0 = (it.j0 + i) * BN, z0 = max(it.n_lo - n0, 0), z1 = min(it.n_end - n0, BN);
-                if (z0 > 0 || z1 < BN) zero_rows<HD>(smem + Lay::OFF_V + (h * Lay::kD + slot) * Lay::kKV, z0, z1);
+                // (streams that share the tile both write the zeros)
+                if (z0 > 0 || z1 < BN) zero_rows<HD>(smem + Lay::OFF_V + (ring + slot) * Lay::kKV, z0, z1);
                 // the previous segment's output must be out of TMEM before its O is overwritten. (B may have
                 // had no tile in it; its softmax warps have then passed the end of that segment with A's.)
-                if (i == h && n > 0 && !(ok = warp_wait(bar(Lay::B_OFREE), (n - 1) & 1, abort_flag))) break;
+                if (i == first && n > 0 && !(ok = warp_wait(bar(Lay::B_OFREE + (kCols ? h : 0)), (n - 1) & 1, abort_flag)))
+                    break;
                 tc_fence_after();
                 if (lane == 0) {
-                    pv(slot, i > h);
+                    pv(slot, i > first);
                     tc_commit(bar(Lay::B_O + h));
-                    tc_commit(bar(Lay::B_VEMPTY + h * Lay::kD + slot));
+                    tc_commit(bar(Lay::B_VEMPTY + ring + slot));
                 }
                 __syncwarp();
             }
@@ -387,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t s_row = tmem + lane_off + h * NT, o_row = tmem + lane_off + (2 + h) * NT;
         unsigned char *prow = smem + Lay::OFF_P + h * Lay::kP + wt * 128;
-        constexpr int CH = NT < 32 ? NT : 32;
+        const int first = kCols ? 0 : h;         // the stream's first key tile of a segment
+        const int col0 = kCols ? h * NT : 0;     // the query row of its first column
         float *red = fl + Lay::kRed + h * 4 * NT, *fac = fl + Lay::kFac + h * NT;
         volatile uint32_t *votes = reinterpret_cast<volatile uint32_t *>(fl + Lay::kFloats) + h * 2;
         uint32_t t = 0;                  // key tiles of this stream before this one
@@ -412,39 +424,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             const int cnt = it.j1 - it.j0, rows = it.tok * p.G, par = n & 1;
             float *mx = fl + Lay::kMax + (par * 2 + h) * NT;
             // columns without a query row have a maximum that leaves them no weight
-            if (wt < NT) mx[wt] = wt < rows ? kUnset : INFINITY;
+            if (wt < NT) mx[wt] = col0 + wt < rows ? kUnset : INFINITY;
             if (!(ok = meet(false, any))) break;
             float l[NT];
 #pragma unroll
             for (int c = 0; c < NT; ++c) l[c] = 0.f;
             const int last_pos = it.p0 + it.tok - 1;
-            for (int i = h; i < cnt; i += 2, ++t) {
+            for (int i = first; i < cnt; i += kStep, ++t) {
                 if (!(ok = warp_wait(bar(Lay::B_S + h), t & 1, abort_flag))) break;
                 tc_fence_after();
                 const int key = (it.j0 + i) * BN + wt, n0 = (it.j0 + i) * BN;
                 // every row sees every key of the tile?
                 const bool masked = n0 + BN > it.p0 + 1 || (p.window > 0 && n0 < last_pos - p.window + 1);
-                // CH columns at a time: 64 scores and 64 sums a thread would not fit the registers, so
-                // two halves of 64 columns are read again for the exponentials
-                uint32_t sv[CH];
-                auto read_s = [&](int c0) {
+                uint32_t sv[NT];
+                auto read_s = [&]() {
 #pragma unroll
-                    for (int c = 0; c < CH; c += 16) tmem_ld<16>(s_row + c0 + c, sv + c);
+                    for (int c = 0; c < NT; c += 16) tmem_ld<16>(s_row + c, sv + c);
                     tmem_wait_ld();
                     if (masked) {
-                        int pos = it.p0 + c0 / p.G, in_tok = c0 % p.G;
+                        int pos = it.p0 + col0 / p.G, in_tok = col0 % p.G;
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) {
+                        for (int c = 0; c < NT; ++c) {
                             if (key > pos || (p.window > 0 && key <= pos - p.window)) sv[c] = 0xff800000u;  // -inf
                             if (++in_tok == p.G) in_tok = 0, ++pos;
                         }
                     }
                 };
-                auto shift = [&](int c0) {  // s -> s * scale - reference, in place; the largest
+                auto shift = [&]() {  // s -> s * scale - reference, in place; the largest
                     float most = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < CH; c += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4 *>(mx + c0 + c);
+                    for (int c = 0; c < NT; c += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4 *>(mx + c);
                         const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -455,29 +465,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                     }
                     return most;
                 };
+                read_s();
                 any = true;  // the segment's first tile sets the references
-                if (i > h) {
+                if (i > first) {
                     // A reference moves when some score exceeds it by more than 2^8: the sum uses the same
                     // reference, so the result is exact, and P stays below 2^8.
-                    float most = -INFINITY;
-#pragma unroll
-                    for (int c0 = 0; c0 < NT; c0 += CH) {
-                        read_s(c0);
-                        most = fmaxf(most, shift(c0));
-                    }
-                    if (!(ok = meet(most > 8.f, any))) break;
+                    if (!(ok = meet(shift() > 8.f, any))) break;
                 }
-                const bool moved = any;
-                if (moved) {
+                if (any) {
+                    if (i > first) read_s();
+                    float v[NT];
 #pragma unroll
-                    for (int c0 = 0; c0 < NT; c0 += CH) {
-                        read_s(c0);
-                        float v[CH];
-#pragma unroll
-                        for (int c = 0; c < CH; ++c) v[c] = __uint_as_float(sv[c]);
-                        const float top = fold(v, [](float a, float b) { return fmaxf(a, b); });
-                        if (lane < CH) red[quarter * NT + c0 + lane] = top;
-                    }
+                    for (int c = 0; c < NT; ++c) v[c] = __uint_as_float(sv[c]);
+                    const float top = fold(v, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < NT) red[quarter * NT + lane] = top;
                     if (!(ok = meet(false, any))) break;
                     if (wt < NT) {
                         const float x = fmaxf(fmaxf(red[wt], red[NT + wt]), fmaxf(red[2 * NT + wt], red[3 * NT + wt]));
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                         const float4 f4 = *reinterpret_cast<const float4 *>(fac + c);
                         l[c] *= f4.x, l[c + 1] *= f4.y, l[c + 2] *= f4.z, l[c + 3] *= f4.w;
                     }
-                    if (i > h) {
+                    if (i > first) {
                         if (!(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
                         tc_fence_after();
 #pragma unroll
@@ -506,38 +507,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                         }
                         tmem_wait_st();
                     }
+                    shift();
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Lay::B_F + h));  // S has been read
                 // the stream's previous PV has read P
                 if (t > 0 && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
 #pragma unroll
-                for (int c0 = 0; c0 < NT; c0 += CH) {
-                    if (moved && CH == NT) {
-                        shift(c0);  // the scores are in registers, as they are where nothing moved
-                    } else if (CH < NT) {
-                        read_s(c0);
-                        shift(c0);
-                    }
-                    if (c0 + CH == NT) {  // S has been read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(Lay::B_F + h));
-                    }
+                for (int q = 0; q < NT / 8; ++q) {
+                    uint32_t pk[4];
 #pragma unroll
-                    for (int q = 0; q < CH / 8; ++q) {
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = q * 8 + e * 2;
-                            const float p0 = fast_exp2(__uint_as_float(sv[c])), p1 = fast_exp2(__uint_as_float(sv[c + 1]));
-                            l[c0 + c] += p0;
-                            l[c0 + c + 1] += p1;
-                            // P is rounded to the storage type (the tensor cores' operand), the sum is not
-                            pk[e] = E::pack2(p0, p1);
-                        }
-                        // 16-byte chunk q of a key's row sits at q ^ (key % 8)
-                        *reinterpret_cast<uint4 *>(prow + (((c0 / 8 + q) ^ (wt & 7)) << 4)) =
-                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = q * 8 + e * 2;
+                        const float p0 = fast_exp2(__uint_as_float(sv[c])), p1 = fast_exp2(__uint_as_float(sv[c + 1]));
+                        l[c] += p0;
+                        l[c + 1] += p1;
+                        // P is rounded to the storage type (the tensor cores' operand), the sum is not
+                        pk[e] = E::pack2(p0, p1);
                     }
+                    // 16-byte chunk q of a key's row sits at q ^ (key % 8)
+                    *reinterpret_cast<uint4 *>(prow + ((q ^ (wt & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -547,30 +537,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             if (!ok) break;
             // ---- the segment's end: sums over the warp's keys
             float *sums = fl + Lay::kSum + ((par * 2 + h) * 4 + quarter) * NT;
-#pragma unroll
-            for (int c0 = 0; c0 < NT; c0 += CH) {
-                float v[CH];
-#pragma unroll
-                for (int c = 0; c < CH; ++c) v[c] = l[c0 + c];
-                const float sum = fold(v, [](float a, float b) { return a + b; });
-                if (lane < CH) sums[c0 + lane] = sum;
+            const float sum_c = fold(l, [](float a, float b) { return a + b; });
+            if (lane < NT) sums[lane] = sum_c;
+            const int cnt_b = kCols ? 0 : cnt / 2;  // tiles of the other stream's accumulator to be joined with A's
+            // this stream's products are complete; then, where the streams halve the keys, both streams', with
+            // their maxima and sums
+            if (cnt > first && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+            if constexpr (kCols) {
+                if (!(ok = meet(false, any))) break;
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Lay::B_BOTH));
+                if (!(ok = warp_wait(bar(Lay::B_BOTH), n & 1, abort_flag))) break;
             }
-            const int cnt_b = cnt / 2;
-            // this stream's products are complete; then both streams', with their maxima and sums
-            if (cnt > h && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(Lay::B_BOTH));
-            if (!(ok = warp_wait(bar(Lay::B_BOTH), n & 1, abort_flag))) break;
             tc_fence_after();
-            // this stream writes columns [h NT / 2, (h + 1) NT / 2)
+            // this stream writes the query rows [c_lo, c_lo + kMine): its own, or half of the streams' common ones
+            constexpr int kMine = kCols ? NT : NT / 2;
+            const int c_lo = h * kMine, acc = kCols ? h : 0;  // the stream whose state counts as A's
             const bool bad = bad_seg[n & (kBadRing - 1)] == n + 1;  // a table entry of the segment was bad
             float *piece = it.part < 0 ? nullptr
                                        : p.pieces + (static_cast<size_t>(blockIdx.x) * 2 + it.part) * Lay::kPieceFloats;
             float *wa = fl + Lay::kWgt + par * 2 * NT, *wb = wa + NT;
-            if (wt < NT / 2) {
-                const int c = h * (NT / 2) + wt;
-                const float *sa = fl + Lay::kSum + par * 8 * NT + c, *sb = sa + 4 * NT;
-                const float ma = fl[Lay::kMax + par * 2 * NT + c], mb = cnt_b > 0 ? fl[Lay::kMax + (par * 2 + 1) * NT + c] : kUnset;
+            if (wt < kMine) {
+                const int c = c_lo + wt, ca = c - (kCols ? col0 : 0);  // its column in the stream
+                const float *sa = fl + Lay::kSum + (par * 2 + acc) * 4 * NT + ca, *sb = fl + Lay::kSum + (par * 2 + 1) * 4 * NT + ca;
+                const float ma = fl[Lay::kMax + (par * 2 + acc) * NT + ca], mb = cnt_b > 0 ? fl[Lay::kMax + (par * 2 + 1) * NT + ca] : kUnset;
                 const float la = (sa[0] + sa[NT]) + (sa[2 * NT] + sa[3 * NT]);
                 const float lb = cnt_b > 0 ? (sb[0] + sb[NT]) + (sb[2 * NT] + sb[3 * NT]) : 0.f;
                 const float m = fmaxf(ma, mb), fa = fast_exp2(ma - m), fb = cnt_b > 0 ? fast_exp2(mb - m) : 0.f;
@@ -578,26 +569,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                 float scale = 1.f;  // a piece: O unnormalised, with its maximum and sum (sum -1: bad)
                 if (!piece) scale = sum > 0.f ? 1.f / sum : sum == sum ? 0.f : sum;
                 wa[c] = fa * scale;
-                wb[c] = fb * scale;
+                if (!kCols) wb[c] = fb * scale;
                 if (piece) {
                     piece[c] = m;
-                    piece[NT + c] = bad ? -1.f : sum;
+                    piece[Lay::kNC + c] = bad ? -1.f : sum;
                 }
             }
             if (!(ok = meet(false, any))) break;
-            const uint32_t oa = tmem + lane_off + 2 * NT, ob = oa + NT;
+            const uint32_t oa = tmem + lane_off + (2 + acc) * NT - (kCols ? col0 : 0), ob = oa + NT;  // at column c: + c
             const int d = wt;  // element of the head
             T *out = static_cast<T *>(p.out);
-            constexpr int W = NT / 2 < 16 ? 8 : 16;
+            constexpr int W = kMine < 16 ? 8 : 16;
 #pragma unroll 1
-            for (int c0 = h * (NT / 2); c0 < (h + 1) * (NT / 2) && c0 < rows; c0 += W) {
+            for (int c0 = c_lo; c0 < c_lo + kMine && c0 < rows; c0 += W) {
                 uint32_t a[W], b[W];
                 tmem_ld<W>(oa + c0, a);
                 if (cnt_b > 0) tmem_ld<W>(ob + c0, b);
                 tmem_wait_ld();
                 if (d < HD) {
                     int tk = c0 / p.G, in_tok = c0 - tk * p.G;
-                    float *pc = piece + 2 * NT + c0 * HD + d;
+                    float *pc = piece + 2 * Lay::kNC + c0 * HD + d;
                     T *oc = out + (static_cast<size_t>(it.tok0 + tk) * p.Hq + it.g * p.G + in_tok) * HD + d;
 #pragma unroll
                     for (int e = 0; e < W; ++e) {
@@ -616,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(Lay::B_OFREE));
+            if (lane == 0) mbar_arrive(bar(Lay::B_OFREE + acc));
         }
         if (!ok && lane == 0) give_up(p.err, abort_flag);
     }
@@ -639,9 +630,9 @@ constexpr int kJoinWork = 64, kJoinGroups = 4;  // outputs of four columns of a 
 // 1); the pieces after it are slot 0 of the CTAs up to last_cta. An item of a long sequence has tens of
 // pieces: four groups of threads read four pieces each at a time (a thread for all 25 pieces of
 // one, one after the other, took 41 us; so 4 us).
-template <class E, int HD, int NT>
+template <class E, int HD, int NT, bool kCols>
 __global__ void __launch_bounds__(kJoinWork * kJoinGroups) chunk_narrow_join_kernel(const __grid_constant__ ChunkParams p) {
-    using Lay = Narrow<HD, NT>;
+    using Lay = Narrow<HD, NT, kCols>;
     __shared__ float part[kJoinGroups][6][kJoinWork];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PieceRec rec = p.recs[blockIdx.x];
@@ -663,8 +654,8 @@ __global__ void __launch_bounds__(kJoinWork * kJoinGroups) chunk_narrow_join_ker
                 if (c <= rec.last_cta) {
                     const float *src = p.pieces + (static_cast<size_t>(c) * 2 + (c == first)) * Lay::kPieceFloats;
                     pm[k] = __ldg(src + row);
-                    pl[k] = __ldg(src + NT + row);
-                    po[k] = __ldg(reinterpret_cast<const float4 *>(src + 2 * NT + row * HD + col));
+                    pl[k] = __ldg(src + Lay::kNC + row);
+                    po[k] = __ldg(reinterpret_cast<const float4 *>(src + 2 * Lay::kNC + row * HD + col));
                 }
             }
             const float mn = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
@@ -705,10 +696,10 @@ __global__ void __launch_bounds__(kJoinWork * kJoinGroups) chunk_narrow_join_ker
     *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (static_cast<size_t>(tk) * p.Hq + head) * HD + col) = u;
 }
 
-template <class E, int HD, int NT, bool kGather>
+template <class E, int HD, int NT, bool kCols, bool kGather>
 cudaError_t launch_typed(const ChunkParams &prm, cudaStream_t stream) {
-    using Lay = Narrow<HD, NT>;
-    auto kern = chunk_narrow_kernel<E, HD, NT, kGather>;
+    using Lay = Narrow<HD, NT, kCols>;
+    auto kern = chunk_narrow_kernel<E, HD, NT, kCols, kGather>;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -731,17 +722,17 @@ cudaError_t launch_typed(const ChunkParams &prm, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, chunk_narrow_join_kernel<E, HD, NT>, prm);
+    return cudaLaunchKernelEx(&cfg, chunk_narrow_join_kernel<E, HD, NT, kCols>, prm);
 }
 
 template <class E, int HD>
 cudaError_t launch_rows(const ChunkParams &prm, bool gather, cudaStream_t stream) {
     const int rows = prm.max_seqlen_q * prm.G;
     // gathered keys are bound by their copies, whatever the columns: one form for all
-    if (gather) return launch_typed<E, HD, 64, true>(prm, stream);
-    if (rows <= 16) return launch_typed<E, HD, 16, false>(prm, stream);
-    if (rows <= 32) return launch_typed<E, HD, 32, false>(prm, stream);
-    return launch_typed<E, HD, 64, false>(prm, stream);
+    if (gather) return launch_typed<E, HD, 32, true, true>(prm, stream);
+    if (rows <= 16) return launch_typed<E, HD, 16, false, false>(prm, stream);
+    if (rows <= 32) return launch_typed<E, HD, 32, false, false>(prm, stream);
+    return launch_typed<E, HD, 32, true, false>(prm, stream);
 }
 
 }  // namespace
