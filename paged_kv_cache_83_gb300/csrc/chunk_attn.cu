@@ -336,7 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             }
             // PV of key tile j
             int slot;
-            if (rows && !(ok = warp_wait(bar(B_P + h), static_cast<uint32_t>(t & 1), abort_flag))) break;
             if (!(ok = next_load(slot))) break;
             const int z0 = max(cur.n_lo - j * BN, 0), z1 = min(cur.n_end - j * BN, BN);  // rows that hold keys
             if (rows && (z0 > 0 || z1 < BN)) {
@@ -353,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
                 }
                 zt += both;
             }
+            if (rows && !(ok = warp_wait(bar(B_P + h), static_cast<uint32_t>(t & 1), abort_flag))) break;
             // the previous segment's output must be out of TMEM before its O is overwritten
             if (rows && j == cur.j0 && done > 0 && !(ok = warp_wait(bar(B_OFREE + h), (done - 1) & 1, abort_flag)))
                 break;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         unsigned char *prow = ptile + r * 128;  // half 0
         const uint32_t s_full = bar(B_S + h), s_free = bar(B_F + h), p_full = bar(B_P + h);
         const uint32_t o_done = bar(B_O + h), o_free = bar(B_OFREE + h);
-        const int row_tok = r / p.G;  // this row's token within its tile
+        const int row_tok = p.div_g(r);  // this row's token within its tile
         long long t = 0;
         bool ok = true;
         SegInfo it{};
@@ -428,10 +428,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free);
                 const int n0 = j * BN;
-                if (n0 + BN > lim || n0 < lo) {
+                if (n0 + BN > lim) {
+                    const int from = lim - n0;
 #pragma unroll
                     for (int e = 0; e < 128; ++e)
-                        if (n0 + e >= lim || n0 + e < lo) sv[e] = 0xff800000u;  // -inf
+                        if (e >= from) sv[e] = 0xff800000u;  // -inf
+                }
+                if (n0 < lo) {
+                    const int to = lo - n0;
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        if (e < to) sv[e] = 0xff800000u;
                 }
                 float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -548,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
                 const uint4 u = *reinterpret_cast<const uint4 *>(ptile + (c >> 3) * kHalf + rr * 128 +
                                                                  (((c & 7) ^ (rr & 7)) << 4));
                 if (rr < rows) {
-                    const int tk = it.tok0 + h * p.tt + rr / p.G, head = it.g * p.G + rr % p.G;
+                    const int in_tile = p.div_g(rr);
+                    const int tk = it.tok0 + h * p.tt + in_tile, head = it.g * p.G + rr - in_tile * p.G;
                     *reinterpret_cast<uint4 *>(out + (static_cast<size_t>(tk) * p.Hq + head) * HD + c * 8) = u;
                 }
             }
@@ -709,6 +717,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream) {
     while (R < 128 && a.block_size % (2 * R) == 0) R *= 2;
     const bool gather = R < 8;  // less than a swizzle atom of 8 rows
     prm.G = a.Hq / a.Hkv;
+    prm.inv_g = (65536 + prm.G - 1) / prm.G;
     prm.tt = BM / prm.G;
     // Chunks of at most 64 query rows a kv head take the form with keys as the rows: an item is a
     // whole chunk, its Q box as many tokens as the columns hold.

@@ -366,12 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
             for (int i = first; i < cnt; i += kStep, ++done) {
                 if (i + kStep < cnt && !(ok = issue_qk(n, i + 2 * kStep >= cnt))) break;
                 const int slot = static_cast<int>(done % Lay::kD);
-                if (!(ok = warp_wait(bar(Lay::B_P + h), done & 1, abort_flag) &&
-                           warp_wait(bar(Lay::B_VFULL + ring + slot), (done / Lay::kD) & 1, abort_flag)))
-                    break;
+                if (!(ok = warp_wait(bar(Lay::B_VFULL + ring + slot), (done / Lay::kD) & 1, abort_flag))) break;
                 const int n0 = (it.j0 + i) * BN, z0 = max(it.n_lo - n0, 0), z1 = min(it.n_end - n0, BN);
                 // (streams that share the tile both write the zeros)
                 if (z0 > 0 || z1 < BN) zero_rows<HD>(smem + Lay::OFF_V + (ring + slot) * Lay::kKV, z0, z1);
+                if (!(ok = warp_wait(bar(Lay::B_P + h), done & 1, abort_flag))) break;
                 // the previous segment's output must be out of TMEM before its O is overwritten. (B may have
                 // had no tile in it; its softmax warps have then passed the end of that segment with A's.)
                 if (i == first && n > 0 && !(ok = warp_wait(bar(Lay::B_OFREE + (kCols ? h : 0)), (n - 1) & 1, abort_flag)))
@@ -442,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                     for (int c = 0; c < NT; c += 16) tmem_ld<16>(s_row + c, sv + c);
                     tmem_wait_ld();
                     if (masked) {
-                        int pos = it.p0 + col0 / p.G, in_tok = col0 % p.G;
+                        const int tok_c = p.div_g(col0);
+                        int pos = it.p0 + tok_c, in_tok = col0 - tok_c * p.G;
 #pragma unroll
                         for (int c = 0; c < NT; ++c) {
                             if (key > pos || (p.window > 0 && key <= pos - p.window)) sv[c] = 0xff800000u;  // -inf
@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                 if (cnt_b > 0) tmem_ld<W>(ob + c0, b);
                 tmem_wait_ld();
                 if (d < HD) {
-                    int tk = c0 / p.G, in_tok = c0 - tk * p.G;
+                    const int tk = p.div_g(c0);
+                    int in_tok = c0 - tk * p.G;
                     float *pc = piece + 2 * Lay::kNC + c0 * HD + d;
                     T *oc = out + (static_cast<size_t>(it.tok0 + tk) * p.Hq + it.g * p.G + in_tok) * HD + d;
 #pragma unroll

@@ -41,8 +41,10 @@ struct ChunkParams {
     int tt;        // tokens of a row tile
     int item_tok;  // tokens of an item
     int max_blocks, num_blocks, total_q, max_seqlen_q, window, box_rows;
+    uint32_t inv_g;  // 2^16 / G, rounded up: x inv_g >> 16 is x / G for x < 256
     BlockGeom geom;
     float scale_log2;
+    __device__ __forceinline__ int div_g(int x) const { return static_cast<int>(x * inv_g >> 16); }
 };
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
@@ -264,10 +266,13 @@ __device__ __forceinline__ void gather_tile(uint32_t dst, const T *pool, const l
 // one warp before the PV product reads them: P is zero there, but 0 * NaN is not.
 template <int HD>
 __device__ __forceinline__ void zero_rows(unsigned char *tile, int z0, int z1) {
-    for (int c = threadIdx.x & 31; c < (z0 + BN - z1) * (HD / 8); c += 32) {
-        const int rr = c / (HD / 8), c16 = c % (HD / 8), r = rr < z0 ? rr : rr - z0 + z1;
-        *reinterpret_cast<uint4 *>(tile + (c16 >> 3) * kHalf + r * 128 + (c16 & 7) * 16) = make_uint4(0, 0, 0, 0);
-    }
+    constexpr int kRows = 32 / (HD / 8);  // rows that the warp writes at a time, 16 bytes a lane
+    const int lane = threadIdx.x & 31, c16 = lane % (HD / 8), r0 = lane / (HD / 8);
+    unsigned char *at = tile + (c16 >> 3) * kHalf + (c16 & 7) * 16;
+#pragma unroll 4
+    for (int r = r0; r < z0; r += kRows) *reinterpret_cast<uint4 *>(at + r * 128) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int r = z1 + r0; r < BN; r += kRows) *reinterpret_cast<uint4 *>(at + r * 128) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
 }
