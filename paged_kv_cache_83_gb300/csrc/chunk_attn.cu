@@ -205,17 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             ++L;
             return true;
         };
-        SegInfo prev{}, cur{};
-        Rows wp{}, wc{}, wn{};
-        bool have_prev = false;
+        SegInfo cur{};
+        Rows wc{}, wn{};
         while (ok) {
             if (!(ok = read_seg(n, cur)) || cur.j0 == cur.j1) break;
             wc = rows_of(cur, cur.j0, n);
-            ok = load_tile(cur, wc, false);
-            if (ok && have_prev) ok = load_tile(prev, wp, true);
-            // this segment's Q once both issuers are past the previous segment's last QK
-            if (ok && n > 0) ok = warp_wait(bar(B_QEMPTY), (n - 1) & 1, abort_flag);
-            if (!ok) break;
+            // this segment's Q once both issuers are past the previous segment's last QK, its first K before
+            if (!(ok = load_tile(cur, wc, false))) break;
+            if (n > 0 && !(ok = warp_wait(bar(B_QEMPTY), (n - 1) & 1, abort_flag))) break;
             if (lane == 0) {
                 const int tiles = has_b(cur) ? 2 : 1;
                 const uint32_t half_bytes = static_cast<uint32_t>(p.tt) * p.G * 128;
@@ -233,12 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
                 ok = load_tile(cur, w, false) && load_tile(cur, wc, true);
                 wc = w;
             }
-            prev = cur;
-            wp = wc;
-            have_prev = true;
+            ok = ok && load_tile(cur, wc, true);
             ++n;
         }
-        if (ok && have_prev) ok = load_tile(prev, wp, true);
         if constexpr (kGather) {
             cp_async_wait<0>();
             if (ok) announce(L - 1);
@@ -310,70 +304,59 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             __syncwarp();
             return true;
         };
-        int n = 0, zt = 0;    // segments read; zeroed tiles that both row tiles take
-        long long t = 0;      // key tiles of this row tile so far
-        int done = 0;         // segments of this row tile so far
-        SegInfo cur{}, nxt{};
-        bool ok = read_seg(0, cur);
-        bool active = ok && cur.j0 < cur.j1;
-        n = 1;
-        if (active) ok = warp_wait(bar(B_QFULL), 0, abort_flag) && issue_qk(h == 0 || has_b(cur), cur.j0 + 1 == cur.j1);
-        int j = cur.j0;
-        while (ok && active) {
+        int zt = 0;       // zeroed tiles that both row tiles take
+        long long t = 0;  // key tiles of this row tile so far
+        int done = 0;     // segments of this row tile so far
+        SegInfo cur{};
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            if (!(ok = read_seg(n, cur)) || cur.j0 == cur.j1) break;
             const bool rows = h == 0 || has_b(cur);
-            // S(t + 1) as soon as the softmax holds S(t) in registers
-            if (rows && !(ok = warp_wait(bar(B_F + h), static_cast<uint32_t>(t & 1), abort_flag))) break;
-            bool has_next = true;
-            if (j + 1 < cur.j1) {
-                if (!(ok = issue_qk(rows, j + 2 == cur.j1))) break;
-            } else {
-                if (!(ok = read_seg(n, nxt))) break;
-                has_next = nxt.j0 < nxt.j1;
-                if (has_next && !(ok = warp_wait(bar(B_QFULL), n & 1, abort_flag) &&
-                                       issue_qk(h == 0 || has_b(nxt), nxt.j0 + 1 == nxt.j1)))
+            if (!(ok = warp_wait(bar(B_QFULL), n & 1, abort_flag))) break;
+            // S(t) as soon as the softmax holds S(t - 1) in registers
+            if (rows && t > 0 && !(ok = warp_wait(bar(B_F + h), static_cast<uint32_t>((t - 1) & 1), abort_flag))) break;
+            if (!(ok = issue_qk(rows, cur.j0 + 1 == cur.j1))) break;
+            for (int j = cur.j0; j < cur.j1; ++j, t += rows) {
+                if (j + 1 < cur.j1) {
+                    if (rows && !(ok = warp_wait(bar(B_F + h), static_cast<uint32_t>(t & 1), abort_flag))) break;
+                    if (!(ok = issue_qk(rows, j + 2 == cur.j1))) break;
+                }
+                // PV of key tile j
+                int slot;
+                if (!(ok = next_load(slot))) break;
+                const int z0 = max(cur.n_lo - j * BN, 0), z1 = min(cur.n_end - j * BN, BN);  // rows that hold keys
+                if (rows && (z0 > 0 || z1 < BN)) {
+                    const bool both = has_b(cur);
+                    if (h == 0) {
+                        if (both && zt > 0 &&
+                            !(ok = warp_wait(bar(B_VZACK), static_cast<uint32_t>((zt - 1) & 1), abort_flag)))
+                            break;
+                        zero_rows<HD>(smem + OFF_RING + slot * Lay::kKV, z0, z1);
+                        if (both && lane == 0) mbar_arrive(bar(B_VZ));
+                    } else {
+                        if (!(ok = warp_wait(bar(B_VZ), zt & 1, abort_flag))) break;
+                        if (lane == 0) mbar_arrive(bar(B_VZACK));
+                    }
+                    zt += both;
+                }
+                if (rows && !(ok = warp_wait(bar(B_P + h), static_cast<uint32_t>(t & 1), abort_flag))) break;
+                // the previous segment's output must be out of TMEM before its O is overwritten
+                if (rows && j == cur.j0 && done > 0 &&
+                    !(ok = warp_wait(bar(B_OFREE + h), (done - 1) & 1, abort_flag)))
                     break;
-                ++n;
-            }
-            // PV of key tile j
-            int slot;
-            if (!(ok = next_load(slot))) break;
-            const int z0 = max(cur.n_lo - j * BN, 0), z1 = min(cur.n_end - j * BN, BN);  // rows that hold keys
-            if (rows && (z0 > 0 || z1 < BN)) {
-                const bool both = has_b(cur);
-                if (h == 0) {
-                    if (both && zt > 0 &&
-                        !(ok = warp_wait(bar(B_VZACK), static_cast<uint32_t>((zt - 1) & 1), abort_flag)))
-                        break;
-                    zero_rows<HD>(smem + OFF_RING + slot * Lay::kKV, z0, z1);
-                    if (both && lane == 0) mbar_arrive(bar(B_VZ));
-                } else {
-                    if (!(ok = warp_wait(bar(B_VZ), zt & 1, abort_flag))) break;
-                    if (lane == 0) mbar_arrive(bar(B_VZACK));
+                tc_fence_after();
+                if (lane == 0) {
+                    if (rows) {
+                        pv(slot, j > cur.j0);
+                        tc_commit(bar(B_O + h));
+                        tc_commit(bar(B_EMPTY + slot));
+                    } else {
+                        mbar_arrive(bar(B_EMPTY + slot));
+                    }
                 }
-                zt += both;
+                __syncwarp();
             }
-            if (rows && !(ok = warp_wait(bar(B_P + h), static_cast<uint32_t>(t & 1), abort_flag))) break;
-            // the previous segment's output must be out of TMEM before its O is overwritten
-            if (rows && j == cur.j0 && done > 0 && !(ok = warp_wait(bar(B_OFREE + h), (done - 1) & 1, abort_flag)))
-                break;
-            tc_fence_after();
-            if (lane == 0) {
-                if (rows) {
-                    pv(slot, j > cur.j0);
-                    tc_commit(bar(B_O + h));
-                    tc_commit(bar(B_EMPTY + slot));
-                } else {
-                    mbar_arrive(bar(B_EMPTY + slot));
-                }
-            }
-            __syncwarp();
-            t += rows;
-            if (++j == cur.j1) {
-                done += rows;
-                if (!has_next) break;
-                cur = nxt;
-                j = cur.j0;
-            }
+            done += rows;
         }
         if (!ok && lane == 0) give_up(p.err, abort_flag);
         if (lane == 0) {  // every MMA this thread issued has finished before the TMEM is freed
@@ -467,6 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
                     if (!(ok = warp_wait(o_done, static_cast<uint32_t>((t - 1) & 1), abort_flag))) break;
                     tc_fence_after();
                 }
+                if (!kPTmem && j == it.j0) {  // the warp's rows may still leave for the previous segment
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                }
                 if constexpr (kPTmem) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
@@ -543,11 +530,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
-            // the warp's rows leave through its rows of the P buffer, 16 bytes a lane, whole rows
+            // The warp's rows leave through its rows of the P buffer, swizzled like P: by TMA when they are whole
+            // tokens, all of the item, else 16 bytes a lane, whole rows.
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < HD / 8; ++c)
                 *reinterpret_cast<uint4 *>(prow + (c >> 3) * kHalf + (((c & 7) ^ (r & 7)) << 4)) =
                     make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
+            if (quarter * 32 + 32 <= rows && p.store_tok > 0) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int half = 0; half < kHalves; ++half)
+                        tma_store_3d(&p.tm_o, half * 64, it.g * p.G, it.tok0 + h * p.tt + quarter * p.store_tok,
+                                     smem_addr(ptile + half * kHalf + quarter * 32 * 128));
+                    bulk_commit();
+                }
+                __syncwarp();
+                continue;
+            }
             __syncwarp();
 #pragma unroll 4
             for (int i = 0; i < HD / 8; ++i) {
@@ -562,6 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             }
             __syncwarp();  // the rows are read before the next tile's P overwrites them
         }
+        if (lane == 0) bulk_wait_all();  // the output stores are complete before the CTA exits
+        __syncwarp();
         if (!ok && lane == 0) give_up(p.err, abort_flag);
     }
     // ------------------------------------------------------------------------------------------
@@ -733,6 +737,9 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream) {
     if (!gather && (!encode(&prm.tm_k, a.k_cache, a.dtype, a.Hkv, a.D, krows, 1, R) ||
                     !encode(&prm.tm_v, a.v_cache, a.dtype, a.Hkv, a.D, krows, 1, R)))
         return cudaErrorInvalidValue;
+    // a warp's 32 output rows as one box, where they are whole tokens
+    prm.store_tok = 32 % prm.G == 0 && BM % prm.G == 0 ? 32 / prm.G : 0;
+    if (!encode(&prm.tm_o, a.out, a.dtype, a.Hq, a.D, a.total_q, prm.G, prm.store_tok > 0 ? prm.store_tok : 1)) return cudaErrorInvalidValue;
     prm.cu_q = a.cu_q;
     prm.ctx = a.ctx;
     prm.block_tables = a.block_tables;

@@ -31,6 +31,7 @@ struct PieceRec {
 
 struct ChunkParams {
     CUtensorMap tm_q, tm_k, tm_v;  // q: [total_q, Hq, D], boxes of `tt` tokens x G heads x 64
+    CUtensorMap tm_o;              // out, boxes of `store_tok` tokens (0: no boxes)
     const int32_t *cu_q, *ctx, *block_tables;
     const void *k_cache, *v_cache;
     void *out;
@@ -40,6 +41,7 @@ struct ChunkParams {
     int S, Hq, Hkv, G;
     int tt;        // tokens of a row tile
     int item_tok;  // tokens of an item
+    int store_tok;
     int max_blocks, num_blocks, total_q, max_seqlen_q, window, box_rows;
     uint32_t inv_g;  // 2^16 / G, rounded up: x inv_g >> 16 is x / G for x < 256
     BlockGeom geom;
