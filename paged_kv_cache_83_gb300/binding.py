@@ -145,14 +145,47 @@ def _stream(stream, ref: torch.Tensor) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _elsewhere(ref: torch.Tensor, *others) -> bool:
-    """Whether the call's device, ref's, is not the current one (the caller then makes it current
-    for the call). Raises when the tensors (None: not given) are on different devices."""
+_DTYPES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+
+
+def _device_of(ref: torch.Tensor, *others) -> int:
+    """The device of a call: all of its tensors (None: not given) have to be on one CUDA device."""
     dev = ref.get_device()
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be on one CUDA device")
-    return dev >= 0 and dev != torch._C._cuda_getDevice()
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return dev
+
+
+def _addr(t: torch.Tensor | None):
+    """The address of a tensor whose device has been checked."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _addr_i32(t: torch.Tensor, name: str) -> int:
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32")
+    return _addr(t)
+
+
+def _call(fn, name: str, dev: int, stream, args) -> None:
+    """Calls entry point `fn` with `args` and the stream (the current one of device `dev` if None), with that
+    device current."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else \
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status:
+        raise PagedAttnError(name, status)
 
 
 def _check(fn: str, status: int) -> None:
@@ -176,15 +209,12 @@ def pa_store_kv(k, v, k_cache, v_cache, slot_mapping, err=None, stream=None) -> 
         bs, Hkv, D, dt, _i32(err, "err"), _stream(stream, k)))
 
 
-def _token_stride(t: torch.Tensor, name: str) -> int:
-    """The elements between tokens of a [T, heads, D] tensor whose tokens may lie apart."""
-    if not t.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    T, H, D = t.shape
-    stride = t.stride()
-    if stride[2] != 1 or (stride[1] != D and H > 1):
+def _token_stride(t: torch.Tensor, T: int, H: int, D: int, name: str) -> int:
+    """The elements between tokens of a [T, H, D] tensor whose tokens may lie apart."""
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return stride[0] if T > 1 else H * D
+    return s[0] if T > 1 else H * D
 
 
 def rope_pair_axis(sections, interleaved: bool = False) -> bytes:
@@ -210,33 +240,34 @@ def pa_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
     projection's output); q_out may be q itself. pair_axis: bytes, the axis of each rotated pair
     (rope_pair_axis)."""
     NB, bs, Hkv, D = k_cache.shape
-    T, Hq, _ = q.shape
-    if q.shape[2] != D or q_out.shape != q.shape or k.shape != (T, Hkv, D) or v.shape != k.shape or \
-            v_cache.shape != k_cache.shape:
+    T, Hq, Dq = q.shape
+    kv = (T, Hkv, D)
+    if Dq != D or q_out.shape != q.shape or k.shape != kv or v.shape != kv or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch")
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    n_axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.shape[-1] != T or positions.dim() > 2:
+    pos_shape = positions.shape
+    if len(pos_shape) not in (1, 2) or pos_shape[-1] != T:
         raise ValueError("positions must be [T] or [axes, T]")
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2:
         raise TypeError("cos_sin must be a float32 [max_pos, rot_dim] table")
     max_pos, rot = cos_sin.shape
     if pair_axis is not None and (type(pair_axis) is not bytes or len(pair_axis) != rot // 2):
         raise ValueError("pair_axis must be rot_dim / 2 bytes")
-    if _elsewhere(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, err):
-        with torch.cuda.device(q.device):
-            return pa_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, pair_axis,
-                                    interleaved, err, stream)
     dtype = k_cache.dtype
-    dt = _dtype(k_cache)
-    if q.dtype != dtype or q_out.dtype != dtype or k.dtype != dtype or v.dtype != dtype or v_cache.dtype != dtype:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if q.dtype is not dtype or q_out.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype or \
+            v_cache.dtype is not dtype:
         raise TypeError("q, q_out, k, v and the pools must share a dtype")
-    _check("pa_rope_store_kv", load().pa_rope_store_kv(
-        q_out.data_ptr(), _token_stride(q_out, "q_out"), q.data_ptr(), _token_stride(q, "q"), k.data_ptr(),
-        _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"), _ptr(k_cache), _ptr(v_cache),
-        _i32(slot_mapping, "slot_mapping"), _i32(positions, "positions"), n_axes, pair_axis, _ptr(cos_sin),
-        max_pos, rot, int(bool(interleaved)), T, NB, bs, Hq, Hkv, D, dt, _i32(err, "err"), _stream(stream, q)))
+    dev = _device_of(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, err)
+    _call((_lib or load()).pa_rope_store_kv, "pa_rope_store_kv", dev, stream, (
+        q_out.data_ptr(), _token_stride(q_out, T, Hq, D, "q_out"), q.data_ptr(), _token_stride(q, T, Hq, D, "q"),
+        k.data_ptr(), _token_stride(k, T, Hkv, D, "k"), v.data_ptr(), _token_stride(v, T, Hkv, D, "v"), _addr(k_cache),
+        _addr(v_cache), _addr_i32(slot_mapping, "slot_mapping"), _addr_i32(positions, "positions"),
+        1 if len(pos_shape) == 1 else pos_shape[0], pair_axis, _addr(cos_sin), max_pos, rot, 1 if interleaved else 0, T, NB,
+        bs, Hq, Hkv, D, dt, None if err is None else _addr_i32(err, "err")))
 
 
 def pa_decode_workspace_size(B: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,
@@ -399,28 +430,27 @@ def pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_
     if Dq != D or out.shape != q.shape or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
             block_tables.shape[0] != S or context_lens.dim() != 1 or cu_seqlens_q.shape != (S + 1,):
         raise ValueError("shape mismatch")
-    if _elsewhere(q, out, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, workspace, err):
-        with torch.cuda.device(q.device):
-            return pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_seqlen_q,
-                                 scale, window, workspace, err, stream)
     dtype = q.dtype
-    dt = _dtype(q)
-    if out.dtype != dtype or k_cache.dtype != dtype or v_cache.dtype != dtype:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if out.dtype is not dtype or k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise TypeError("q, out and the pools must share a dtype")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("pa_chunk_attn", load().pa_chunk_attn(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _i32(block_tables, "block_tables"), block_tables.shape[1],
-        _i32(cu_seqlens_q, "cu_seqlens_q"), _i32(context_lens, "context_lens"), S, Tq, int(max_seqlen_q),
-        int(window), Hq, Hkv, D, bs, NB, float(scale), dt, _ptr(workspace), ws_bytes, _i32(err, "err"),
-        _stream(stream, q)))
+    dev = _device_of(q, out, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, workspace, err)
+    _call((_lib or load()).pa_chunk_attn, "pa_chunk_attn", dev, stream, (
+        _addr(out), _addr(q), _addr(k_cache), _addr(v_cache), _addr_i32(block_tables, "block_tables"),
+        block_tables.shape[1], _addr_i32(cu_seqlens_q, "cu_seqlens_q"), _addr_i32(context_lens, "context_lens"), S, Tq,
+        int(max_seqlen_q), int(window), Hq, Hkv, D, bs, NB, float(scale), dt, _addr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        None if err is None else _addr_i32(err, "err")))
 
 
 def _per_row(t: torch.Tensor | None, B: int, dtype, name: str):
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != (B,):
+    if t.dtype is not dtype or t.shape != (B,):
         raise TypeError(f"{name} must be {dtype} [B]")
-    return _ptr(t)
+    return _addr(t)
 
 
 _LOGITS = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
@@ -434,23 +464,19 @@ def pa_sample(tokens, logits, u=None, temperature=None, top_k=None, top_p=None, 
     B, V = logits.shape
     if tokens.shape != (B,):
         raise ValueError("tokens must be [B]")
-    if _elsewhere(logits, tokens, u, temperature, top_k, top_p, min_p, err):
-        with torch.cuda.device(logits.device):
-            return pa_sample(tokens, logits, u, temperature, top_k, top_p, min_p, err, stream)
     dt = _LOGITS.get(logits.dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {logits.dtype}")
-    if not logits.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
+    dev = _device_of(logits, tokens, u, temperature, top_k, top_p, min_p, err)
     s0, s1 = logits.stride()
     if s1 != 1 and V > 1:
         raise ValueError("a row of logits must be contiguous")
     f32 = torch.float32
-    _check("pa_sample", load().pa_sample(
-        _i32(tokens, "tokens"), logits.data_ptr(), s0 if B > 1 else V, B, V, dt, _per_row(u, B, f32, "u"),
+    _call((_lib or load()).pa_sample, "pa_sample", dev, stream, (
+        _addr_i32(tokens, "tokens"), logits.data_ptr(), s0 if B > 1 else V, B, V, dt, _per_row(u, B, f32, "u"),
         _per_row(temperature, B, f32, "temperature"), _per_row(top_k, B, torch.int32, "top_k"),
-        _per_row(top_p, B, f32, "top_p"), _per_row(min_p, B, f32, "min_p"), _i32(err, "err"),
-        _stream(stream, logits)))
+        _per_row(top_p, B, f32, "top_p"), _per_row(min_p, B, f32, "min_p"),
+        None if err is None else _addr_i32(err, "err")))
 
 
 # ---------------------------------------------------------------------------------------------
