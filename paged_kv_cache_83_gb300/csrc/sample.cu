@@ -102,24 +102,43 @@ __device__ __forceinline__ float octaves(const Heat &h, float x) {
     return __fmul_rn(__fadd_rn(x, -h.max), h.ch);
 }
 
-// The weight 2^(44 + (x - max) log2(e) / T) of x, by Dekker's pair arithmetic: the difference and its
-// rounding error (Knuth's two-sum), times the pair ch + cl; then 2^t = 2^n 2^(k/32) 2^y with |y| < 1/64
+// The weights 2^(44 + (x - max) log2(e) / T) of two logits, by Dekker's pair arithmetic: the difference and
+// its rounding error (Knuth's two-sum), times the pair ch + cl; then 2^t = 2^n 2^(k/32) 2^y with |y| < 1/64
 // and four terms of the exponential series in y ln 2 (the fifth is below 2^-39). Rounding to an
 // integer is the addition of 1.5 * 2^23, whose low bits then hold it. From 45 octaves below the
-// maximum on (x = -inf, a temperature near zero) the shift leaves nothing.
-__device__ __forceinline__ u64 weight(const Pow *pow, const Heat &h, float x) {
+// maximum on (x = -inf, a temperature near zero) the shift leaves nothing. The arithmetic before the table runs
+// on both numbers at a time (the packed fp32 instructions).
+__device__ __forceinline__ void weight2(const Pow *pow, const Heat &h, float x0, float x1, u64 &w0, u64 &w1) {
     constexpr float kRound = 12582912.f;
-    const float d = __fadd_rn(x, -h.max), th = fmaxf(__fmul_rn(d, h.ch), -60.f);
-    const float bb = __fadd_rn(d, -x);
-    const float e = __fadd_rn(__fadd_rn(x, -__fadd_rn(d, -bb)), __fadd_rn(-h.max, -bb));
-    const float tl = __fmaf_rn(d, h.ch, -th) + __fmaf_rn(d, h.cl, e * h.ch);
-    const float nr = __fadd_rn(th, kRound), f = __fadd_rn(th, -__fadd_rn(nr, -kRound));
-    const float kr = __fmaf_rn(f, 32.f, kRound), k = __fadd_rn(kr, -kRound);
-    const float y = __fmaf_rn(k, -1.f / 32.f, f) + tl;
-    const float q = y * __fmaf_rn(y, __fmaf_rn(y, __fmaf_rn(y, 9.618129e-3f, 5.550411e-2f), 2.4022651e-1f), 6.9314718e-1f);
-    const Pow w = pow[__float_as_uint(kr) & (kTable - 1)];
-    const uint32_t m = w.fixed + __float2int_rn(w.f * q);
-    return (static_cast<u64>(m) << (kFrac - 31)) >> ((__float_as_int(kRound) - __float_as_int(nr)) & 63);
+    const uint64_t x = f2_pack(x0, x1), neg_max = f2_pack(-h.max, -h.max), ch = f2_pack(h.ch, h.ch),
+                   cl = f2_pack(h.cl, h.cl), minus = f2_pack(-1.f, -1.f),
+                   up = f2_pack(kRound, kRound), down = f2_pack(-kRound, -kRound);
+    auto sub = [&](uint64_t a, uint64_t b) { return f2_fma(b, minus, a); };  // exact product: rounds once
+    const uint64_t d = f2_add(x, neg_max);
+    const uint64_t t = f2_mul(d, ch);
+    const uint64_t th = f2_pack(fmaxf(f2_lo(t), -60.f), fmaxf(f2_hi(t), -60.f));
+    const uint64_t bb = sub(d, x);
+    const uint64_t e = f2_add(sub(x, sub(d, bb)), sub(neg_max, bb));
+    const uint64_t lo = f2_add(f2_fma(d, ch, f2_mul(th, minus)), f2_fma(d, cl, f2_mul(e, ch)));
+    const uint64_t nr = f2_add(th, up), f = sub(th, f2_add(nr, down));
+    const uint64_t kr = f2_fma(f, f2_pack(32.f, 32.f), up), k = f2_add(kr, down);
+    const uint64_t y = f2_add(f2_fma(k, f2_pack(-1.f / 32.f, -1.f / 32.f), f), lo);
+    uint64_t q = f2_fma(y, f2_pack(9.618129e-3f, 9.618129e-3f), f2_pack(5.550411e-2f, 5.550411e-2f));
+    q = f2_fma(y, q, f2_pack(2.4022651e-1f, 2.4022651e-1f));
+    q = f2_fma(y, q, f2_pack(6.9314718e-1f, 6.9314718e-1f));
+    q = f2_mul(y, q);
+    auto finish = [&](float kr1, float nr1, float q1) {
+        const Pow w = pow[__float_as_uint(kr1) & (kTable - 1)];
+        const uint32_t m = w.fixed + __float2int_rn(w.f * q1);
+        return (static_cast<u64>(m) << (kFrac - 31)) >> ((__float_as_int(kRound) - __float_as_int(nr1)) & 63);
+    };
+    w0 = finish(f2_lo(kr), f2_lo(nr), f2_lo(q));
+    w1 = finish(f2_hi(kr), f2_hi(nr), f2_hi(q));
+}
+__device__ __forceinline__ u64 weight(const Pow *pow, const Heat &h, float x) {
+    u64 w, unused;
+    weight2(pow, h, x, x, w, unused);
+    return w;
 }
 
 template <class L>
@@ -238,6 +257,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
         // a stretch of the warp's elements per lane, then one stretch 32 elements at a time
         const int n = PW / 32;
         u64 s = 0;
+#pragma unroll 4
         for (int i = lane * n; i < lane * n + n; ++i) s += f(mine[i], base + i);
         auto scan = [&](u64 v) {
 #pragma unroll
@@ -365,7 +385,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
             if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) == -INFINITY) continue;
             u64 w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = weight(sh.pow, heat, x[e]);
+            for (int e = 0; e < 4; e += 2) weight2(sh.pow, heat, x[e], x[e + 1], w[e], w[e + 1]);
             fn(w, x);
         }
     };
@@ -451,11 +471,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
             if (tid == 0) sh.n_cand = 0;
             __syncthreads();
             auto add = [&](int b, u64 w) {
-#pragma unroll
-                for (int j = 0; j < kPieces; ++j) {
-                    const uint32_t part = static_cast<uint32_t>(w >> (j * kPieceBits)) & ((1u << kPieceBits) - 1);
-                    if (part) atomicAdd(&sh.hist[j][b], part);
-                }
+                constexpr uint32_t kMask = (1u << kPieceBits) - 1;
+                atomicAdd(&sh.hist[0][b], static_cast<uint32_t>(w) & kMask);
+                atomicAdd(&sh.hist[1][b], static_cast<uint32_t>(w >> kPieceBits) & kMask);
+                const uint32_t top = static_cast<uint32_t>(w >> (2 * kPieceBits));
+                if (top) atomicAdd(&sh.hist[2][b], top);
             };
             if (kUsed == 1 || level > 0) {
                 each(lo, hi, [&](float x, int) {
@@ -637,9 +657,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     // ---- the kept sum, and the token
     // no logit below this is kept: min-p's border with room for rounding
     const float from = fmaxf(tau, mp > 0.f ? heat.max + fminf((__log2f(fminf(mp, 1.f)) - 0.01f) / heat.ch, 0.f) : floor_x);
-    auto share = [&](float x, int at) {
-        if (!(x >= from) || !kept(x, at)) return static_cast<u64>(0);
-        const u64 w = weight(sh.pow, heat, x);
+    auto share = [&](float x, int at) {  // without branches, so that several run at a time
+        const u64 w = weight(sh.pow, heat, x >= from && kept(x, at) ? x : -INFINITY);
         return w >= least ? w : static_cast<u64>(0);
     };
     u64 m = 0;
