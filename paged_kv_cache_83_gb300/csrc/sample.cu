@@ -73,6 +73,7 @@ struct Shared {
     u64 mass[2][kMaxCluster];  // one CTA's partial sums each, written by that CTA
     u64 warp_mass[kWarps];
     u64 bcast[2][2];
+    u64 landed[kWarps];  // mbarriers: each warp's part of the row
     Candidate cand[kCandidates];  // this CTA's own; rank 0 then joins them in `joined`
     Candidate joined[kCandidates];
     u64 warp_max[kMaxCluster * kWarps];  // of every warp of the cluster: key of its maximum, and ...
@@ -141,20 +142,13 @@ __device__ __forceinline__ u64 weight(const Pow *pow, const Heat &h, float x) {
     return w;
 }
 
-template <class L>
-__device__ __forceinline__ void load16(const unsigned char *src, float (&f)[16 / sizeof(L)]);
-template <>
-__device__ __forceinline__ void load16<float>(const unsigned char *src, float (&f)[4]) {
-    const uint4 v = ldg_stream(src);
+// the elements of a 16-byte word
+__device__ __forceinline__ void split(const uint4 &v, float (&f)[4]) {
     f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
 }
-template <>
-__device__ __forceinline__ void load16<__half>(const unsigned char *src, float (&f)[8]) {
-    unpack8<F16>(ldg_stream(src), f);
-}
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const unsigned char *src, float (&f)[8]) {
-    unpack8<BF16>(ldg_stream(src), f);
+template <class L>
+__device__ __forceinline__ void split(const uint4 &v, float (&f)[8]) {
+    unpack8<std::conditional_t<std::is_same_v<L, __half>, F16, BF16>>(v, f);
 }
 
 template <class L>
@@ -170,6 +164,22 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     float *mine = vals + warp * PW;  // this warp's part of the row, in the row's order
     const int base = (rank * kWarps + warp) * PW;
 
+    // ---- The row into shared memory: one bulk copy a warp, of the whole 16-byte words that hold elements of the
+    // row. Element i of the held row is element i - skew of the row: rows may start off the 16-byte grid.
+    // 16-bit logits land in the upper half of the warp's part and spread over it from below.
+    constexpr int EV = 16 / static_cast<int>(sizeof(L));
+    const unsigned char *src = static_cast<const unsigned char *>(p.logits) + row * p.row_stride * static_cast<long long>(sizeof(L));
+    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(L));
+    src -= skew * sizeof(L);
+    const int end = p.V + skew, words = max(0, (min(PW, end - base) + EV - 1) / EV);
+    const unsigned char *raw = reinterpret_cast<unsigned char *>(mine) + (4 - sizeof(L)) * PW;
+    const uint32_t landed = smem_addr(&sh.landed[warp]);
+    if (lane == 0) {
+        mbar_init(landed, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(landed, words * 16);
+        if (words > 0) bulk_load(smem_addr(raw), src + static_cast<size_t>(base) * sizeof(L), words * 16, landed);
+    }
     if (tid < kTable) sh.pow[tid] = p.pow[tid];
     const float T = p.temperature ? __ldg(p.temperature + row) : 1.f;
     const bool greedy = !(T > 0.f);
@@ -180,20 +190,19 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
         sh.cl = sh.ch < FLT_MAX ? static_cast<float>(c - static_cast<double>(sh.ch)) : 0.f;
     }
 
-    // ---- the row into shared memory: whole 16-byte words, those that hold elements of the row.
-    // Element i of the held row is element i - skew of the row: rows may start off the 16-byte grid.
-    constexpr int EV = 16 / static_cast<int>(sizeof(L));
-    const unsigned char *src = static_cast<const unsigned char *>(p.logits) + row * p.row_stride * static_cast<long long>(sizeof(L));
-    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(L));
-    src -= skew * sizeof(L);
-    const int end = p.V + skew;
+    __syncwarp();
+    if (!mbar_wait(landed, 0)) raise_err(p.err, PA_DEVERR_TIMEOUT);
     float mx = -INFINITY;
     int mx_at = lane * EV;  // where in `mine` this lane's first word with its maximum lies
-#pragma unroll 4
-    for (int i = lane * EV; i < PW; i += 32 * EV) {
+#pragma unroll 2
+    for (int i0 = 0; i0 < PW; i0 += 32 * EV) {
+        const int i = i0 + lane * EV, at = base + i;
+        const bool in = i < PW;
         float f[EV];
-        const int at = base + i;
-        if (at < end) load16<L>(src + static_cast<size_t>(at) * sizeof(L), f);
+        if constexpr (EV == 4)
+            split(*reinterpret_cast<const uint4 *>(raw + (in ? i : 0) * sizeof(L)), f);
+        else
+            split<L>(*reinterpret_cast<const uint4 *>(raw + (in ? i : 0) * sizeof(L)), f);
         if (at < skew || at + EV > end) {  // the row's first and last word, and what lies behind
 #pragma unroll
             for (int e = 0; e < EV; ++e)
@@ -205,10 +214,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
             f[e] = fmaxf(f[e], -INFINITY) + 0.f;  // NaN is never chosen; -0 equals 0
             m = fmaxf(m, f[e]);
         }
-        if (m > mx) mx = m, mx_at = i;
+        if (in && m > mx) mx = m, mx_at = i;
+        __syncwarp();  // the words have been read before they are written over
+        if (in)
 #pragma unroll
-        for (int e = 0; e < EV; e += 4)
-            *reinterpret_cast<float4 *>(mine + i + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            for (int e = 0; e < EV; e += 4)
+                *reinterpret_cast<float4 *>(mine + i + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        if constexpr (EV > 4) __syncwarp();
     }
     cluster.sync();  // the table is set, and every CTA of the cluster runs before another writes to it
 
