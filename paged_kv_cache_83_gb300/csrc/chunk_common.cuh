@@ -50,6 +50,7 @@ struct ChunkParams {
 };
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
     const bool ok = mbar_wait(bar, parity) && !*abort_flag;
     const bool all = __all_sync(kFull, ok);
     __syncwarp();

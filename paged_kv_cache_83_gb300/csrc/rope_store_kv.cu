@@ -44,6 +44,15 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
     return v;
 }
 
+// 16-byte store; kStream: of data that will have left L2 before anyone reads it
+template <bool kStream>
+__device__ __forceinline__ void st_row(unsigned char *p, const uint4 &v) {
+    if constexpr (kStream)
+        __stcs(reinterpret_cast<uint4 *>(p), v);
+    else
+        stg128(p, v);
+}
+
 // two packed words of elements (x0 in a, x1 in b), two pairs, rotated in place
 template <class E>
 __device__ __forceinline__ void rotate_word(uint32_t &a, uint32_t &b, float c0, float s0, float c1, float s1) {
@@ -59,7 +68,7 @@ __device__ __forceinline__ void rotate_pair(uint32_t &w, float c, float s) {
 }
 
 // kRows head rows per thread, loaded together before any is stored.
-template <class E, int kRows, bool kPairs>
+template <class E, int kRows, bool kPairs, bool kStream>
 __global__ void __launch_bounds__(kRopeThreads) rope_store_kv_kernel(const __grid_constant__ RopeParams p) {
     const int per_token = p.units * p.row_par;
     const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -155,17 +164,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_store_kv_kernel(const __gri
             : is_v   ? p.v_cache + (static_cast<size_t>(slot) * p.Hkv + (r - p.Hq - p.Hkv)) * row_bytes
                      : p.k_cache + (static_cast<size_t>(slot) * p.Hkv + (r - p.Hq)) * row_bytes;
         const int a = is_v ? vo0 : o0, b = is_v ? vo1 : o1;
-        if (a < static_cast<int>(row_bytes)) stg128(dst + a, x0[i]);
-        if (b < static_cast<int>(row_bytes)) stg128(dst + b, x1[i]);
+        if (a < static_cast<int>(row_bytes)) st_row<kStream>(dst + a, x0[i]);
+        if (b < static_cast<int>(row_bytes)) st_row<kStream>(dst + b, x1[i]);
     }
 }
 
-template <class E, int kRows>
+template <class E, int kRows, bool kStream>
 cudaError_t launch_rope_typed(const RopeParams &prm, bool pairs, unsigned grid, cudaStream_t stream) {
     if (pairs)
-        rope_store_kv_kernel<E, kRows, true><<<grid, kRopeThreads, 0, stream>>>(prm);
+        rope_store_kv_kernel<E, kRows, true, kStream><<<grid, kRopeThreads, 0, stream>>>(prm);
     else
-        rope_store_kv_kernel<E, kRows, false><<<grid, kRopeThreads, 0, stream>>>(prm);
+        rope_store_kv_kernel<E, kRows, false, kStream><<<grid, kRopeThreads, 0, stream>>>(prm);
     return cudaGetLastError();
 }
 
@@ -195,19 +204,26 @@ cudaError_t launch_rope_store_kv(const RopeStoreArgs &a, cudaStream_t stream) {
     for (int i = 0; a.pair_axis && i < a.rot_dim / 2; ++i)
         prm.axis[i / 8] |= static_cast<uint32_t>(a.pair_axis[i]) << (4 * (i % 8));
     const int rows = a.Hq + 2 * a.Hkv;
-    // Four rows a thread once that still fills the SMs; one row a thread below, where the time is
-    // one chain of dependent loads and more threads shorten it.
+    // Four rows a thread once that still fills the SMs (33,673 tokens of 16/8 heads x 128: 84 us; with one, two
+    // or eight rows 93, 88 and 85); one row a thread below, where the time is one chain of dependent loads
+    // and more threads shorten it.
     constexpr int kMany = 4;
     const long long all = static_cast<long long>(a.T) * prm.units * rows;
     const bool many = all / kMany >= static_cast<long long>(device_sm_count()) * 1024;
     prm.row_par = many ? (rows + kMany - 1) / kMany : rows;
     const long long threads = static_cast<long long>(a.T) * prm.units * prm.row_par;
     const unsigned grid = static_cast<unsigned>((threads + kRopeThreads - 1) / kRopeThreads);
-    if (a.dtype == PA_BF16)
-        return many ? launch_rope_typed<BF16, kMany>(prm, a.interleaved, grid, stream)
-                    : launch_rope_typed<BF16, 1>(prm, a.interleaved, grid, stream);
-    return many ? launch_rope_typed<F16, kMany>(prm, a.interleaved, grid, stream)
-                : launch_rope_typed<F16, 1>(prm, a.interleaved, grid, stream);
+    // Above half of L2 what is written will have left it before it is read: stores that ask for no room
+    // there leave the row buffers to the reads (84 us against 96 at that size); below, the attention that
+    // follows finds the rows in L2.
+    const bool streamed = many && static_cast<long long>(a.T) * rows * a.D * 2 > (64ll << 20);
+    auto go = [&](auto e) {
+        using E = decltype(e);
+        if (streamed) return launch_rope_typed<E, kMany, true>(prm, a.interleaved, grid, stream);
+        return many ? launch_rope_typed<E, kMany, false>(prm, a.interleaved, grid, stream)
+                    : launch_rope_typed<E, 1, false>(prm, a.interleaved, grid, stream);
+    };
+    return a.dtype == PA_BF16 ? go(BF16{}) : go(F16{});
 }
 
 }  // namespace pa

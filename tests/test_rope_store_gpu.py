@@ -112,6 +112,8 @@ class Case:
     (3, 2, 2, 512, 256, 8, "bf16", {}),
     (2000, 16, 8, 128, 128, 256, "bf16", dict(pad=17)),     # several rows a thread
     (9001, 5, 1, 80, 80, 16, "f16", dict(fused=True)),
+    (9003, 16, 8, 128, 128, 256, "bf16", dict(fused=True, pad=5)),  # more than stays in L2
+    (8300, 16, 8, 128, 64, 16, "f16", dict(pairs=True)),
     (900, 32, 8, 64, 32, 16, "bf16", dict(pairs=True)),
     (77, 16, 8, 128, 128, 16, "bf16", dict(axes=3, pair_axis=pa.rope_pair_axis([16, 24, 24]))),
     (77, 16, 8, 128, 128, 16, "bf16", dict(axes=3, pair_axis=pa.rope_pair_axis([24, 20, 20], interleaved=True))),
