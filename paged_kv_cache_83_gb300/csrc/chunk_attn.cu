@@ -76,6 +76,11 @@ struct Layout {
     static constexpr size_t kPieceFloats = 256 * (HD + 2);
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b),
                  "r"(c), "r"(d)
@@ -425,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
                 }
                 float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 128; ++e) mq[e & 3] = fmaxf(mq[e & 3], __uint_as_float(sv[e]));
+                for (int e = 0; e < 128; e += 2)
+                    mq[(e >> 1) & 3] = max3(mq[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                 const float mraw = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
                 const float mx = mraw == -INFINITY ? -INFINITY : mraw * p.scale_log2;
                 // the reference moves only when the maximum grew by more than 2^8 (or was unset): the
@@ -514,19 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
                 continue;
             }
             const float inv = l > 0.f && !bad ? 1.f / l : 0.f;
-            uint32_t ov[HD / 2];
+            uint32_t acc[HD];
 #pragma unroll
-            for (int c = 0; c < HD / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld32(orow + c * 32, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    // bad: zero, whatever the accumulator holds
-                    const float a = bad ? 0.f : __uint_as_float(v[e]) * inv, b = bad ? 0.f : __uint_as_float(v[e + 1]) * inv;
-                    ov[c * 16 + (e >> 1)] = E::pack2(a, b);
-                }
-            }
+            for (int c = 0; c < HD / 32; ++c)
+                tmem_ld32(orow + c * 32, *reinterpret_cast<uint32_t(*)[32]>(acc + 32 * c));
+            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
@@ -536,8 +534,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < HD / 8; ++c)
+            {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)  // bad: zero, whatever the accumulator holds
+                    o[e] = bad ? 0u : E::pack2(__uint_as_float(acc[c * 8 + e * 2]) * inv, __uint_as_float(acc[c * 8 + e * 2 + 1]) * inv);
                 *reinterpret_cast<uint4 *>(prow + (c >> 3) * kHalf + (((c & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
             if (quarter * 32 + 32 <= rows && p.store_tok > 0) {
                 fence_proxy_async_smem();
                 __syncwarp();
