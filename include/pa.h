@@ -339,8 +339,8 @@ pa_status pa_prefill_varlen(void *out, const void *q, const void *k, const void 
  * max_seqlen_q  host int >= every q_len.
  * window        host int >= 0.
  * scale         positive: from FLT_MIN to FLT_MAX / 2 (masked scores are -infinity times it).
- * workspace     device scratch of at least pa_chunk_attn_workspace_size(S, Hq, Hkv, D) bytes (up to
- *               82 MB, by the SM count and D, not the lengths). Its contents on entry do not
+ * workspace     device scratch of at least pa_chunk_attn_workspace_size(S, Hq, Hkv, D) bytes (41 MB
+ *               on a GB300 at D = 128, 21 MB at 64: two pieces of 256 query rows per SM). Its contents on entry do not
  *               matter; calls that share a workspace must not overlap on the GPU.
  * Keys and values that no row of the chunk sees may hold anything, NaN included. Those that some
  * rows see and others do not have to be finite for the result of the others to be.

@@ -436,6 +436,8 @@ def pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_
         raise TypeError(f"unsupported dtype {dtype}")
     if out.dtype is not dtype or k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise TypeError("q, out and the pools must share a dtype")
+    if not (0 <= max_seqlen_q < 1 << 31 and 0 <= window < 1 << 31):
+        raise ValueError("max_seqlen_q and window must be from 0 to 2^31 - 1")
     dev = _device_of(q, out, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, workspace, err)
     _call((_lib or load()).pa_chunk_attn, "pa_chunk_attn", dev, stream, (
         _addr(out), _addr(q), _addr(k_cache), _addr(v_cache), _addr_i32(block_tables, "block_tables"),

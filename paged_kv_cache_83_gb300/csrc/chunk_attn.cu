@@ -615,10 +615,10 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
             for (int e = 0; e < 8; ++e) po[k][e] = 0.f;
             if (c <= rec.last_cta) {
                 const float *w = p.pieces + (static_cast<size_t>(c) * 2 + (c == first)) * Lay::kPieceFloats + r;
-                pm[k] = __ldg(w);
-                pl[k] = __ldg(w + 256);
+                pm[k] = __ldcg(w);  // written by the kernel this one was launched beside: not the read-only path
+                pl[k] = __ldcg(w + 256);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) po[k][e] = __ldg(w + 512 + (col + e) * 256);
+                for (int e = 0; e < 8; ++e) po[k][e] = __ldcg(w + 512 + (col + e) * 256);
             }
         }
         const float mn = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));

@@ -20,6 +20,9 @@
 //   warp 0      producer: Q of up to two segments, and the streams' K and V tiles in turn
 //   warps 1, 2  one MMA issuer per stream
 //   warps 4-7   softmax of stream A (tiles 0, 2, ... of a segment), warps 8-11 of stream B (1, 3, ...)
+// With 33 to 64 query rows the streams take half of the columns each instead, of every key tile: 64 scores
+// and 64 sums a thread do not fit the registers (3 drafts of 3-8 tokens, groups of 7, at 9-16k
+// contexts: 28 us against 22).
 //   TMEM columns: S_A, S_B, O_A, O_B of NT columns each; lanes are keys in S and head elements in O.
 #include <type_traits>
 
@@ -654,9 +657,9 @@ __global__ void __launch_bounds__(kJoinWork * kJoinGroups) chunk_narrow_join_ker
                 pm[k] = -INFINITY, pl[k] = 0.f, po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c <= rec.last_cta) {
                     const float *src = p.pieces + (static_cast<size_t>(c) * 2 + (c == first)) * Lay::kPieceFloats;
-                    pm[k] = __ldg(src + row);
-                    pl[k] = __ldg(src + Lay::kNC + row);
-                    po[k] = __ldg(reinterpret_cast<const float4 *>(src + 2 * Lay::kNC + row * HD + col));
+                    pm[k] = __ldcg(src + row);  // written by the kernel this one was launched beside: not the read-only path
+                    pl[k] = __ldcg(src + Lay::kNC + row);
+                    po[k] = __ldcg(reinterpret_cast<const float4 *>(src + 2 * Lay::kNC + row * HD + col));
                 }
             }
             const float mn = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));

@@ -165,6 +165,62 @@ def test_few_rows_growing_scores(Hq, Hkv, q):
         c.check()
 
 
+@pytest.mark.parametrize("q,Hq,Hkv,D", [(4, 4, 2, 64), (9, 14, 2, 128), (200, 8, 2, 128)])
+def test_a_query_that_is_not_finite_stays_alone(q, Hq, Hkv, D):
+    """NaN and infinities in one query row: every other row keeps its result."""
+    c = Case([(q, 1500), (2, 300)], Hq, Hkv, D, 16, "bf16", seed=7)
+    c.run()
+    torch.cuda.synchronize()
+    want = c.out.clone()
+    for value in (float("nan"), float("inf"), float("-inf")):
+        keep = c.q[1, 1].clone()
+        c.q[1, 1, 3:9] = value
+        c.out.fill_(7)
+        c.run()
+        torch.cuda.synchronize()
+        c.q[1, 1] = keep
+        same = torch.ones(c.Tq, Hq, dtype=torch.bool, device="cuda")
+        same[1, 1] = False
+        assert torch.equal(c.out[same], want[same])
+        assert not torch.isfinite(c.out[1, 1]).any()
+
+
+def test_keys_that_some_rows_do_not_see_may_be_nan():
+    """A key that is NaN reaches the rows that see it and no other (its value is finite)."""
+    for q, Hq, Hkv in ((4, 4, 2), (100, 8, 2)):
+        c = Case([(q, 700)], Hq, Hkv, 64, 16, "f16")
+        c.run()
+        torch.cuda.synchronize()
+        want = c.out.clone()
+        slot = int(c.bt[0, 699 // 16]) * 16 + 699 % 16
+        c.kc.view(-1, Hkv, 64)[slot] = float("nan")
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out[: q - 1], want[: q - 1])
+        assert torch.isnan(c.out[q - 1]).all()
+
+
+def test_a_cache_of_more_than_four_gigabytes():
+    """Slots whose byte offsets pass 2^32, by boxes and gathered row by row."""
+    for bs, q in ((16, 3), (16, 100), (4, 3)):
+        c = Case([(q, 1000)], 16, 8, 128, bs, "bf16")
+        nb = (5 << 30) // (bs * 8 * 128 * 2)
+        kc, vc = (torch.zeros(nb, bs, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        n = c.kc.shape[0]
+        kc[-n:], vc[-n:] = c.kc, c.vc
+        c.kc, c.vc = kc, vc
+        c.bt = torch.where((c.bt >= 0) & (c.bt < n), c.bt + nb - n, c.bt)
+        c.check()
+        assert int(c.err.item()) == 0
+
+
+def test_the_largest_group_and_lengths_that_fill_the_table():
+    c = Case([(8, 4096), (1, 4096), (8, 8)], 8, 1, 128, 256, "f16")
+    c.check()
+    c = Case([(64, 4096), (128, 4096), (65, 128)], 2, 2, 64, 256, "bf16")
+    c.check()
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, single tokens and drafts, empty ones among them."""
     r = np.random.default_rng(5)
