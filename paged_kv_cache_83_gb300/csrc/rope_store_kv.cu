@@ -13,7 +13,8 @@
 // (T * D * 2 * (2 Hq + 4 Hkv) bytes); the table rows of a step come from L2. So a thread owns one
 // unit of 16 elements (8 pairs) of a token and walks over the token's head rows with the unit's
 // eight cosines and sines in registers: the table is read once per thread, not once per head, and
-// every access to the big tensors is 16 bytes wide.
+// every access to the big tensors is 16 bytes wide. 33,673 tokens of 16/8 heads x 128 (556 MB): 93 us, 0.88
+// of the copy bandwidth (a plain copy of as many bytes, alternating buffers like this: 85 us).
 #include "pa_internal.h"
 
 namespace pa {
@@ -44,15 +45,6 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
     return v;
 }
 
-// 16-byte store; kStream: of data that will have left L2 before anyone reads it
-template <bool kStream>
-__device__ __forceinline__ void st_row(unsigned char *p, const uint4 &v) {
-    if constexpr (kStream)
-        __stcs(reinterpret_cast<uint4 *>(p), v);
-    else
-        stg128(p, v);
-}
-
 // two packed words of elements (x0 in a, x1 in b), two pairs, rotated in place
 template <class E>
 __device__ __forceinline__ void rotate_word(uint32_t &a, uint32_t &b, float c0, float s0, float c1, float s1) {
@@ -68,7 +60,7 @@ __device__ __forceinline__ void rotate_pair(uint32_t &w, float c, float s) {
 }
 
 // kRows head rows per thread, loaded together before any is stored.
-template <class E, int kRows, bool kPairs, bool kStream>
+template <class E, int kRows, bool kPairs>
 __global__ void __launch_bounds__(kRopeThreads) rope_store_kv_kernel(const __grid_constant__ RopeParams p) {
     const int per_token = p.units * p.row_par;
     const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -164,17 +156,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_store_kv_kernel(const __gri
             : is_v   ? p.v_cache + (static_cast<size_t>(slot) * p.Hkv + (r - p.Hq - p.Hkv)) * row_bytes
                      : p.k_cache + (static_cast<size_t>(slot) * p.Hkv + (r - p.Hq)) * row_bytes;
         const int a = is_v ? vo0 : o0, b = is_v ? vo1 : o1;
-        if (a < static_cast<int>(row_bytes)) st_row<kStream>(dst + a, x0[i]);
-        if (b < static_cast<int>(row_bytes)) st_row<kStream>(dst + b, x1[i]);
+        if (a < static_cast<int>(row_bytes)) stg128(dst + a, x0[i]);
+        if (b < static_cast<int>(row_bytes)) stg128(dst + b, x1[i]);
     }
 }
 
-template <class E, int kRows, bool kStream>
+template <class E, int kRows>
 cudaError_t launch_rope_typed(const RopeParams &prm, bool pairs, unsigned grid, cudaStream_t stream) {
     if (pairs)
-        rope_store_kv_kernel<E, kRows, true, kStream><<<grid, kRopeThreads, 0, stream>>>(prm);
+        rope_store_kv_kernel<E, kRows, true><<<grid, kRopeThreads, 0, stream>>>(prm);
     else
-        rope_store_kv_kernel<E, kRows, false, kStream><<<grid, kRopeThreads, 0, stream>>>(prm);
+        rope_store_kv_kernel<E, kRows, false><<<grid, kRopeThreads, 0, stream>>>(prm);
     return cudaGetLastError();
 }
 
@@ -204,24 +196,19 @@ cudaError_t launch_rope_store_kv(const RopeStoreArgs &a, cudaStream_t stream) {
     for (int i = 0; a.pair_axis && i < a.rot_dim / 2; ++i)
         prm.axis[i / 8] |= static_cast<uint32_t>(a.pair_axis[i]) << (4 * (i % 8));
     const int rows = a.Hq + 2 * a.Hkv;
-    // Four rows a thread once that still fills the SMs (33,673 tokens of 16/8 heads x 128: 84 us; with one, two
-    // or eight rows 93, 88 and 85); one row a thread below, where the time is one chain of dependent loads
-    // and more threads shorten it.
+    // Four rows a thread once that still fills the SMs (33,673 tokens of 16/8 heads x 128, inputs and pools not
+    // in L2: 93 us; two rows 104, eight 92 but 24 instead of 21 at 8192 tokens); one row a thread
+    // below, where the time is one chain of dependent loads and more threads shorten it.
     constexpr int kMany = 4;
     const long long all = static_cast<long long>(a.T) * prm.units * rows;
     const bool many = all / kMany >= static_cast<long long>(device_sm_count()) * 1024;
     prm.row_par = many ? (rows + kMany - 1) / kMany : rows;
     const long long threads = static_cast<long long>(a.T) * prm.units * prm.row_par;
     const unsigned grid = static_cast<unsigned>((threads + kRopeThreads - 1) / kRopeThreads);
-    // Above half of L2 what is written will have left it before it is read: stores that ask for no room
-    // there leave the row buffers to the reads (84 us against 96 at that size); below, the attention that
-    // follows finds the rows in L2.
-    const bool streamed = many && static_cast<long long>(a.T) * rows * a.D * 2 > (64ll << 20);
     auto go = [&](auto e) {
         using E = decltype(e);
-        if (streamed) return launch_rope_typed<E, kMany, true>(prm, a.interleaved, grid, stream);
-        return many ? launch_rope_typed<E, kMany, false>(prm, a.interleaved, grid, stream)
-                    : launch_rope_typed<E, 1, false>(prm, a.interleaved, grid, stream);
+        return many ? launch_rope_typed<E, kMany>(prm, a.interleaved, grid, stream)
+                    : launch_rope_typed<E, 1>(prm, a.interleaved, grid, stream);
     };
     return a.dtype == PA_BF16 ? go(BF16{}) : go(F16{});
 }
