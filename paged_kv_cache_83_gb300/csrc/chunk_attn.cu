@@ -743,7 +743,9 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     // a warp's 32 output rows as one box, where they are whole tokens
     prm.store_tok = 32 % prm.G == 0 && BM % prm.G == 0 ? 32 / prm.G : 0;
-    if (!encode(&prm.tm_o, a.out, a.dtype, a.Hq, a.D, a.total_q, prm.G, prm.store_tok > 0 ? prm.store_tok : 1)) return cudaErrorInvalidValue;
+    if (!narrow && prm.store_tok > 0 &&
+        !encode(&prm.tm_o, a.out, a.dtype, a.Hq, a.D, a.total_q, prm.G, prm.store_tok))
+        return cudaErrorInvalidValue;
     prm.cu_q = a.cu_q;
     prm.ctx = a.ctx;
     prm.block_tables = a.block_tables;

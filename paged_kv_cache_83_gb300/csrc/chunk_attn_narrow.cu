@@ -589,21 +589,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
                 tmem_ld<W>(oa + c0, a);
                 if (cnt_b > 0) tmem_ld<W>(ob + c0, b);
                 tmem_wait_ld();
-                if (d < HD) {
+                float o[W];
+#pragma unroll
+                for (int e = 0; e < W; e += 4) {
+                    const float4 fa = *reinterpret_cast<const float4 *>(wa + c0 + e);
+                    o[e] = __uint_as_float(a[e]) * fa.x, o[e + 1] = __uint_as_float(a[e + 1]) * fa.y;
+                    o[e + 2] = __uint_as_float(a[e + 2]) * fa.z, o[e + 3] = __uint_as_float(a[e + 3]) * fa.w;
+                }
+                if (cnt_b > 0)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) o[e] = fmaf(__uint_as_float(b[e]), wb[c0 + e], o[e]);
+                if (d >= HD) continue;
+                if (piece) {
+                    float *pc = piece + 2 * Lay::kNC + c0 * HD + d;  // columns behind the rows: room, never read
+#pragma unroll
+                    for (int e = 0; e < W; ++e) pc[e * HD] = o[e];
+                } else {
                     const int tk = p.div_g(c0);
                     int in_tok = c0 - tk * p.G;
-                    float *pc = piece + 2 * Lay::kNC + c0 * HD + d;
                     T *oc = out + (static_cast<size_t>(it.tok0 + tk) * p.Hq + it.g * p.G + in_tok) * HD + d;
 #pragma unroll
                     for (int e = 0; e < W; ++e) {
-                        if (c0 + e < rows) {
-                            float o = __uint_as_float(a[e]) * wa[c0 + e];
-                            if (cnt_b > 0) o = fmaf(__uint_as_float(b[e]), wb[c0 + e], o);
-                            if (piece)
-                                pc[e * HD] = o;
-                            else
-                                *oc = T(bad ? 0.f : o);
-                        }
+                        if (c0 + e < rows) *oc = T(bad ? 0.f : o[e]);
                         oc += HD;
                         if (++in_tok == p.G) in_tok = 0, oc += (p.Hq - p.G) * HD;
                     }
