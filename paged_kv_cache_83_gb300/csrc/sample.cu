@@ -192,6 +192,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     const float T = p.temperature ? __ldg(p.temperature + row) : 1.f;
     const bool greedy = !(T > 0.f);
     const int top_k = !greedy && p.top_k ? __ldg(p.top_k + row) : 0;
+    const float pp = p.top_p ? __ldg(p.top_p + row) : 1.f, mp = p.min_p ? __ldg(p.min_p + row) : 0.f;
+    const u64 least = mp > 0.f ? __float2ull_ru(fminf(mp, 1.f) * static_cast<float>(1ull << kFrac)) : 0;
+    const float u = p.u ? __ldg(p.u + row) : 0.f;
     if (tid == kTable) {  // one thread: there are few 64-bit units
         const double c = 1.4426950408889634 / static_cast<double>(greedy ? 1.f : T);
         sh.ch = static_cast<float>(fmin(c, static_cast<double>(FLT_MAX)));
@@ -253,15 +256,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     };
     auto plus = [](u64 a, u64 b) { return a + b; };
     auto sum = [&](u64 v) { return exchange(v, plus); };
-    // two values from one CTA (its lanes of one warp, `from` on one lane's authority) to all
+    // Two values from the one thread of the cluster with `from` to all (bcast[told ^ 1] afterwards); the lanes of
+    // its warp write to a CTA each.
     int told = 0;
-    auto tell = [&](bool from, u64 a, u64 b) {  // the caller's warp of `from` is converged
-        if (from)
-            for (int i = 0; i < CS; ++i) {
-                Shared *to = cluster.map_shared_rank(&sh, i);
+    auto tell = [&](bool from, u64 a, u64 b) {
+        const unsigned who = __ballot_sync(kAll, from);
+        if (who) {
+            a = __shfl_sync(kAll, a, __ffs(who) - 1);
+            b = __shfl_sync(kAll, b, __ffs(who) - 1);
+            if (lane < CS) {
+                Shared *to = cluster.map_shared_rank(&sh, lane);
                 to->bcast[told][0] = a;
                 to->bcast[told][1] = b;
             }
+        }
         cluster.sync();
         told ^= 1;
     };
@@ -421,16 +429,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     };
     auto join = [&]() {
         cluster.sync();
-        uint32_t n = 0, before_me = 0;
-        const int from = tid % CS;  // the CTA whose candidates this thread fetches
-        for (int i = 0; i < CS; ++i) {
-            const uint32_t c = cluster.map_shared_rank(&sh, i)->n_cand;
-            if (i < from) before_me += c;
-            n += c;
+        // lane i: the candidates of CTA i, and of those before it
+        const uint32_t c = lane < CS ? cluster.map_shared_rank(&sh, lane)->n_cand : 0;
+        uint32_t upto = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += t;
         }
+        const uint32_t n = __shfl_sync(kAll, upto, 31);
+        const int from = tid % CS;  // the CTA whose candidates this thread fetches
+        const uint32_t before_me = __shfl_sync(kAll, upto - c, from), theirs = __shfl_sync(kAll, c, from);
         if (rank == 0 && n <= kCandidates) {
             const Shared *other = cluster.map_shared_rank(&sh, from);
-            for (uint32_t j = tid / CS; j < other->n_cand; j += kSampleThreads / CS)
+            for (uint32_t j = tid / CS; j < theirs; j += kSampleThreads / CS)
                 sh.joined[before_me + j] = other->cand[j];
             __syncthreads();
         }
@@ -628,9 +640,6 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
         const u64 f = __float2ull_rz(x * 18446744073709551616.f);
         return __umul64hi(f, m) + (f * m != 0);
     };
-    const float pp = p.top_p ? __ldg(p.top_p + row) : 1.f, mp = p.min_p ? __ldg(p.min_p + row) : 0.f;
-    const u64 least = mp > 0.f ? __float2ull_ru(fminf(mp, 1.f) * static_cast<float>(1ull << kFrac)) : 0;
-    const float u = p.u ? __ldg(p.u + row) : 0.f;
     auto target_of = [&](u64 whole) { return u >= 1.f ? whole - 1 : u > 0.f ? down(u, whole) : 0; };
     // kept by top-p while the sum before a token is below pp of the whole
     auto want_of = [&](u64 whole) { return max(up(fmaxf(pp, 0.f), whole), 1ull); };
