@@ -127,6 +127,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     }
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
 
+    // Launched beside what precedes it in the stream: nothing that it wrote is read, and nothing that it reads is
+    // written, before it has finished (the set-up above takes place meanwhile).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     plan_share(p, plan, share);
     zero_bad_sequences<T, HD>(p);
     if (tid == 0) p.recs[blockIdx.x].valid = 0;
@@ -599,6 +602,8 @@ constexpr int kJoinThreads = kJoinRows * (kJoinCols / 8);
 template <class E, int HD>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
     using Lay = Layout<HD>;
+    // the next call's kernel may set itself up beside this one: it waits for this grid itself
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PieceRec rec = p.recs[blockIdx.x];
     if (!rec.valid) return;
@@ -699,19 +704,23 @@ cudaError_t launch_typed(const ChunkParams &prm, cudaStream_t stream) {
         configured[dev] = 1;
     }
     const unsigned P = device_sm_count();
-    kern<<<P, kThreads, Layout<HD>::kSmem, stream>>>(prm);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // the joining kernel is on the SMs when the last share ends (programmatic dependent launch)
+    // Both kernels are launched beside what precedes them (programmatic dependent launch): the set-up of the first
+    // overlaps the end of the call before, and the second is on the SMs when the last share ends.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    const int rows = prm.max_seqlen_q > prm.tt ? 256 : (prm.max_seqlen_q * prm.G + kJoinRows - 1) / kJoinRows * kJoinRows;
-    cfg.gridDim = dim3(P, rows / kJoinRows, HD / kJoinCols);
-    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3(P);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<HD>::kSmem;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, prm)) != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
+    const int rows = prm.max_seqlen_q > prm.tt ? 256 : (prm.max_seqlen_q * prm.G + kJoinRows - 1) / kJoinRows * kJoinRows;
+    cfg.gridDim = dim3(P, rows / kJoinRows, HD / kJoinCols);
+    cfg.blockDim = dim3(kJoinThreads);
     return cudaLaunchKernelEx(&cfg, chunk_join_kernel<E, HD>, prm);
 }
 

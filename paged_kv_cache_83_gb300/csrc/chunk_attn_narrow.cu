@@ -143,9 +143,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         *abort_flag = 0;
         for (int i = 0; i < kBadRing; ++i) bad_seg[i] = 0;
         for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(fl + Lay::kFloats)[i] = 0;  // votes
-        p.recs[blockIdx.x].valid = 0;
     }
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), Lay::kTmem);
+    // Launched beside what precedes it in the stream: nothing that it wrote is read, and nothing that it reads is
+    // written, before it has finished (the set-up above takes place meanwhile).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) p.recs[blockIdx.x].valid = 0;
     plan_share(p, plan, share);
     zero_bad_sequences<T, HD>(p);
     tc_fence_before();
@@ -645,6 +648,8 @@ template <class E, int HD, int NT, bool kCols>
 __global__ void __launch_bounds__(kJoinWork * kJoinGroups) chunk_narrow_join_kernel(const __grid_constant__ ChunkParams p) {
     using Lay = Narrow<HD, NT, kCols>;
     __shared__ float part[kJoinGroups][6][kJoinWork];
+    // the next call's kernel may set itself up beside this one: it waits for this grid itself
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PieceRec rec = p.recs[blockIdx.x];
     if (!rec.valid) return;
@@ -722,17 +727,20 @@ cudaError_t launch_typed(const ChunkParams &prm, cudaStream_t stream) {
         configured[dev] = 1;
     }
     const unsigned P = device_sm_count();
-    kern<<<P, kThreads, Lay::kSmem, stream>>>(prm);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(P, (prm.max_seqlen_q * prm.G * (HD / 4) + kJoinWork - 1) / kJoinWork);
-    cfg.blockDim = dim3(kJoinWork * kJoinGroups);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3(P);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay::kSmem;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, prm)) != cudaSuccess) return e;  // as in chunk_attn.cu
+    cfg.dynamicSmemBytes = 0;
+    cfg.gridDim = dim3(P, (prm.max_seqlen_q * prm.G * (HD / 4) + kJoinWork - 1) / kJoinWork);
+    cfg.blockDim = dim3(kJoinWork * kJoinGroups);
     return cudaLaunchKernelEx(&cfg, chunk_narrow_join_kernel<E, HD, NT, kCols>, prm);
 }
 

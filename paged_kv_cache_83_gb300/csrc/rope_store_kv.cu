@@ -62,6 +62,7 @@ __device__ __forceinline__ void rotate_pair(uint32_t &w, float c, float s) {
 // kRows head rows per thread, loaded together before any is stored.
 template <class E, int kRows, bool kPairs>
 __global__ void __launch_bounds__(kRopeThreads) rope_store_kv_kernel(const __grid_constant__ RopeParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");  // the attention's set-up may run beside this grid
     const int per_token = p.units * p.row_par;
     const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
     const int t = static_cast<int>(idx / per_token);
