@@ -7,6 +7,8 @@ instructions and the sums inside them off by at most 2^-22 of sum |q k| scale, 1
 and so the output by 2 e_s A; the fp32 sums over n keys, the base-2 exponential and the sum of
 weights by (n / 16 + 16) 2^-22 A; the output is rounded once, u |out|.
 """
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -331,3 +333,81 @@ def test_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     a.check(run=False)
     b.check(run=False)
+
+
+def mixed_cases():
+    """Calls of every kind: few and many rows, pages that tile a box and pages that do not, windows, long caches."""
+    r = np.random.default_rng(11)
+    cases = []
+    for i in range(24):
+        Hkv, G = int(r.choice([1, 2, 8])), int(r.integers(1, 9))
+        most = int(r.choice([1, 4, 8, 30, 100, 400]))
+        new = [int(n) for n in r.integers(1, most + 1, r.choice([1, 3, 10]))]
+        lens = [(n, max(n, int(r.integers(1, 4000)))) for n in new]
+        cases.append(Case(lens, G * Hkv, Hkv, int(r.choice([64, 128])), int(r.choice([4, 16, 64, 256])),
+                          str(r.choice(["f16", "bf16"])), window=int(r.choice([0, 0, 200])), seed=i))
+    return cases
+
+
+def test_calls_in_a_row_share_a_workspace():
+    # on one stream, with nothing between: the set-up of a call overlaps the end of the one before it
+    cases = mixed_cases()
+    ws = max((c.ws for c in cases), key=lambda t: t.numel())
+    for c in cases:
+        c.ws = ws
+        c.check()
+        c.want = c.out.clone()
+    r = np.random.default_rng(12)
+    for _ in range(20):
+        for c in cases:
+            c.out.fill_(7)
+        for i in r.permutation(len(cases)):
+            cases[i].run()
+        torch.cuda.synchronize()
+        for c in cases:
+            assert torch.equal(c.out, c.want)
+            assert int(c.err.item()) == 0
+
+
+def test_an_input_written_by_the_work_before():
+    # the queries, the lengths and the page table come from kernels queued directly before the call
+    c = Case([(4, 900), (1, 77), (7, 3000)], 16, 8, 128, 16, "bf16", seed=3)
+    c.check()
+    want, q, ctx, bt = c.out.clone(), c.q.clone(), c.ctx.clone(), c.bt.clone()
+    for _ in range(20):
+        c.q.zero_(), c.ctx.zero_(), c.bt.fill_(0), c.out.fill_(7)
+        torch.cuda.synchronize()
+        c.bt.copy_(bt), c.ctx.copy_(ctx), c.q.copy_(q)
+        c.run()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, want)
+
+
+def test_calls_from_threads():
+    cases = mixed_cases()[:8]
+    for c in cases:
+        c.check()
+        c.want = c.out.clone()
+        c.out.fill_(7)
+    torch.cuda.synchronize()
+
+    def work(c):
+        stream = torch.cuda.Stream()
+        for _ in range(20):
+            c.run(stream=stream.cuda_stream)
+        stream.synchronize()
+
+    with ThreadPoolExecutor(len(cases)) as ex:
+        list(ex.map(work, cases))
+    for c in cases:
+        assert torch.equal(c.out, c.want)
+        assert int(c.err.item()) == 0
+
+
+def test_the_first_call_of_a_thread():
+    # nothing has bound a context to the thread before
+    c = Case([(4, 900), (300, 1200)], 16, 8, 128, 16, "bf16", seed=4)
+    stream = torch.cuda.current_stream().cuda_stream
+    with ThreadPoolExecutor(1) as ex:
+        ex.submit(c.run, stream=stream).result()
+    c.check(run=False)

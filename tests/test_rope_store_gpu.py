@@ -6,6 +6,8 @@ type. The two products and their sum are each off by at most 2^-24 of their size
 smallest subnormal below the normal range). Values, unrotated elements and everything that is not
 written are compared bit for bit.
 """
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -200,6 +202,19 @@ def test_captured_and_on_another_stream():
     pa.pa_rope_store_kv(c.q_out, c.q, c.k, c.v, c.kc, c.vc, c.slots, c.pos, c.table, stream=side)
     side.synchronize()
     assert torch.equal(c.q_out, want_q)
+
+
+def test_the_first_call_of_a_thread():
+    c = Case(57, 16, 8, 128, 128, 16, "bf16", fused=True)
+    c.check()
+    want = c.q_out.clone()
+    c.q_out.zero_()
+    torch.cuda.synchronize()
+    stream = torch.cuda.current_stream().cuda_stream
+    with ThreadPoolExecutor(1) as ex:
+        ex.submit(pa.pa_rope_store_kv, c.q_out, c.q, c.k, c.v, c.kc, c.vc, c.slots, c.pos, c.table, stream=stream).result()
+    torch.cuda.synchronize()
+    assert torch.equal(c.q_out, want)
 
 
 def test_slots_behind_two_gigabytes():

@@ -5,6 +5,8 @@ running sum (the weights' errors are below 2^-31 of themselves and independent),
 probability below N^1.5 2^-31 / N = sqrt(N) 2^-31 a row, 2^-22 at the largest vocabulary here; a top-p border moves
 the choice with less. At borders that are hit on purpose (equal weights) both sides are exact.
 """
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -229,6 +231,21 @@ def test_captured_and_on_another_stream():
     torch.cuda.synchronize()
     pa.pa_sample(tokens, x, u, top_p=p, stream=side)
     side.synchronize()
+    assert torch.equal(tokens, want)
+
+
+def test_the_first_call_of_a_thread():
+    x = model_logits(33, 40000, 6).half()
+    tokens, u = torch.zeros(33, dtype=torch.int32, device="cuda"), torch.rand(33, device="cuda")
+    pa.pa_sample(tokens, x, u)
+    torch.cuda.synchronize()
+    want = tokens.clone()
+    tokens.zero_()
+    torch.cuda.synchronize()
+    stream = torch.cuda.current_stream().cuda_stream
+    with ThreadPoolExecutor(1) as ex:
+        ex.submit(pa.pa_sample, tokens, x, u, stream=stream).result()
+    torch.cuda.synchronize()
     assert torch.equal(tokens, want)
 
 
