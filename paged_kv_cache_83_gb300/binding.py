@@ -8,9 +8,13 @@ fallback: if the library is missing or a call fails, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 from pathlib import Path
 
 import torch
+
+from .build import args_path
 
 PKG = Path(__file__).resolve().parent
 LIB_PATH = PKG / "_build" / "libpagedattn.so"
@@ -26,6 +30,7 @@ EXPORTS = ("pa_store_kv", "pa_rope_store_kv", "pa_decode_workspace_size", "pa_de
 PA_DECODE_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 _lib = None
+_args = None
 
 
 class PagedAttnError(RuntimeError):
@@ -101,6 +106,21 @@ def load(path: Path | str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+def _load_args():
+    """The module that checks the arguments of the calls where microseconds count, bound to the library (csrc/args.cpp)."""
+    global _args
+    lib, path = load(), args_path()
+    if not path.exists():
+        raise RuntimeError(f"{path} is missing: build it with paged_kv_cache_83_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("pa_args", str(path))
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_args", loader))
+    loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+               for name in ("pa_rope_store_kv", "pa_chunk_attn", "pa_sample")))
+    _args = mod
+    return mod
+
+
 def pa_decode_debug_tail_units(workspace, B: int, Hq: int, Hkv: int, D: int,
                                max_blocks_per_seq: int, block_size: int) -> int:
     """Diagnostics: the dynamic-tail units the last completed pa_decode / pa_store_decode launch on
@@ -145,49 +165,6 @@ def _stream(stream, ref: torch.Tensor) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-_DTYPES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
-
-
-def _device_of(ref: torch.Tensor, *others) -> int:
-    """The device of a call: all of its tensors (None: not given) have to be on one CUDA device."""
-    dev = ref.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on one CUDA device")
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    return dev
-
-
-def _addr(t: torch.Tensor | None):
-    """The address of a tensor whose device has been checked."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
-
-
-def _addr_i32(t: torch.Tensor, name: str) -> int:
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name} must be int32")
-    return _addr(t)
-
-
-def _call(fn, name: str, dev: int, stream, args) -> None:
-    """Calls entry point `fn` with `args` and the stream (the current one of device `dev` if None), with that
-    device current."""
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else \
-        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev == torch._C._cuda_getDevice():
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status:
-        raise PagedAttnError(name, status)
-
-
 def _check(fn: str, status: int) -> None:
     if status != 0:
         raise PagedAttnError(fn, status)
@@ -207,14 +184,6 @@ def pa_store_kv(k, v, k_cache, v_cache, slot_mapping, err=None, stream=None) -> 
     _check("pa_store_kv", load().pa_store_kv(
         _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _i32(slot_mapping, "slot_mapping"), T, NB,
         bs, Hkv, D, dt, _i32(err, "err"), _stream(stream, k)))
-
-
-def _token_stride(t: torch.Tensor, T: int, H: int, D: int, name: str) -> int:
-    """The elements between tokens of a [T, H, D] tensor whose tokens may lie apart."""
-    s = t.stride()
-    if s[2] != 1 or (s[1] != D and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if T > 1 else H * D
 
 
 def rope_pair_axis(sections, interleaved: bool = False) -> bytes:
@@ -239,35 +208,10 @@ def pa_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
     slot_mapping [T]. q, q_out, k and v may be views whose tokens lie apart (slices of one
     projection's output); q_out may be q itself. pair_axis: bytes, the axis of each rotated pair
     (rope_pair_axis)."""
-    NB, bs, Hkv, D = k_cache.shape
-    T, Hq, Dq = q.shape
-    kv = (T, Hkv, D)
-    if Dq != D or q_out.shape != q.shape or k.shape != kv or v.shape != kv or v_cache.shape != k_cache.shape:
-        raise ValueError("shape mismatch")
-    if slot_mapping.shape != (T,):
-        raise ValueError("slot_mapping must be [T]")
-    pos_shape = positions.shape
-    if len(pos_shape) not in (1, 2) or pos_shape[-1] != T:
-        raise ValueError("positions must be [T] or [axes, T]")
-    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2:
-        raise TypeError("cos_sin must be a float32 [max_pos, rot_dim] table")
-    max_pos, rot = cos_sin.shape
-    if pair_axis is not None and (type(pair_axis) is not bytes or len(pair_axis) != rot // 2):
-        raise ValueError("pair_axis must be rot_dim / 2 bytes")
-    dtype = k_cache.dtype
-    dt = _DTYPES.get(dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    if q.dtype is not dtype or q_out.dtype is not dtype or k.dtype is not dtype or v.dtype is not dtype or \
-            v_cache.dtype is not dtype:
-        raise TypeError("q, q_out, k, v and the pools must share a dtype")
-    dev = _device_of(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, err)
-    _call((_lib or load()).pa_rope_store_kv, "pa_rope_store_kv", dev, stream, (
-        q_out.data_ptr(), _token_stride(q_out, T, Hq, D, "q_out"), q.data_ptr(), _token_stride(q, T, Hq, D, "q"),
-        k.data_ptr(), _token_stride(k, T, Hkv, D, "k"), v.data_ptr(), _token_stride(v, T, Hkv, D, "v"), _addr(k_cache),
-        _addr(v_cache), _addr_i32(slot_mapping, "slot_mapping"), _addr_i32(positions, "positions"),
-        1 if len(pos_shape) == 1 else pos_shape[0], pair_axis, _addr(cos_sin), max_pos, rot, 1 if interleaved else 0, T, NB,
-        bs, Hq, Hkv, D, dt, None if err is None else _addr_i32(err, "err")))
+    status = (_args or _load_args()).pa_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                                                      pair_axis, interleaved, err, stream)
+    if status:
+        raise PagedAttnError("pa_rope_store_kv", status)
 
 
 def pa_decode_workspace_size(B: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,
@@ -424,38 +368,10 @@ def pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_
     """Causal attention of a chunk of new tokens of each sequence over its paged cache: out, q
     [Tq, Hq, D]; sequence s has rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] at the last positions of its
     context_lens[s] keys. window > 0: a token sees its last `window` keys only."""
-    NB, bs, Hkv, D = k_cache.shape
-    Tq, Hq, Dq = q.shape
-    S = context_lens.shape[0]
-    if Dq != D or out.shape != q.shape or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
-            block_tables.shape[0] != S or context_lens.dim() != 1 or cu_seqlens_q.shape != (S + 1,):
-        raise ValueError("shape mismatch")
-    dtype = q.dtype
-    dt = _DTYPES.get(dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    if out.dtype is not dtype or k_cache.dtype is not dtype or v_cache.dtype is not dtype:
-        raise TypeError("q, out and the pools must share a dtype")
-    if not (0 <= max_seqlen_q < 1 << 31 and 0 <= window < 1 << 31):
-        raise ValueError("max_seqlen_q and window must be from 0 to 2^31 - 1")
-    dev = _device_of(q, out, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, workspace, err)
-    _call((_lib or load()).pa_chunk_attn, "pa_chunk_attn", dev, stream, (
-        _addr(out), _addr(q), _addr(k_cache), _addr(v_cache), _addr_i32(block_tables, "block_tables"),
-        block_tables.shape[1], _addr_i32(cu_seqlens_q, "cu_seqlens_q"), _addr_i32(context_lens, "context_lens"), S, Tq,
-        int(max_seqlen_q), int(window), Hq, Hkv, D, bs, NB, float(scale), dt, _addr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        None if err is None else _addr_i32(err, "err")))
-
-
-def _per_row(t: torch.Tensor | None, B: int, dtype, name: str):
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != (B,):
-        raise TypeError(f"{name} must be {dtype} [B]")
-    return _addr(t)
-
-
-_LOGITS = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
+    status = (_args or _load_args()).pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens,
+                                                   max_seqlen_q, scale, window, workspace, err, stream)
+    if status:
+        raise PagedAttnError("pa_chunk_attn", status)
 
 
 def pa_sample(tokens, logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None, err=None,
@@ -463,22 +379,9 @@ def pa_sample(tokens, logits, u=None, temperature=None, top_k=None, top_p=None, 
     """One token per row of logits [B, V] (rows may lie apart) into tokens [B] int32, from the given
     uniform numbers u [B]; temperature, top_k (int32), top_p, min_p: one per row, or None for 1 and
     no truncation. A row with temperature 0 takes its largest logit; u may be None when all do."""
-    B, V = logits.shape
-    if tokens.shape != (B,):
-        raise ValueError("tokens must be [B]")
-    dt = _LOGITS.get(logits.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {logits.dtype}")
-    dev = _device_of(logits, tokens, u, temperature, top_k, top_p, min_p, err)
-    s0, s1 = logits.stride()
-    if s1 != 1 and V > 1:
-        raise ValueError("a row of logits must be contiguous")
-    f32 = torch.float32
-    _call((_lib or load()).pa_sample, "pa_sample", dev, stream, (
-        _addr_i32(tokens, "tokens"), logits.data_ptr(), s0 if B > 1 else V, B, V, dt, _per_row(u, B, f32, "u"),
-        _per_row(temperature, B, f32, "temperature"), _per_row(top_k, B, torch.int32, "top_k"),
-        _per_row(top_p, B, f32, "top_p"), _per_row(min_p, B, f32, "min_p"),
-        None if err is None else _addr_i32(err, "err")))
+    status = (_args or _load_args()).pa_sample(tokens, logits, u, temperature, top_k, top_p, min_p, err, stream)
+    if status:
+        raise PagedAttnError("pa_sample", status)
 
 
 # ---------------------------------------------------------------------------------------------

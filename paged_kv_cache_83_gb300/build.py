@@ -2,7 +2,8 @@
 
 Each translation unit is compiled in parallel, then the objects are linked into one shared
 library that exports the C ABI of ``include/pa.h``. The runtime is linked shared, so a process
-that already loaded PyTorch's CUDA runtime uses that one instance.
+that already loaded PyTorch's CUDA runtime uses that one instance. The binding's argument checks
+(``csrc/args.cpp``) become an extension module for the installed PyTorch and Python.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -43,6 +45,30 @@ def _stale(out: Path, deps: list[Path]) -> bool:
     return any(d.stat().st_mtime > t for d in deps)
 
 
+def args_path() -> Path:
+    """The extension module of csrc/args.cpp; a name of its own for each PyTorch and Python."""
+    import torch
+    return BUILD / f"pa_args-{torch.__version__}-{sys.implementation.cache_tag}.so"
+
+
+def _build_args(headers: list[Path], force: bool) -> None:
+    src, out = CSRC / "args.cpp", args_path()
+    if not (force or _stale(out, [src] + headers)):
+        return
+    import torch
+    home = Path(torch.__file__).resolve().parent
+    tmp = out.with_suffix(f".{os.getpid()}.tmp")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-isystem{home / 'include'}",
+           f"-isystem{home / 'include' / 'torch' / 'csrc' / 'api' / 'include'}",
+           f"-isystem{sysconfig.get_paths()['include']}", f"-isystem{cuda_home() / 'include'}", str(src), "-o", str(tmp),
+           f"-L{home / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{home / 'lib'}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {src.name}:\n{r.stderr}")
+    os.replace(tmp, out)
+
+
 def build(verbose: bool = False, force: bool = False) -> Path:
     BUILD.mkdir(parents=True, exist_ok=True)
     headers = list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + [ROOT / "include" / "pa.h"]
@@ -63,8 +89,10 @@ def build(verbose: bool = False, force: bool = False) -> Path:
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        args = ex.submit(_build_args, headers, force)
         objs = list(ex.map(compile_one, srcs))
+        args.result()
     if force or _stale(LIB, objs):
         tmp = LIB.with_suffix(f".{os.getpid()}.tmp")
         libdir = cuda_home() / "lib64"

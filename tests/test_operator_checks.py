@@ -180,3 +180,55 @@ def test_sample_binding_refusals():
         pa.pa_sample(t[:2], x)
     with pytest.raises(TypeError):
         pa.pa_sample(t, x.double())
+
+
+def test_binding_refuses_other_types():
+    q = torch.zeros(3, 4, 64, dtype=torch.float16)
+    k, pool = q[:, :2].contiguous(), torch.zeros(2, 16, 2, 64, dtype=torch.float16)
+    idx, table = torch.zeros(3, dtype=torch.int32), torch.zeros(8, 64)
+    rope = [q, q, k, k, pool, pool, idx, idx, table]
+    for i in range(len(rope)):
+        with pytest.raises(TypeError):
+            pa.pa_rope_store_kv(*rope[:i], None, *rope[i + 1:])
+        with pytest.raises(ValueError):              # a dimension too many
+            pa.pa_rope_store_kv(*rope[:i], rope[i][None, None], *rope[i + 1:]) if i != 8 else \
+                pa.pa_rope_store_kv(*rope[:3], k[None], *rope[4:])
+    for i in (6, 7):
+        with pytest.raises(TypeError):
+            pa.pa_rope_store_kv(*rope[:i], idx.long(), *rope[i + 1:])
+    with pytest.raises(TypeError):
+        pa.pa_rope_store_kv(*rope, err=torch.zeros(1))
+    with pytest.raises(TypeError):
+        pa.pa_rope_store_kv(*rope, err=3)
+
+
+def test_chunk_attn_binding_refuses_numbers():
+    q, pool = torch.zeros(6, 4, 64, dtype=torch.float16), torch.zeros(2, 16, 2, 64, dtype=torch.float16)
+    bt, cu, ctx = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    args = [q, q, pool, pool, bt, cu, ctx]
+    for mq, window in ((-1, 0), (1 << 31, 0), (3, -1), (3, 1 << 31)):
+        with pytest.raises(ValueError):
+            pa.pa_chunk_attn(*args, mq, 0.125, window)
+    with pytest.raises((TypeError, OverflowError)):
+        pa.pa_chunk_attn(*args, 1 << 80, 0.125)
+    for mq, scale in (("3", 0.125), (3.5, 0.125), (3, "0.125")):
+        with pytest.raises(TypeError):
+            pa.pa_chunk_attn(*args, mq, scale)
+    for i in range(len(args)):
+        with pytest.raises(TypeError):
+            pa.pa_chunk_attn(*args[:i], None, *args[i + 1:], 3, 0.125)
+    for i in (4, 5, 6):
+        with pytest.raises(TypeError):
+            pa.pa_chunk_attn(*args[:i], args[i].long(), *args[i + 1:], 3, 0.125)
+
+
+def test_sample_binding_refuses_settings():
+    x, t = torch.zeros(3, 50), torch.zeros(3, dtype=torch.int32)
+    for bad in (dict(u=torch.zeros(2)), dict(u=torch.zeros(3).double()), dict(temperature=torch.zeros(3, 1)), dict(top_k=torch.zeros(3)),
+                dict(top_p=t), dict(min_p=0.5), dict(err=torch.zeros(1))):
+        with pytest.raises(TypeError):
+            pa.pa_sample(t, x, **bad)
+    with pytest.raises(TypeError):
+        pa.pa_sample(t.long(), x)
+    with pytest.raises(ValueError):
+        pa.pa_sample(t, x[0])
