@@ -13,7 +13,7 @@
 // (T * D * 2 * (2 Hq + 4 Hkv) bytes); the table rows of a step come from L2. So a thread owns one
 // unit of 16 elements (8 pairs) of a token and walks over the token's head rows with the unit's
 // eight cosines and sines in registers: the table is read once per thread, not once per head, and
-// every access to the big tensors is 16 bytes wide. 33,673 tokens of 16/8 heads x 128 (556 MB): 93 us, 0.88
+// every access to the big tensors is 16 bytes wide. 33,673 tokens of 16/8 heads x 128 (556 MB): 90 us, 0.91
 // of the copy bandwidth (a plain copy of as many bytes, alternating buffers like this: 85 us).
 #include "pa_internal.h"
 
@@ -22,6 +22,7 @@ namespace pa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBlocks = 4;     // on an SM: 64 registers a thread (33,673 tokens: 90 us, at 94 registers 116, at 80 94)
 constexpr int kRopeMaxUnits = 16;  // rot_dim <= 256
 
 struct RopeParams {
@@ -61,7 +62,7 @@ __device__ __forceinline__ void rotate_pair(uint32_t &w, float c, float s) {
 
 // kRows head rows per thread, loaded together before any is stored.
 template <class E, int kRows, bool kPairs>
-__global__ void __launch_bounds__(kRopeThreads) rope_store_kv_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_store_kv_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;");  // the attention's set-up may run beside this grid
     const int per_token = p.units * p.row_par;
     const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -197,19 +198,23 @@ cudaError_t launch_rope_store_kv(const RopeStoreArgs &a, cudaStream_t stream) {
     for (int i = 0; a.pair_axis && i < a.rot_dim / 2; ++i)
         prm.axis[i / 8] |= static_cast<uint32_t>(a.pair_axis[i]) << (4 * (i % 8));
     const int rows = a.Hq + 2 * a.Hkv;
-    // Four rows a thread once that still fills the SMs (33,673 tokens of 16/8 heads x 128, inputs and pools not
-    // in L2: 93 us; two rows 104, eight 92 but 24 instead of 21 at 8192 tokens); one row a thread
-    // below, where the time is one chain of dependent loads and more threads shorten it.
-    constexpr int kMany = 4;
+    // One row a thread while the SMs hold all threads at once: the time is one chain of dependent loads, and more
+    // threads shorten it (256 tokens of 16/8 heads x 128: 2.6 us, four rows 3.4; 600 tokens: 3.6 and 4.3). Beyond
+    // that three or four rows, as leaves fewer of the last thread's without work (inputs and pools not in L2:
+    // 800 tokens 5.2 us, one row 5.7; 1000: 6.0 and 6.9; 33,673: four rows 90, three 95, two 105. 9001 tokens of
+    // 14/2 heads x 64, so 18 rows: three rows 13.2, four 14.9, two 14.4, one 19.1).
     const long long all = static_cast<long long>(a.T) * prm.units * rows;
-    const bool many = all / kMany >= static_cast<long long>(device_sm_count()) * 1024;
-    prm.row_par = many ? (rows + kMany - 1) / kMany : rows;
+    int each = 1;
+    if (all > static_cast<long long>(device_sm_count()) * kRopeThreads * kRopeBlocks)
+        each = (rows + 3) / 4 * 4 <= (rows + 2) / 3 * 3 ? 4 : 3;
+    prm.row_par = (rows + each - 1) / each;
     const long long threads = static_cast<long long>(a.T) * prm.units * prm.row_par;
     const unsigned grid = static_cast<unsigned>((threads + kRopeThreads - 1) / kRopeThreads);
     auto go = [&](auto e) {
         using E = decltype(e);
-        return many ? launch_rope_typed<E, kMany>(prm, a.interleaved, grid, stream)
-                    : launch_rope_typed<E, 1>(prm, a.interleaved, grid, stream);
+        return each == 4   ? launch_rope_typed<E, 4>(prm, a.interleaved, grid, stream)
+               : each == 3 ? launch_rope_typed<E, 3>(prm, a.interleaved, grid, stream)
+                           : launch_rope_typed<E, 1>(prm, a.interleaved, grid, stream);
     };
     return a.dtype == PA_BF16 ? go(BF16{}) : go(F16{});
 }

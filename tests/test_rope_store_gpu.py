@@ -183,6 +183,20 @@ def test_empty_step():
     assert torch.equal(c.kc, kc)
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,kw", [
+    (9001, 14, 2, 64, 64, dict(fused=True, axes=3, pad=7)),  # three rows a thread, none left over
+    (4999, 3, 1, 128, 64, dict(pairs=True, pad=3)),          # five rows by threes
+    (3500, 5, 1, 128, 128, {}),                              # seven rows by fours
+    (2500, 16, 8, 128, 96, dict(axes=2)),                    # four, none left over
+    (700, 64, 1, 256, 256, {}),                              # 66: three
+    (160000, 1, 1, 16, 16, dict(pairs=True)),            # three rows: one thread a token
+])
+def test_many_tokens(T, Hq, Hkv, D, rot, kw):
+    c = Case(T, Hq, Hkv, D, rot, 16, "bf16", **kw)
+    c.check()
+    assert int(c.err.item()) == 0
+
+
 def test_captured_and_on_another_stream():
     c = Case(57, 16, 8, 128, 128, 16, "bf16", fused=True)
     c.check()
