@@ -73,9 +73,27 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_store_kv_kerne
     const long long slot = __ldg(p.slot_mapping + t);
     if (slot < 0) return;  // padding: nothing of this token is read or written
     bool bad_pos = false;
-    for (int a = 0; a < p.n_axes; ++a)
-        bad_pos |= static_cast<unsigned>(__ldg(p.positions + static_cast<size_t>(a) * p.T + t)) >=
-                   static_cast<unsigned>(p.max_pos);
+    // The positions of the token's axes stay in registers for the table rows (9001 tokens on three axes: 13.2 -> 11.9
+    // us), where registers are left: with four rows a thread they spill (33,673 tokens: 90 -> 93 us).
+    constexpr bool kHold = kRows < 4;
+    const auto load_pos = [&](uint32_t a) { return __ldg(p.positions + static_cast<size_t>(a) * p.T + t); };
+    int pos[4];  // of each axis; those that are not there hold the first's
+    if constexpr (kHold) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            pos[a] = a == 0 || a < p.n_axes ? load_pos(a) : pos[0];
+            bad_pos |= static_cast<unsigned>(pos[a]) >= static_cast<unsigned>(p.max_pos);
+        }
+    } else {
+        for (int a = 0; a < p.n_axes; ++a)
+            bad_pos |= static_cast<unsigned>(load_pos(a)) >= static_cast<unsigned>(p.max_pos);
+    }
+    const auto pos_of = [&](uint32_t a) {  // a < 4
+        if constexpr (kHold)
+            return a & 2u ? a & 1u ? pos[3] : pos[2] : a & 1u ? pos[1] : pos[0];
+        else
+            return load_pos(a);
+    };
     if (slot >= p.num_slots || bad_pos) {
         if (in_token == 0)
             raise_err(p.err, (slot >= p.num_slots ? PA_DEVERR_SLOT : 0) | (bad_pos ? PA_DEVERR_POSITION : 0));
@@ -115,17 +133,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_store_kv_kerne
         const int half = p.rot / 2;
         if (axes == (axes & 15u) * 0x11111111u) {
             // one position for the unit: four 16-byte loads
-            const int pos = __ldg(p.positions + static_cast<size_t>(axes & 15u) * p.T + t);
-            const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + static_cast<size_t>(pos) * p.rot + u * 8);
-            const float4 *srow = reinterpret_cast<const float4 *>(p.cos_sin + static_cast<size_t>(pos) * p.rot + half + u * 8);
+            const float4 *row =
+                reinterpret_cast<const float4 *>(p.cos_sin + static_cast<size_t>(pos_of(axes & 3u)) * p.rot + u * 8);
+            const float4 *srow = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(row) + half);
             const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(srow), s1 = __ldg(srow + 1);
             c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
             s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int pos = __ldg(p.positions + static_cast<size_t>((axes >> (4 * e)) & 15u) * p.T + t);
-                const float *row = p.cos_sin + static_cast<size_t>(pos) * p.rot + u * 8 + e;
+                const float *row = p.cos_sin + static_cast<size_t>(pos_of((axes >> (4 * e)) & 3u)) * p.rot + u * 8 + e;
                 c[e] = __ldg(row);
                 s[e] = __ldg(row + half);
             }
@@ -202,7 +219,7 @@ cudaError_t launch_rope_store_kv(const RopeStoreArgs &a, cudaStream_t stream) {
     // threads shorten it (256 tokens of 16/8 heads x 128: 2.6 us, four rows 3.4; 600 tokens: 3.6 and 4.3). Beyond
     // that three or four rows, as leaves fewer of the last thread's without work (inputs and pools not in L2:
     // 800 tokens 5.2 us, one row 5.7; 1000: 6.0 and 6.9; 33,673: four rows 90, three 95, two 105. 9001 tokens of
-    // 14/2 heads x 64, so 18 rows: three rows 13.2, four 14.9, two 14.4, one 19.1).
+    // 14/2 heads x 64, so 18 rows: three rows 13.2, four 14.9, two 14.4, one 19.1, before positions were held).
     const long long all = static_cast<long long>(a.T) * prm.units * rows;
     int each = 1;
     if (all > static_cast<long long>(device_sm_count()) * kRopeThreads * kRopeBlocks)
