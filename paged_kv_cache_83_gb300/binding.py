@@ -2,8 +2,10 @@
 
 Each function takes torch CUDA tensors, checks their dtype / shape / contiguity, and calls the
 entry point of the same name in ``_build/libpagedattn.so`` with raw device pointers and the
-current CUDA stream. Every step of the computation runs in the library's kernels; there is no
-fallback: if the library is missing or a call fails, these functions raise.
+current CUDA stream; those of rotation, chunk attention and sampling do so in an extension module
+(``csrc/args.cpp``), since a call of theirs takes a few microseconds. Every step of the computation
+runs in the library's kernels; there is no fallback: if the library is missing or a call fails, these
+functions raise.
 """
 from __future__ import annotations
 

@@ -3,7 +3,8 @@
 //
 // The kernel of a decode step's rotation takes 2 us. Its eleven tensors checked in Python and 27 arguments passed
 // through ctypes made the call 10.4 us (4 tokens) and 11.1 us (256 tokens), back to back; checked here it is 4.1 us for
-// both. A draft's attention of two launches went from 12.5 to 8.9 us, where its kernels bound it.
+// both. A draft's attention of two launches went from 12.5 to 8.9 us, where its kernels
+// bound it.
 // Each function takes the tensors and settings of the binding's function of the same name, all of them and
 // in that order, raises TypeError or ValueError for what does not fit, and returns the entry point's status.
 // The entry points are those of the loaded library: bind() takes their addresses. No C++ exception leaves
@@ -116,8 +117,8 @@ cudaStream_t stream_of(PyObject *o, int dev) {
         PyObject *d = PyLong_FromLong(dev);
         v = d ? PyObject_CallOneArg(current_raw_stream, d) : nullptr;
         Py_XDECREF(d);
-    } else if (PyLong_Check(o)) {
-        v = Py_NewRef(o);
+    } else if (PyIndex_Check(o)) {
+        v = PyNumber_Index(o);
     } else {
         v = PyObject_GetAttrString(o, "cuda_stream");
     }
@@ -128,7 +129,6 @@ cudaStream_t stream_of(PyObject *o, int dev) {
     return reinterpret_cast<cudaStream_t>(raw);
 }
 
-// call() with `dev` current, and without the interpreter's lock
 // the status of call(), made with `dev` current and without the interpreter's lock
 template <class F>
 PyObject *run(int dev, F call) {

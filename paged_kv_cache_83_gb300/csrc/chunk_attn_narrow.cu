@@ -11,7 +11,7 @@
 // in each thread until the segment ends.
 //
 // Bound by HBM: every key and value is read once per kv head (2.2 GB for 256 drafts of up to 5 tokens
-// over contexts to 4096 take 354 us, 0.92 of the copy bandwidth; with 128-row tiles 684 us). The
+// over contexts to 4096 take 352 us, 0.93 of the copy bandwidth; with 128-row tiles 684 us). The
 // loads run ahead in rings of tiles; two streams of softmax warps take the key tiles in
 // turn, each with its own maximum, sum and accumulator, so that one computes while the other waits
 // for its matrix products. They join at the end of a segment.
