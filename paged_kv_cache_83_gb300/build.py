@@ -21,6 +21,9 @@ CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIB = BUILD / "libpagedattn.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+FAST_MATH = ["--use_fast_math"]
+# Subnormal logits have an order, which flushing them to zero would lose.
+EXACT_MATH = {"sample.cu"}
 
 
 def nvcc() -> str:
@@ -73,14 +76,15 @@ def build(verbose: bool = False, force: bool = False) -> Path:
     BUILD.mkdir(parents=True, exist_ok=True)
     headers = list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + [ROOT / "include" / "pa.h"]
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
-                    f"-I{ROOT / 'include'}", "--use_fast_math"]
+                    f"-I{ROOT / 'include'}"]
     if verbose:
         flags += ["-Xptxas", "-v"]
 
     def compile_one(src: Path) -> Path:
         obj = BUILD / (src.stem + ".o")
         if force or _stale(obj, [src] + headers):
-            cmd = [nvcc(), *flags, "-c", str(src), "-o", str(obj)]
+            math = [] if src.name in EXACT_MATH else FAST_MATH
+            cmd = [nvcc(), *flags, *math, "-c", str(src), "-o", str(obj)]
             r = subprocess.run(cmd, capture_output=True, text=True)
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {src.name}:\n{r.stderr}")

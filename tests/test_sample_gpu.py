@@ -251,3 +251,44 @@ def test_the_first_call_of_a_thread():
 
 def test_empty_batch():
     pa.pa_sample(torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(0, 10, device="cuda"))
+
+
+def test_subnormal_logits():
+    """Logits below the smallest normal number, of either sign and among zeros, are ordered like any others: at
+    temperature 1 all weights are equal (to 2^-126), so that top-k's and top-p's choice is that order alone."""
+    r = np.random.default_rng(21)
+    small = r.integers(-3000, 3001, (8, 700))
+    for x in (torch.tensor([[-1.0, 1e-39, 2e-39, 0.0, -0.0]] * 8),
+              torch.from_numpy(small * 2.0 ** -149).float(),
+              torch.from_numpy(np.clip(small, -120, 120) * 2.0 ** -133).bfloat16(),
+              torch.from_numpy(np.clip(small, -900, 900) * 2.0 ** -24).half()):
+        u = r.uniform(0, 1, 8)
+        x = x.cuda()
+        check(x, temperature=0.0)
+        for k in (1, 2, 40, 650):
+            check(x, top_k=k, u=u)
+        check(x, top_p=0.3, u=u)
+        check(x, top_k=500, top_p=0.5, u=u)
+
+
+@pytest.mark.parametrize("T", [2.0 ** -149, 7 * 2.0 ** -149, 1e-40, 2.0 ** -126, 1e-30, 2.0 ** -63, (1 - 2.0 ** -24) * 2.0 ** -62, 2.0 ** -62,
+                               2.0 ** -60])
+def test_cold_temperatures(T):
+    """Logits a few temperatures apart, and equal ones, at temperatures whose inverse fp32 does not hold."""
+    r = np.random.default_rng(22)
+    step = r.integers(-40, 1, (12, 300)).astype(np.float64)
+    u = np.linspace(0.02, 0.98, 12)
+    for x in (step * T, (step + 17) * T, np.where(step < -2, -np.inf, step * T), np.where(step == -1, 1.0, step * T),
+              np.where(step < -3, -1e30, 0.75), np.where(step < -3, 1e-6, 2e-6)):
+        x = torch.from_numpy(x).float().cuda()
+        check(x, temperature=T, u=u)
+        check(x, temperature=T, top_k=5, u=u)
+        check(x, temperature=T, top_p=0.6, u=u)
+        check(x, temperature=T, top_k=90, top_p=0.9, min_p=0.04, u=u)
+
+
+def test_hot_temperatures():
+    x = torch.from_numpy(np.random.default_rng(23).normal(0, 2.0 ** 100, (12, 300))).float().cuda()
+    u = np.linspace(0.02, 0.98, 12)
+    for kw in ({}, dict(top_k=7), dict(top_p=0.4), dict(min_p=0.2)):
+        check(x, temperature=2.0 ** 100, u=u, **kw)
