@@ -379,8 +379,8 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
  * u             fp32 [B], uniform in [0, 1); NaN and values below 0 count as 0, values from 1 on
  *               choose the last kept token with weight. May be NULL where every row is greedy (0).
  * temperature, top_k, top_p, min_p  [B] each (top_k int32, the others fp32); NULL: 1, none, none, none.
- * Weights are exact to about 2^-31 of themselves (at temperatures above 2^100, and for logits more than
- * FLT_MAX apart, to about 2^-20) and held as multiples of 2^-44 of the largest
+ * Weights are exact to about 2^-31 of themselves (to about 2^-20 at temperatures above 2^100, and none for a
+ * logit more than FLT_MAX below the largest) and held as multiples of 2^-44 of the largest
  * (smaller ones count as zero); their sums are integers, so the tokens do not depend on how the
  * work is divided. Subnormal logits and temperatures count as what they are. Supported: 1 <= V <= 262144. B == 0 is a no-op. Reads the logits once.
  */

@@ -758,24 +758,24 @@ cudaError_t launch_typed(const SampleArgs &a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto divide = [&](int ctas) {
-        const int held = a.V + 16 / static_cast<int>(sizeof(L)) - 1;  // the row and the skew of its start
+    auto divide = [&](int V, int ctas) {
+        const int held = V + 16 / static_cast<int>(sizeof(L)) - 1;  // the row and the skew of its start
         prm.per_warp = (held + ctas * kWarps * 32 - 1) / (ctas * kWarps * 32) * 32;
         attr[0].val.clusterDim.x = ctas;
         cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ctas);
         cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(kWarps) * prm.per_warp * 4;
     };
-    divide(CS);
-    if (few) {  // clusters of sixteen, where the device has room for one (asked once)
+    if (few) {  // clusters of sixteen, where the device has room for one with the longest rows (asked once)
         if (sixteen[dev] == 0) {
             int n = 0;
-            divide(16);
+            divide(kSampleMaxVocab, 16);
             e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
             if (e != cudaSuccess) cudaGetLastError();  // that answer is not the launch's
             sixteen[dev] = e == cudaSuccess && n > 0 ? 1 : -1;
         }
-        divide(sixteen[dev] > 0 ? 16 : CS);
+        if (sixteen[dev] > 0) CS = 16;
     }
+    divide(a.V, CS);
     return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 

@@ -292,3 +292,76 @@ def test_hot_temperatures():
     u = np.linspace(0.02, 0.98, 12)
     for kw in ({}, dict(top_k=7), dict(top_p=0.4), dict(min_p=0.2)):
         check(x, temperature=2.0 ** 100, u=u, **kw)
+
+
+def kinds(B, r):
+    """Settings of B rows: greedy, top-k of few and of many, top-p, min-p and their combinations, plain."""
+    i = np.arange(B) % 8
+    return dict(temperature=np.where(i == 0, 0.0, r.uniform(0.3, 2.0, B)),
+                top_k=np.where(np.isin(i, (1, 4)), r.integers(1, 200, B), np.where(i == 6, r.integers(300, 20000, B), 0)),
+                top_p=np.where(np.isin(i, (2, 4, 7)), r.uniform(0.05, 0.999, B), 1.0),
+                min_p=np.where(np.isin(i, (5, 6, 7)), r.uniform(0.001, 0.3, B), 0.0), u=r.uniform(0, 1, B))
+
+
+def check_in_parts(x, n, **kw):
+    """check(), n rows a call: few long rows take wider clusters than many do."""
+    for b in range(0, x.shape[0], n):
+        check(x[b:b + n], **{k: np.broadcast_to(np.asarray(v), x.shape[:1])[b:b + n] for k, v in kw.items()})
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("V", [32768, 32769, 50257, 151936, 262144])
+@pytest.mark.parametrize("n", [1, 4, 5])
+def test_few_long_rows(n, V, dt):
+    r = np.random.default_rng(V + n)
+    check_in_parts(model_logits(8, V, V + 1).to(DT[dt]), n, **kinds(8, r))
+
+
+@pytest.mark.parametrize("dt,V,stride,offset", [("f32", 40001, 40003, 3), ("f16", 50257, 50261, 5), ("bf16", 151935, 151943, 1)])
+def test_few_long_rows_off_the_grid(dt, V, stride, offset):
+    flat = torch.full((offset + 8 * stride + 64,), 1000.0, device="cuda").to(DT[dt])
+    x = flat[offset:offset + 8 * stride].view(8, stride)[:, :V]
+    x.copy_(model_logits(8, V, 13).to(DT[dt]))
+    for n in (1, 3):
+        check_in_parts(x, n, **kinds(8, np.random.default_rng(n)))
+
+
+@pytest.mark.parametrize("n", [1, 2])
+def test_few_long_rows_of_equals(n):
+    """Borders among equal logits that lie in every CTA of the cluster."""
+    V = 100003
+    u = np.array([0, 0.25, 0.999, 1 / 3])
+    x = torch.zeros(4, V, device="cuda")
+    z = torch.randint(-2, 3, (4, V), device="cuda").float()
+    for y in (x, z):
+        check_in_parts(y, n, u=u)
+        check_in_parts(y, n, temperature=0.0)
+        for k in (1, 2, 255, 700, 30000, V - 1, V, V + 1):
+            check_in_parts(y, n, top_k=k, u=u)
+        for p in (1e-9, 0.25, 0.6, 0.999999):
+            check_in_parts(y, n, top_p=p, u=u)
+            check_in_parts(y, n, top_p=p, top_k=9000, u=u)
+        check_in_parts(y, n, min_p=1.0, u=u)
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_few_long_flat_tails(n):
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = 0.05 * torch.randn(4, 200000, generator=g, device="cuda")
+    u = np.random.default_rng(31).uniform(0, 1, 4)
+    check_in_parts(x, n, u=u)
+    check_in_parts(x, n, top_p=0.9, u=u)
+    check_in_parts(x, n, top_k=70001, top_p=0.5, min_p=0.9, u=u)
+
+
+def test_few_long_rows_with_nothing_left():
+    inf, nan = float("inf"), float("nan")
+    x = model_logits(6, 90000, 14)
+    x[0, :] = -inf
+    x[1, :] = nan
+    x[2, 1:] = nan
+    x[3, [5, 40000, 89999]] = inf
+    x[4, :-1] = -inf
+    for kw in ({}, dict(temperature=0.0), dict(top_k=3), dict(top_p=0.9), dict(top_k=200, top_p=0.5, min_p=0.01)):
+        check_in_parts(x, 1, u=0.6, **kw)
+        check_in_parts(x, 3, u=0.6, **kw)
