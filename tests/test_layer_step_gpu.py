@@ -124,3 +124,204 @@ def test_prompts_in_chunks_then_drafts_then_single_tokens(Hq, Hkv, D, bs, dt):
     pa.pa_prefill_varlen(out, q, None, None, kc, vc, cu, cu, len(ids), len(ids), bt, Hkv=Hkv, scale=D ** -0.5)
     torch.cuda.synchronize()
     assert float((out.double() - m.attention(ids, 0)).abs().max()) <= tol
+
+
+class Overlap:
+    """A rotation of several waves and the attention that reads its queries and pool rows, with nothing between
+    the two calls: the attention's kernels may start while the rotation's last blocks run."""
+
+    def __init__(self, form, D, bs, dt, seed):
+        # query rows a kv head: whole chunks (128-row tiles), or up to 16, 32 and 64
+        Hq, Hkv, q, S = {"wide": (16, 8, 700, 16), "rows16": (16, 8, 8, 1400), "rows32": (8, 2, 8, 1400),
+                         "rows64": (8, 1, 8, 1400)}[form]
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = np.random.default_rng(seed)
+        ctx = q + r.integers(0, 60, S)
+        used = -(-ctx // bs)
+        nb = int(used.sum()) + 2
+        ids = r.permutation(nb)
+        bt = np.zeros((S, used.max()), np.int64)
+        slots, pos, at = [], [], 0
+        for s in range(S):
+            bt[s, :used[s]] = ids[at:at + used[s]]
+            at += used[s]
+            p = np.arange(ctx[s] - q, ctx[s])
+            slots.append(bt[s, p // bs] * bs + p % bs)
+            pos.append(p)
+        i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.slots, self.pos, self.bt, self.ctx = i32(np.concatenate(slots)), i32(np.concatenate(pos)), i32(bt), i32(ctx)
+        self.cu = i32(np.arange(S + 1) * q)
+        n, self.most, self.scale = S * q, q, D ** -0.5
+        x = torch.randn(n, Hq + 2 * Hkv, D, generator=g, device="cuda").to(dt)
+        self.qkv = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+        self.base = [torch.randn(nb, bs, Hkv, D, generator=g, device="cuda").to(dt) for _ in range(2)]
+        for pool in self.base:
+            pool.view(-1, Hkv, D)[self.slots.long()] = float("nan")
+        self.pools = [torch.empty_like(p) for p in self.base]
+        self.q = torch.empty(n, Hq, D, dtype=dt, device="cuda")
+        self.out = torch.empty_like(self.q)
+        self.table = table(1024, D)
+        self.ws = torch.empty(pa.pa_chunk_attn_workspace_size(S, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def poison(self):
+        for pool, base in zip(self.pools, self.base):
+            pool.copy_(base)
+        self.q.fill_(float("nan"))
+        self.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    def rotate(self):
+        pa.pa_rope_store_kv(self.q, *self.qkv, *self.pools, self.slots, self.pos, self.table, err=self.err)
+
+    def attend(self):
+        pa.pa_chunk_attn(self.out, self.q, *self.pools, self.bt, self.cu, self.ctx, self.most, self.scale, workspace=self.ws,
+                         err=self.err)
+
+    def result(self):
+        torch.cuda.synchronize()
+        assert int(self.err.item()) == 0
+        return self.out.clone()
+
+
+@pytest.mark.parametrize("bs", [16, 4])
+@pytest.mark.parametrize("D,dt", [(128, torch.bfloat16), (64, torch.float16)])
+@pytest.mark.parametrize("form", ["wide", "rows16", "rows32", "rows64"])
+def test_attention_directly_behind_its_rotation(form, D, dt, bs):
+    o = Overlap(form, D, bs, dt, D + bs)
+    o.poison()
+    o.rotate()
+    torch.cuda.synchronize()
+    o.attend()
+    want = o.result()
+    assert torch.isfinite(want).all()
+    for _ in range(15):
+        o.poison()
+        o.rotate()
+        o.attend()
+        assert torch.equal(o.result(), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o.rotate()
+        o.attend()
+    for _ in range(15):
+        o.poison()
+        g.replay()
+        assert torch.equal(o.result(), want)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dt,B,most", [(16, 8, 128, torch.bfloat16, 5000, 250), (14, 2, 64, torch.float16, 5000, 250),
+                                                (16, 8, 128, torch.bfloat16, 700, 2000), (14, 2, 64, torch.float16, 900, 2000)])
+def test_decode_directly_behind_its_rotation(Hq, Hkv, D, dt, B, most):
+    """Single tokens: pa_decode's kernels (short tables and long ones) start beside the rotation too."""
+    bs = 16
+    g = torch.Generator(device="cuda").manual_seed(B)
+    r = np.random.default_rng(B)
+    ctx = r.integers(1, most, B)
+    used = -(-ctx // bs)
+    nb = int(used.sum())
+    ids, at = r.permutation(nb), 0
+    bt = np.zeros((B, -(-most // bs)), np.int64)
+    for b in range(B):
+        bt[b, :used[b]] = ids[at:at + used[b]]
+        at += used[b]
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots = i32(bt[np.arange(B), (ctx - 1) // bs] * bs + (ctx - 1) % bs)
+    btd, cl, pos, cos_sin = i32(bt), i32(ctx), i32(ctx - 1), table(most, D)
+    x = torch.randn(B, Hq + 2 * Hkv, D, generator=g, device="cuda").to(dt)
+    base = [torch.randn(nb, bs, Hkv, D, generator=g, device="cuda").to(dt) for _ in range(2)]
+    for pool in base:
+        pool.view(-1, Hkv, D)[slots.long()] = float("nan")
+    pools = [torch.empty_like(p) for p in base]
+    q = torch.empty(B, Hq, D, dtype=dt, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(max(16, pa.pa_decode_workspace_size(B, Hq, Hkv, D, bt.shape[1], bs)), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step(apart):
+        for pool, b in zip(pools, base):
+            pool.copy_(b)
+        q.fill_(float("nan")), out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        pa.pa_rope_store_kv(q, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], *pools, slots, pos, cos_sin, err=err)
+        if apart:
+            torch.cuda.synchronize()
+        pa.pa_decode(out, q, *pools, btd, cl, D ** -0.5, workspace=ws, err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return out.clone()
+
+    want = step(True)
+    assert torch.isfinite(want).all()
+    for _ in range(10):
+        got = step(False)
+        assert torch.isfinite(got).all()
+        # the split form hands its last units out as CTAs come free, so that sums may be joined in another order
+        assert float((got.double() - want.double()).abs().max()) <= (4e-3 if dt == torch.float16 else 2e-2)
+
+
+def test_layers_in_a_row():
+    """Layer by layer into the same buffers, nothing between the calls: a layer's rotation must not overtake the
+    attention that still reads them."""
+    layers = [Overlap(form, 128, 16, torch.bfloat16, 40 + i) for i, form in enumerate(["wide", "rows16", "wide", "rows16"])]
+    for a, b in zip(layers, layers[2:]):  # the same shapes: one q, one set of pools' room, one workspace
+        b.q, b.ws = a.q, a.ws
+    want = []
+    for o in layers:
+        o.poison()
+        o.rotate()
+        torch.cuda.synchronize()
+        o.attend()
+        want.append(o.result())
+    for _ in range(10):
+        for o in layers:
+            o.poison()
+        for o in layers:
+            o.rotate()
+            o.attend()
+        for o, w in zip(layers, want):
+            assert torch.equal(o.result(), w)
+
+
+def test_lengths_and_tables_from_a_kernel_that_lets_its_dependents_start():
+    """The rotation lets what follows start early. Here its output, bit for bit its input (cosines 1, sines 0), is the
+    attention's lengths and page table, written by its last blocks; what lies there before is valid and empty."""
+    T, S, Hq, Hkv, D, bs = 60000, 20, 4, 2, 64, 16
+    r = np.random.default_rng(5)
+    for q in (3, 200):
+        ctx = q + r.integers(0, 512 - 200, S)
+        bt = r.permutation(S * 32).reshape(S, 32)
+        words = torch.zeros(T, 32, dtype=torch.int32)
+        words[T - S:] = torch.from_numpy(bt)
+        words[T - S - 1, :S] = torch.from_numpy(ctx)
+        words[T - S - 2, :S + 1] = torch.arange(S + 1) * q
+        words = words.cuda()
+        moved = torch.zeros_like(words)
+        src, dst = (w.view(torch.float16).view(T, 1, D) for w in (words, moved))
+        kc, vc = (torch.randn(S * 32, bs, Hkv, D, device="cuda").half() for _ in range(2))
+        k, sink = torch.zeros(T, 1, D, device="cuda").half(), torch.zeros(T // 16, 16, 1, D, device="cuda").half()
+        spare = torch.zeros_like(sink)
+        slots, first = torch.arange(T, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+        turn = torch.cat([torch.ones(1, 8), torch.zeros(1, 8)], 1).cuda()
+        x = torch.randn(S * q, Hq, D, device="cuda").half()
+        out = torch.zeros_like(x)
+        ws = torch.empty(pa.pa_chunk_attn_workspace_size(S, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def attend(w):
+            pa.pa_chunk_attn(out, x, kc, vc, w[T - S:], w[T - S - 2, :S + 1], w[T - S - 1, :S], q, D ** -0.5, workspace=ws, err=err)
+
+        attend(words)
+        torch.cuda.synchronize()
+        want = out.clone()
+        assert int(err.item()) == 0 and (want != 0).any(-1).all()
+        for _ in range(20):
+            moved.zero_()
+            out.zero_()
+            torch.cuda.synchronize()
+            pa.pa_rope_store_kv(dst, src, k, k, sink, spare, slots, first, turn, err=err)
+            attend(moved)
+            torch.cuda.synchronize()
+            assert int(err.item()) == 0
+            assert torch.equal(moved, words)
+            assert torch.equal(out, want)
