@@ -65,15 +65,20 @@ __device__ __forceinline__ void give_up(int32_t *err, volatile int *abort_flag) 
 // the shares
 // ------------------------------------------------------------------------------------------
 
+// A length or a table entry. The kernels are launched beside what precedes them, which may still write these: they are
+// read after the wait, by plain loads (the read-only path asks for data that is constant from the kernel's start
+// on, and its loads may be moved before the wait). Past L1, with __ldcg, they cost 0.4 us of a small draft's 8.2.
+__device__ __forceinline__ int ld_index(const int32_t *p) { return *p; }
+
 struct SeqShape {
     int q0, ql, kl;
     bool bad;  // lengths outside the contract: the rows are zero, no work
 };
 __device__ __forceinline__ SeqShape seq_shape(const ChunkParams &p, int s) {
     SeqShape r;
-    r.q0 = __ldg(p.cu_q + s);
-    const int q1 = __ldg(p.cu_q + s + 1);
-    r.kl = __ldg(p.ctx + s);
+    r.q0 = ld_index(p.cu_q + s);
+    const int q1 = ld_index(p.cu_q + s + 1);
+    r.kl = ld_index(p.ctx + s);
     r.bad = r.q0 < 0 || q1 < r.q0 || q1 > p.total_q;
     r.ql = r.bad ? 0 : q1 - r.q0;
     if (r.ql > 0 && (r.ql > p.max_seqlen_q || r.kl < r.ql ||
@@ -181,7 +186,7 @@ __device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p) {
         const SeqShape q = seq_shape(p, s);
         if (!q.bad) continue;
         if (threadIdx.x == 0) raise_err(p.err, PA_DEVERR_LENGTH);
-        const int a = max(q.q0, 0), b = min(__ldg(p.cu_q + s + 1), p.total_q);
+        const int a = max(q.q0, 0), b = min(ld_index(p.cu_q + s + 1), p.total_q);
         for (long long i = static_cast<long long>(a) * p.Hq * HD + threadIdx.x; i < static_cast<long long>(b) * p.Hq * HD;
              i += kThreads)
             out[i] = T(0.f);
@@ -240,7 +245,7 @@ __device__ __forceinline__ bool walk_share(const ChunkParams &p, const Share sh,
 __device__ __forceinline__ long long pool_row(const ChunkParams &p, const SegInfo &it, int pos, int last,
                                               volatile int *bad_seg, int seg_no) {
     if (pos >= it.n_end || last < it.n_lo) return -1;
-    const int id = __ldg(p.block_tables + static_cast<size_t>(it.s) * p.max_blocks + p.geom.block_of(pos));
+    const int id = ld_index(p.block_tables + static_cast<size_t>(it.s) * p.max_blocks + p.geom.block_of(pos));
     if (id < 0 || id >= p.num_blocks) {
         bad_seg[seg_no & (kBadRing - 1)] = seg_no + 1;
         raise_err(p.err, PA_DEVERR_TABLE);
