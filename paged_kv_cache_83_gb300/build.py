@@ -3,7 +3,9 @@
 Each translation unit is compiled in parallel, then the objects are linked into one shared
 library that exports the C ABI of ``include/pa.h``. The runtime is linked shared, so a process
 that already loaded PyTorch's CUDA runtime uses that one instance. The binding's argument checks
-(``csrc/args.cpp``) become an extension module for the installed PyTorch and Python.
+(``csrc/args.cpp``) become an extension module for the installed PyTorch and Python. That needs a C++
+compiler and the headers of both; where they are missing the library is built all the same, with a warning,
+and the calls that go through the module (rotation, chunk attention, sampling) raise.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -54,22 +57,33 @@ def args_path() -> Path:
     return BUILD / f"pa_args-{torch.__version__}-{sys.implementation.cache_tag}.so"
 
 
-def _build_args(headers: list[Path], force: bool) -> None:
-    src, out = CSRC / "args.cpp", args_path()
-    if not (force or _stale(out, [src] + headers)):
-        return
-    import torch
-    home = Path(torch.__file__).resolve().parent
-    tmp = out.with_suffix(f".{os.getpid()}.tmp")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-isystem{home / 'include'}",
-           f"-isystem{home / 'include' / 'torch' / 'csrc' / 'api' / 'include'}",
-           f"-isystem{sysconfig.get_paths()['include']}", f"-isystem{cuda_home() / 'include'}", str(src), "-o", str(tmp),
-           f"-L{home / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{home / 'lib'}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on {src.name}:\n{r.stderr}")
-    os.replace(tmp, out)
+def _build_args(headers: list[Path], force: bool) -> str:
+    """Compiles csrc/args.cpp; what stood in the way, or nothing. A module of other sources does not stay then."""
+    src = CSRC / "args.cpp"
+    try:
+        import torch
+        out = args_path()
+        if not (force or _stale(out, [src] + headers)):
+            return ""
+        home = Path(torch.__file__).resolve().parent
+        tmp = out.with_suffix(f".{os.getpid()}.tmp")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-isystem{home / 'include'}",
+               f"-isystem{home / 'include' / 'torch' / 'csrc' / 'api' / 'include'}",
+               f"-isystem{sysconfig.get_paths()['include']}", f"-isystem{cuda_home() / 'include'}", str(src), "-o", str(tmp),
+               f"-L{home / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{home / 'lib'}"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except ImportError as e:  # no PyTorch: then no binding either
+        return str(e)
+    except OSError as e:  # no compiler
+        lacking = str(e)
+    else:
+        if r.returncode == 0:
+            os.replace(tmp, out)
+            return ""
+        lacking = f"{cmd[0]} failed on {src.name}:\n{r.stderr}"
+    out.unlink(missing_ok=True)
+    return lacking
 
 
 def build(verbose: bool = False, force: bool = False) -> Path:
@@ -96,7 +110,7 @@ def build(verbose: bool = False, force: bool = False) -> Path:
     with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         args = ex.submit(_build_args, headers, force)
         objs = list(ex.map(compile_one, srcs))
-        args.result()
+        lacking = args.result()
     if force or _stale(LIB, objs):
         tmp = LIB.with_suffix(f".{os.getpid()}.tmp")
         libdir = cuda_home() / "lib64"
@@ -106,6 +120,9 @@ def build(verbose: bool = False, force: bool = False) -> Path:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
+    if lacking:
+        warnings.warn(f"the binding's calls for rotation, chunk attention and sampling were not built: {lacking}", RuntimeWarning,
+                      stacklevel=2)
     return LIB
 
 
