@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     T *out = static_cast<T *>(p.out);
 
-    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for this grid itself
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             uint32_t count = 1;
@@ -125,17 +124,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         for (int i = 0; i < kBadRing; ++i) bad_seg[i] = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
 
     // Launched beside what precedes it in the stream: nothing that it wrote is read, and nothing that it reads is
     // written, before it has finished (the set-up above takes place meanwhile).
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Tensor memory is taken only now, and the joining kernel (and with it what follows) let in only when it is
+    // there: no block holds tensor memory while it waits for another grid, whose blocks on this SM may want some.
+    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
     plan_share(p, plan, share);
     zero_bad_sequences<T, HD>(p);
     if (tid == 0) p.recs[blockIdx.x].valid = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for this grid itself
     const uint32_t tmem = *tmem_slot;
 
     // every role reads the segments in the same order: segment n sits in queue entry n % 2

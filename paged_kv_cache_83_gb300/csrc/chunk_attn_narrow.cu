@@ -126,7 +126,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
     auto bar = [&](int i) { return sbase + Lay::OFF_BAR + 8u * i; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for this grid itself
     static_assert(Lay::NBAR <= kThreads);
     if (tid < Lay::NBAR) {
         uint32_t count = 1;
@@ -144,16 +143,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_narrow_kernel(const __grid_
         for (int i = 0; i < kBadRing; ++i) bad_seg[i] = 0;
         for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(fl + Lay::kFloats)[i] = 0;  // votes
     }
-    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), Lay::kTmem);
     // Launched beside what precedes it in the stream: nothing that it wrote is read, and nothing that it reads is
     // written, before it has finished (the set-up above takes place meanwhile).
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Tensor memory is taken only now, and the joining kernel (and with it what follows) let in only when it is
+    // there: no block holds tensor memory while it waits for another grid, whose blocks on this SM may want some.
+    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), Lay::kTmem);
     if (tid == 0) p.recs[blockIdx.x].valid = 0;
     plan_share(p, plan, share);
     zero_bad_sequences<T, HD>(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for this grid itself
     const uint32_t tmem = *tmem_slot;
 
     // every role reads the segments in the same order: segment n sits in queue entry n % 4

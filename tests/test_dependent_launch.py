@@ -26,3 +26,16 @@ def test_there_are_such_kernels():
 def test_nothing_is_read_through_the_read_only_path(path):
     """It asks for data that nothing writes while the kernel runs; the work before may still write when this starts."""
     assert not re.findall(r"__ldg|ld\.global\.nc|ldg_stream|__restrict__ const int32_t", code(path))
+
+
+@pytest.mark.parametrize("name", ["chunk_attn.cu", "chunk_attn_narrow.cu"])
+def test_no_block_waits_for_another_grid_with_tensor_memory(name):
+    """A block takes tensor memory after the wait, and lets dependents start after that. Otherwise one kernel's block
+    could hold it while it waits for the kernel before, whose block on the same SM waits for tensor memory."""
+    text = (CSRC / name).read_text()
+    kernel = text[text.index("__global__"):]
+    kernel = kernel[:kernel.index("\n}\n")]
+    wait, alloc, start = (kernel.index(s) for s in (WAIT, "tmem_alloc(", "griddepcontrol.launch_dependents"))
+    sync = kernel.index("__syncthreads()", alloc)
+    assert wait < alloc < sync < start
+    assert kernel.count("tmem_alloc(") == kernel.count("griddepcontrol.launch_dependents") == 1

@@ -325,3 +325,66 @@ def test_lengths_and_tables_from_a_kernel_that_lets_its_dependents_start():
             assert int(err.item()) == 0
             assert torch.equal(moved, words)
             assert torch.equal(out, want)
+
+
+def test_attention_between_other_kernels_that_use_tensor_memory():
+    """Matrix products, prefill and chunk attention behind one another, on one stream and on two, and captured."""
+    layers = [Overlap(form, D, 16, torch.bfloat16, 60 + i) for i, (form, D) in
+              enumerate([("wide", 128), ("rows16", 64), ("wide", 64), ("rows64", 128)])]
+    want = []
+    for o in layers:
+        o.poison()
+        o.rotate()
+        o.attend()
+        want.append(o.result())
+    a = torch.randn(2048, 2048, device="cuda").bfloat16()
+    c = torch.empty_like(a)
+    torch.matmul(a, a, out=c)
+    cwant = c.clone()
+    cu = torch.tensor([0, 3000], dtype=torch.int32, device="cuda")
+    x = torch.randn(3000, 16 + 2 * 8, 128, device="cuda").bfloat16()
+    q, k, v = (t.contiguous() for t in (x[:, :16], x[:, 16:24], x[:, 24:]))
+    p = torch.empty_like(q)
+
+    def prefill():
+        pa.pa_prefill_varlen(p, q, k, v, None, None, cu, cu, 3000, 3000, None, Hkv=8, scale=128 ** -0.5)
+
+    prefill()
+    torch.cuda.synchronize()
+    pwant = p.clone()
+
+    def step(beside=None):
+        for o in layers:
+            o.rotate()
+            torch.matmul(a, a, out=c)
+            o.attend()
+            if beside is None:
+                torch.matmul(a, a, out=c)
+                prefill()
+            else:
+                with torch.cuda.stream(beside):
+                    prefill()
+
+    def same():
+        torch.cuda.synchronize()
+        for o, w in zip(layers, want):
+            assert torch.equal(o.result(), w)
+        assert torch.equal(c, cwant) and torch.equal(p, pwant)
+
+    side = torch.cuda.Stream()
+    for beside in (None, side):
+        for _ in range(10):
+            for o in layers:
+                o.poison()
+            c.zero_(), p.zero_()
+            torch.cuda.synchronize()
+            step(beside)
+            same()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(10):
+        for o in layers:
+            o.poison()
+        g.replay()
+        same()
