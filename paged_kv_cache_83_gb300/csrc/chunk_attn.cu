@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "chunk_common.cuh"
+#include "tensor_map.h"
 
 namespace pa {
 
@@ -664,38 +665,11 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
 // launch
 // ------------------------------------------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                               cudaSuccess &&
-                           q == cudaDriverEntryPointSuccess;
-        return found ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
-    }();
-    return fn;
-}
-
 // [rows, heads, hd] tensor, box of box_rows x box_heads x 64 columns, 128-byte swizzle
 bool encode(CUtensorMap *m, const void *base, pa_dtype dt, int heads, int hd, long long rows, int box_heads,
             int box_rows) {
-    const auto fn = encode_fn();
-    if (!fn || rows <= 0) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(heads) * hd * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[3] = {1, 1, 1};
-    const auto make = [&] {
-        return fn(m, dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                  const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
-    if (make()) return true;
-    // A thread that has made no call of the runtime yet has no context, which this driver call needs; setting
-    // the device that is current binds one.
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && make();
+    return encode_rows_3d(m, base, dt, heads, hd, rows, box_heads, box_rows, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 template <class E, int HD, bool kGather>

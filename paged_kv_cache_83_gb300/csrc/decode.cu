@@ -38,13 +38,11 @@
 //    tiles land through TMA with the 128-byte swizzle (two 64-column halves when D = 128) so
 //    the ldmatrix reads are free of bank conflicts.
 //  * Every wait is bounded (PA_DEVERR_TIMEOUT); the producer drains its copies before exiting.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <atomic>
 
-#include "pa_internal.h"
+#include "tensor_map.h"
 
 namespace pa {
 
@@ -1397,38 +1395,16 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const __gri
 // host side
 // ------------------------------------------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
-}
-
 // swizzled: boxes of 64 columns with the 128-byte swizzle (tensor-core consumers); else whole
 // unswizzled rows
 bool encode_pool(CUtensorMap *m, const void *pool, pa_dtype dt, int D, int Hkv, long long slots,
                  int box_rows, bool swizzled) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv),
-                          static_cast<cuuint64_t>(slots > 0 ? slots : 1)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hkv) * D * 2};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(swizzled ? 64 : D), 1, static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-              const_cast<void *>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              // L2 fills no wider than one head's row: a 256-byte fill of a 128-byte row (D = 64)
-              // also pulls in the next head's row, which another tile reads much later (measured:
-              // 1.44x the KV bytes from DRAM)
-              D * 2 >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_rows_3d(m, pool, dt, Hkv, D, slots > 0 ? slots : 1, 1, box_rows, swizzled ? 64 : D,
+                          swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          // L2 fills no wider than one head's row: a 256-byte fill of a 128-byte row (D = 64)
+                          // also pulls in the next head's row, which another tile reads much later (measured:
+                          // 1.44x the KV bytes from DRAM)
+                          D * 2 >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 // encode_pool through a small per-thread cache: a tensor map is a pure function of its

@@ -37,14 +37,12 @@
 //   dim 64 P_A 320-383 and P_B 448-511 (16-bit pairs, one row per lane).
 // Every wait is bounded (PA_DEVERR_TIMEOUT); on a timeout every role drains what it started
 // (TMA, MMAs) before the TMEM is freed.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
 #include <atomic>
 
-#include "pa_internal.h"
+#include "tensor_map.h"
 
 namespace pa {
 
@@ -661,31 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn_tc() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
-}
-
 // [rows, heads, hd] tensor, box [box_rows, 1, 64], 128-byte swizzle
 bool encode_rows(CUtensorMap *m, const void *base, pa_dtype dt, int heads, int hd, long long rows, int box_rows) {
-    auto fn = encode_fn_tc();
-    if (!fn || rows <= 0) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(heads) * hd * 2};
-    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_rows_3d(m, base, dt, heads, hd, rows, 1, box_rows, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // Work counters of the persistent launches: [slot][0] the next work item, [slot][1] CTAs done.
