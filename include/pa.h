@@ -324,7 +324,7 @@ pa_status pa_prefill_varlen(void *out, const void *q, const void *k, const void 
  *
  * out           [total_q, Hq, D], written; rows outside every sequence (padding before
  *               cu_seqlens_q[0] or from cu_seqlens_q[S] on) are left as they were.
- * q             [total_q, Hq, D].
+ * q             [total_q, Hq, D]. out may be q itself; any other overlap of the two is PA_ERR_UNSUPPORTED.
  * block_tables  int32 [S, max_blocks_per_seq]. Entries of blocks that end before the first visible
  *               key of the chunk are not read (they may hold anything once a window has passed).
  *               An entry that must be read and lies outside [0, num_blocks) sets PA_DEVERR_TABLE;

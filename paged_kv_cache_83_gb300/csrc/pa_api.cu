@@ -415,6 +415,9 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
     if (max_blocks_per_seq < 1 || num_blocks < 1) return PA_ERR_SHAPE;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !context_lens) return PA_ERR_NULL;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_UNSUPPORTED;
+    // out is q itself (an item's queries are read before its rows are written) or lies clear of it
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), x = reinterpret_cast<uintptr_t>(q), apart = o < x ? x - o : o - x;
+    if (apart != 0 && apart < static_cast<uint64_t>(total_q) * Hq * D * 2) return PA_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < pa::chunk_attn_workspace(D) || !aligned16(workspace))
         return PA_ERR_WORKSPACE;
     pa::ChunkArgs a{};

@@ -411,3 +411,23 @@ def test_the_first_call_of_a_thread():
     with ThreadPoolExecutor(1) as ex:
         ex.submit(c.run, stream=stream).result()
     c.check(run=False)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,bs", [
+    ([(8, 5003), (300, 1600), (2, 700)], 16, 8, 128, 256), ([(300, 2000), (1, 3000), (77, 77)], 14, 2, 64, 16),
+    ([(2000, 2000), (600, 9000)], 8, 1, 128, 16), ([(4, 2000), (1, 300), (3, 77)], 8, 2, 128, 16),
+    ([(9, 4000), (1, 1), (5, 128)], 14, 2, 64, 16), ([(8, 4000), (7, 129)], 8, 2, 64, 4)])
+def test_out_is_q(lens, Hq, Hkv, D, bs):
+    """In place: whole items and joined ones, neighbours' rows in the same load of queries."""
+    c = Case(lens, Hq, Hkv, D, bs, "bf16", seed=17)
+    c.check()
+    q, c.out = c.q.clone(), c.q
+    want = None
+    for _ in range(10):
+        c.q.copy_(q)
+        c.run()
+        torch.cuda.synchronize()
+        want = c.out.clone() if want is None else want
+        assert torch.equal(c.out, want)
+    c.q = q
+    c.check(run=False)

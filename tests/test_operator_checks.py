@@ -135,6 +135,14 @@ def test_chunk_attn_refusals(lib):
     assert lib.pa_chunk_attn_workspace_size(2, 4, 2, 96) == 0
 
 
+def test_chunk_attn_refuses_overlap(lib):
+    rows = 8 * 4 * 64 * 2
+    for out, q in ((FAKE + 16, FAKE), (FAKE, FAKE + 16), (FAKE + rows - 16, FAKE), (FAKE, FAKE + rows - 16)):
+        assert _chunk(lib, out=out, q=q) == UNSUPPORTED
+    for out, q in ((FAKE, FAKE), (FAKE + rows, FAKE), (FAKE, FAKE + rows), (FAR, FAKE)):
+        assert _chunk(lib, out=out, q=q) == WORKSPACE  # the next check
+
+
 def test_chunk_attn_binding_refusals():
     q = torch.zeros(6, 4, 64, dtype=torch.float16)
     pool = torch.zeros(2, 16, 2, 64, dtype=torch.float16)
