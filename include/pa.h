@@ -113,8 +113,9 @@ pa_status pa_store_kv(const void *k, const void *v, void *k_cache, void *v_cache
  * q, q_out      [T, Hq, D], k, v [T, Hkv, D]; the heads of a token contiguous, tokens
  *               q_stride, q_out_stride, k_stride, v_stride elements apart (slices of one
  *               projection's output, for instance). Strides are multiples of 8, at least Hq * D or
- *               Hkv * D. q_out may be q itself (same pointer and stride); any other overlap of
- *               q_out's span with the spans of q, k or v is PA_ERR_UNSUPPORTED.
+ *               Hkv * D. q_out may be q itself (same pointer and stride; k and v may then lie beside
+ *               q in the tokens of one tensor); any other overlap of q_out's span with the spans of
+ *               q, k or v is PA_ERR_UNSUPPORTED. The pools overlap none of them.
  * slot_mapping  int32 [T], as pa_store_kv.
  * positions     int32 [n_axes, T], 1 <= n_axes <= 4. A position outside [0, max_pos) on any axis
  *               sets PA_DEVERR_POSITION and the token is skipped.

@@ -126,14 +126,21 @@ pa_status pa_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int
     for (int i = 0; pair_axis && i < rot_dim / 2; ++i)
         if (pair_axis[i] >= n_axes) return PA_ERR_SHAPE;
     if (static_cast<long long>(T) * (Hq + 2ll * Hkv) * ((D + 15) / 16 + 1) / 256 > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
-    // q_out is q itself or lies clear of everything that is read
+    // q_out is q itself or lies clear of everything that is read; in place, k and v lie clear of q, or beside it in the
+    // tokens of one tensor
     auto span_meets = [&](const void *p, int64_t stride, int64_t width) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(q_out), b = reinterpret_cast<uintptr_t>(p);
         return a < b + 2 * ((T - 1) * stride + width) && b < a + 2 * ((T - 1) * q_out_stride + qw);
     };
-    if (!(q_out == q && q_out_stride == q_stride) &&
-        (span_meets(q, q_stride, qw) || span_meets(k, k_stride, kw) || span_meets(v, v_stride, kw)))
-        return PA_ERR_UNSUPPORTED;
+    auto beside_q = [&](const void *p, int64_t stride) {
+        const int64_t off = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(q))) / 2;
+        const int64_t d = (off % stride + stride) % stride;
+        return stride == q_stride && d >= qw && d + kw <= stride;
+    };
+    const bool in_place = q_out == q && q_out_stride == q_stride;
+    if (!in_place && span_meets(q, q_stride, qw)) return PA_ERR_UNSUPPORTED;
+    if (span_meets(k, k_stride, kw) && !(in_place && beside_q(k, k_stride))) return PA_ERR_UNSUPPORTED;
+    if (span_meets(v, v_stride, kw) && !(in_place && beside_q(v, v_stride))) return PA_ERR_UNSUPPORTED;
     pa::RopeStoreArgs a{};
     a.q_out = q_out;
     a.q = q;

@@ -61,6 +61,16 @@ def test_rope_store_refuses_overlap(lib):
     assert _rope(lib, q=1 << 25, v=FAR - 1024 + 16) == UNSUPPORTED
 
 
+def test_rope_store_in_place_refuses_keys_within_q(lib):
+    # In place on q, k or v would be read from what is written: q's own rows, rows that start in one, rows that run into
+    # the next token's, rows that lie beside the first token's only. (Tokens of 512 elements, of which q takes 256.)
+    far = {"qo": FAKE, "q": FAKE, "qs": 512, "qos": 512, "k": FAR, "v": FAR, "ks": 512, "vs": 512}
+    for name, stride in (("k", "ks"), ("v", "vs")):
+        for at in (0, 128, 512 - 64, -64, 512 + 128):
+            assert _rope(lib, **{**far, name: FAKE + 2 * at}) == UNSUPPORTED, at
+        assert _rope(lib, **{**far, name: FAKE + 2 * 256, stride: 256}) == UNSUPPORTED
+
+
 def test_pair_axis_of_sections():
     assert list(pa.rope_pair_axis([2, 3, 1])) == [0, 0, 1, 1, 1, 2]
     assert list(pa.rope_pair_axis([4, 2, 2], interleaved=True)) == [0, 1, 2, 0, 1, 2, 0, 0]
