@@ -31,7 +31,7 @@
 // Every wait is bounded (PA_DEVERR_TIMEOUT); on a timeout every role drains what it started.
 //
 // Bound by the softmax warps' latency: two chunks of 2k tokens at contexts of 12-16k (16/8 heads x 128, bf16)
-// 320-344 us = 1.33-1.24 PFLOP/s, the tensor pipe 58 % active, a key tile of both row tiles every 3300 clocks against
+// 333-347 us = 1.28-1.23 PFLOP/s, the tensor pipe 58 % active, a key tile of both row tiles every 3300 clocks against
 // 1024 of MMAs and as many of exponentials. Two threads a row, which exchange maxima: 8 % slower; P
 // stored while the exponentials run: 4 % slower.
 #include <type_traits>

@@ -11,7 +11,7 @@
 // in each thread until the segment ends.
 //
 // Bound by HBM: every key and value is read once per kv head (2.2 GB for 256 drafts of up to 5 tokens
-// over contexts to 4096 take 352 us, 0.93 of the copy bandwidth; with 128-row tiles 684 us). The
+// over contexts to 4096 take 345-353 us, 0.93 of the copy bandwidth; with 128-row tiles 684 us). The
 // loads run ahead in rings of tiles; two streams of softmax warps take the key tiles in
 // turn, each with its own maximum, sum and accumulator, so that one computes while the other waits
 // for its matrix products. They join at the end of a segment.
@@ -749,7 +749,9 @@ cudaError_t launch_typed(const ChunkParams &prm, cudaStream_t stream) {
 template <class E, int HD>
 cudaError_t launch_rows(const ChunkParams &prm, bool gather, cudaStream_t stream) {
     const int rows = prm.max_seqlen_q * prm.G;
-    // gathered keys are bound by their copies, whatever the columns: one form for all
+    // gathered keys are bound by the one warp that copies them, whatever the columns: one form for all (128 sequences at
+    // contexts to 4096, 16/8 heads x 128, pages of 4: 470 us with 2 query rows a head, 482 with 32, 514 with 64, by
+    // boxes 190-236; pages of one row 1365-1373)
     if (gather) return launch_typed<E, HD, 32, true, true>(prm, stream);
     if (rows <= 16) return launch_typed<E, HD, 16, false, false>(prm, stream);
     if (rows <= 32) return launch_typed<E, HD, 32, false, false>(prm, stream);

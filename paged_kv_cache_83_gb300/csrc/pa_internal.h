@@ -135,6 +135,7 @@ struct SampleArgs {
     const float *top_p, *min_p;
     int32_t *err;
 };
+// the longest rows that are tested; eight CTAs' shared memory would hold some 417,000 logits
 constexpr int kSampleMaxVocab = 1 << 18;
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
 

@@ -23,10 +23,10 @@
 //
 // Compiled without flush-to-zero: subnormal logits are ordered, and weighed, like any others.
 //
-// Measured: 256 rows of 151,936 fp32 with settings of every kind 149 us (the reads alone: 23); by kind,
-// greedy 48, top-k 91, temperature alone 135, top-p 332: what bounds the last two is the instructions of the
-// weights and the bins, 40 and 100 a token, at two CTAs an SM. One row: greedy 5 us, top-k 12,
-// top-p 32, chains of cluster-wide barriers of about a microsecond.
+// Measured: 256 rows of 151,936 fp32 with settings of every kind 147 us (the reads alone: 23); by kind,
+// greedy 50, top-k 85, temperature alone 131, top-p 317 (bf16: 46, 81, 126, 329): what bounds the last two is the
+// instructions of the weights and the bins, 40 and 100 a token, at two CTAs an SM. One row: greedy 5 us, top-k 11,
+// temperature alone 11, top-p 19-31 by the row, chains of cluster-wide barriers of about a microsecond.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -728,9 +728,10 @@ cudaError_t launch_typed(const SampleArgs &a, cudaStream_t stream) {
     prm.u = a.u, prm.temperature = a.temperature, prm.top_p = a.top_p, prm.min_p = a.min_p, prm.top_k = a.top_k;
     prm.tokens = a.tokens;
     prm.err = a.err;
-    // A CTA for every 4096 elements of a row, up to eight; sixteen where that still leaves half of the SMs idle
-    // (one row of 151,936: 32 us against 45; 256 rows: 223 us against 133 with clusters of eight, 194 of four,
-    // for greedy rows, when measured).
+    // A CTA for every 4096 elements of a row, up to eight (256 rows of 151,936 fp32 with settings of every kind: 148 us,
+    // with clusters of four 174, of sixteen 245; greedy rows 50, 46 and 106); sixteen where that still leaves half
+    // of the SMs idle (top-p, one row: 22 us against 29 with eight, four rows 28 against 37). Five to nine rows
+    // would gain from sixteen too (28-34 us against 37), 16 rows not (51 against 43).
     int CS = 1;
     while (CS < 8 && a.V > 4096 * CS) CS *= 2;
     const bool few = a.V > 4096 * 8 && a.B * 16 <= device_sm_count() / 2;
