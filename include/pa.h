@@ -324,7 +324,7 @@ pa_status pa_prefill_varlen(void *out, const void *q, const void *k, const void 
  * the GPU as the lengths ask, so that few query rows with long contexts use the whole machine, in the
  * window, and in the lengths, which are pa_decode's. Many whole prompts with a short cached prefix are faster there
  * (64 prompts of 100-1024 tokens behind 512: 316 us against 332; without a prefix 207 against 258), few or short
- * chunks with long contexts here (two chunks of 2k tokens at 12-16k: 308 us against 389).
+ * chunks with long contexts here (two chunks of 2k tokens at 13-14k: 308 us against 389).
  *
  * max_seqlen_q chooses the kernels for the whole call: where it is at most 64 / (Hq / Hkv) tokens, those for
  * few query rows, else 128-row tiles, which cost single tokens half as much again (250 of them: 350 and 530 us). So give the
