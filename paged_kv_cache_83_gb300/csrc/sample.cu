@@ -206,7 +206,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     }
 
     __syncwarp();
-    if (!mbar_wait(landed, 0)) raise_err(p.err, PA_DEVERR_TIMEOUT);
+    if (!mbar_wait(landed, 0)) {
+        raise_err(p.err, PA_DEVERR_TIMEOUT);
+        mbar_wait(landed, 0);  // the copy may still land: once more as long before the CTA can end
+    }
     float mx = -INFINITY;
     int mx_at = lane * EV;  // where in `mine` this lane's first word with its maximum lies
 #pragma unroll 2
