@@ -54,7 +54,12 @@ typedef enum {
     PA_ERR_CUDA = 6         /* a CUDA runtime call failed (e.g. the launch) */
 } pa_status;
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 /* pa_sample's logits only */ } pa_dtype;
+typedef enum {
+    PA_F16 = 0,
+    PA_BF16 = 1,
+    PA_F32 = 2, /* pa_sample's logits and pa_verify's probabilities only */
+    PA_E4M3 = 3 /* 8-bit pools only: 4 bits of exponent, 3 of mantissa, largest finite value 448 */
+} pa_dtype;
 
 /* Bits OR-ed into *err by the kernels. */
 #define PA_DEVERR_SLOT 1   /* slot_mapping entry >= num_blocks * block_size: token not stored */
@@ -65,7 +70,8 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 /* pa_sample's logits only */
                               q_len > max_seqlen_q): the sequence's output rows are zero */
 #define PA_DEVERR_POSITION 16 /* a token's position lies outside the cosine/sine table: the token
                               is skipped */
-#define PA_DEVERR_ROW 32 /* a row of logits holds nothing above -infinity: its token is -1 */
+#define PA_DEVERR_ROW 32 /* a row of logits holds nothing above -infinity, or one of probabilities no
+                            weight: its token is -1 */
 #define PA_DEVERR_TIMEOUT 8 /* an internal wait (on an asynchronous copy or on another warp)
                                gave up after about half a second: the kernel stopped early and
                                its outputs are incomplete */
@@ -136,6 +142,43 @@ pa_status pa_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int
                            const float *cos_sin, int max_pos, int rot_dim, int interleaved, int T,
                            int num_blocks, int block_size, int Hq, int Hkv, int D, pa_dtype dtype,
                            int32_t *err, cudaStream_t stream);
+
+/*
+ * pa_norm_rope_store_kv: norms of a step's queries and keys for each head, their rotation, and the append of
+ * keys and values to the pools, which may be of 8 bits, in one launch. pa_chunk_attn_q8 reads the 8-bit pools.
+ *
+ * Source: as pa_rope_store_kv; the norms are those of the engines' Qwen3 models (smzdm deep dive "模型实现细节").
+ *
+ *   for t in [0, T): s = slot_mapping[t]; if s < 0 skip the token, as pa_rope_store_kv
+ *       each row x of q[t], k[t]:  y = x / sqrt(mean(x^2) + eps) * weight   (y = x where the weight is NULL),
+ *           then rotated as in pa_rope_store_kv (rot_dim == 0: not)
+ *       q_out[t] = y of q[t];  k_cache row s = y of k[t];  v_cache row s = v[t]
+ *   with cache_dtype == PA_E4M3 each row z of keys (y) and values (v) of a slot and kv head has a scale of its own:
+ *       scale = max(max |z| / 448, 2^-90),   cache row = z / scale, rounded to the nearest e4m3 (ties to even)
+ *   which reads back as scale * cache row. A row that holds a NaN or an infinity reads back as NaN throughout (its
+ *   scale is NaN or infinite).
+ *
+ * Sums, products and quotients in fp32 (subnormal operands count as 0; squares beyond FLT_MAX make a normalised row 0 or NaN),
+ * rounded once to what is stored; values in pools of the storage type are bit copies.
+ *
+ * q_weight, k_weight  [D] of the storage type, 16-byte aligned, or NULL (each by itself): no norm of those rows.
+ * eps           >= 0 and finite.
+ * cache_dtype   dtype, or PA_E4M3: pools of one byte an element, [num_blocks, block_size, Hkv, D] as ever, and
+ * k_scale, v_scale  fp32 [num_blocks, Hkv, block_size]; written for the stored tokens only, like the pools. NULL
+ *               otherwise. Nothing overlaps them.
+ * rot_dim       0 (positions, pair_axis, cos_sin, n_axes and max_pos are then not looked at), or as pa_rope_store_kv.
+ * All else as pa_rope_store_kv, in place (q_out == q) included. Supported: D % 8 == 0, D <= 512.
+ * Bytes moved: T * D * 2 * (2 * Hq + 4 * Hkv), of which the 8-bit pools save T * Hkv * (2 * D - 8); and the table rows.
+ */
+pa_status pa_norm_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                                const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                const int32_t *slot_mapping, const void *q_weight, const void *k_weight,
+                                float eps, const int32_t *positions, int n_axes,
+                                const uint8_t *pair_axis, const float *cos_sin, int max_pos, int rot_dim,
+                                int interleaved, int T, int num_blocks, int block_size, int Hq, int Hkv,
+                                int D, pa_dtype dtype, pa_dtype cache_dtype, int32_t *err,
+                                cudaStream_t stream);
 
 /*
  * pa_decode_workspace_size: bytes of scratch pa_decode needs for these sizes on the current
@@ -401,6 +444,49 @@ pa_status pa_sample(int32_t *tokens, const void *logits, int64_t row_stride, int
                     pa_dtype dtype, const float *u, const float *temperature,
                     const int32_t *top_k, const float *top_p, const float *min_p, int32_t *err,
                     cudaStream_t stream);
+
+/*
+ * pa_verify: drafted tokens against the target's probabilities, from given random numbers: how many of each
+ * sequence's drafts stand, and the token after them. The chunks are those of pa_chunk_attn: a sequence's rows are the
+ * last token of its text and then its drafts, and row r holds the target's distribution of the token behind the chunk's
+ * token r.
+ *
+ * Source: smzdm nano-vLLM deep dive (sampling from each request's distribution); "nano-vLLM Part 4" section 3 (step 3). The rule
+ * is that of speculative sampling, which leaves the target's distribution as it is for any drafter.
+ *
+ *   for sequence s: rows a = cu_seqlens_q[s] .. b = cu_seqlens_q[s+1], n = b - a - 1 drafts tokens[a+1 .. b)
+ *       k = the number of drafts before the first r with not u[a+r] * q(x) < p(x), where x = tokens[a+r+1],
+ *           p = probs[a+r], q = draft_probs[a+r] (draft_probs NULL, a drafter without distribution: q(x) = 1)
+ *       weights r_j, from row a + k:  k == n: p_j;  else max(p_j - q_j, 0) (draft_probs NULL: p_j, and 0 for the draft);
+ *           where all of these are 0: p_j
+ *       w_j = rint(min(r_j, 1) * 2^44), W their sum;  t = the first token at which the running sum of w, in the order of
+ *           the vocabulary, exceeds floor(W * floor(u[b-1] * 2^31) / 2^31)
+ *       accepted[s] = k;  next_tokens[a .. b) = the k drafts, t, and -1 from there on
+ *
+ * So the number of new tokens is accepted + 1. Products of the tests and sums of the weights are exact, the
+ * differences p - q are fp32 (subnormal ones count as 0): the tokens do not depend on how the work is divided.
+ * A draft outside [0, V) ends the drafts before it, as if the sequence had no more (k == n): a captured step
+ * pads shorter drafts with -1.
+ *
+ * next_tokens   int32 [total_q], written for the rows of the sequences; the others stay as they were. It does not overlap
+ *               tokens (PA_ERR_UNSUPPORTED).
+ * accepted      int32 [S], written; 0 for a sequence without rows.
+ * tokens        int32 [total_q], the chunks.
+ * probs, draft_probs  [total_q, V] fp16, bf16 or fp32 (`dtype`, of both), rows probs_stride and draft_stride elements apart, at
+ *               least V; any alignment that the element type has. A row's numbers sum to about 1; NaN and negative ones count as
+ *               0, larger ones as 1 (in the test: a p that is NaN refuses, as does a q). The last row of a sequence in
+ *               draft_probs is not read, nor is any row behind the one that decides.
+ * cu_seqlens_q  int32 [S+1], non-decreasing, from >= 0 to <= total_q; a span outside that sets PA_DEVERR_LENGTH, and the
+ *               sequence's accepted is 0 and its rows are left as they were.
+ * u             fp32 [total_q], uniform in [0, 1): row a + r the number of draft r's test, row b - 1 that of the token. There NaN and
+ *               values below 0 count as 0, values from 1 on as 1 - 2^-31; in a test a NaN refuses.
+ * A row without any weight gives the token -1 and PA_DEVERR_ROW. Supported: 1 <= V <= 262144. S == 0 is a no-op. Reads one row of
+ * probs a sequence, and where a draft is refused one of draft_probs.
+ */
+pa_status pa_verify(int32_t *next_tokens, int32_t *accepted, const int32_t *tokens, const void *probs,
+                    int64_t probs_stride, const void *draft_probs, int64_t draft_stride,
+                    const int32_t *cu_seqlens_q, const float *u, int S, int total_q, int V,
+                    pa_dtype dtype, int32_t *err, cudaStream_t stream);
 
 /*
  * pa_decode_noalloc: pa_decode for callers that cannot allocate device memory.

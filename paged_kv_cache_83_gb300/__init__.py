@@ -7,11 +7,11 @@ from .binding import (PA_BM_DEGENERATE_HASH, BlockManager, BlockManagerError,
                       PA_DEVERR_TABLE, PA_DEVERR_TIMEOUT, PagedAttnError, load, pa_chunk_attn,
                       pa_chunk_attn_workspace_size, pa_decode,
                       pa_decode_debug_tail_units, pa_decode_noalloc,
-                      pa_decode_workspace_size, pa_prefill_varlen, pa_rope_store_kv, pa_sample, pa_store_decode,
+                      pa_decode_workspace_size, pa_norm_rope_store_kv, pa_prefill_varlen, pa_rope_store_kv, pa_sample, pa_store_decode,
                       pa_store_decode_host, pa_store_decode_host_layout,
-                      pa_store_decode_host_workspace_size, pa_store_kv, rope_pair_axis)
+                      pa_store_decode_host_workspace_size, pa_store_kv, pa_verify, rope_pair_axis)
 
-__all__ = ["load", "pa_store_kv", "pa_rope_store_kv", "rope_pair_axis", "pa_decode", "pa_store_decode", "pa_store_decode_host",
+__all__ = ["load", "pa_store_kv", "pa_norm_rope_store_kv", "pa_verify", "pa_rope_store_kv", "rope_pair_axis", "pa_decode", "pa_store_decode", "pa_store_decode_host",
            "pa_store_decode_host_layout", "pa_store_decode_host_workspace_size", "pa_decode_workspace_size",
            "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample",
            "pa_decode_noalloc", "PA_DECODE_NOALLOC_SCRATCH_BYTES", "BlockManager",

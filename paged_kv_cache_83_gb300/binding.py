@@ -2,7 +2,7 @@
 
 Each function takes torch CUDA tensors, checks their dtype / shape / contiguity, and calls the
 entry point of the same name in ``_build/libpagedattn.so`` with raw device pointers and the
-current CUDA stream; those of rotation, chunk attention and sampling do so in an extension module
+current CUDA stream; those of rotation, chunk attention, sampling and verification do so in an extension module
 (``csrc/args.cpp``), since a call of theirs takes a few microseconds. Every step of the computation
 runs in the library's kernels; there is no fallback: if the library is missing or a call fails, these
 functions raise.
@@ -21,11 +21,12 @@ from .build import args_path
 PKG = Path(__file__).resolve().parent
 LIB_PATH = PKG / "_build" / "libpagedattn.so"
 
-PA_F16, PA_BF16, PA_F32 = 0, 1, 2
+PA_F16, PA_BF16, PA_F32, PA_E4M3 = 0, 1, 2, 3
 PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION, PA_DEVERR_ROW = 1, 2, 4, 8, 16, 32
 EXPORTS = ("pa_store_kv", "pa_rope_store_kv", "pa_decode_workspace_size", "pa_decode", "pa_store_decode",
            "pa_store_decode_host", "pa_store_decode_host_workspace_size", "pa_store_decode_host_layout",
-           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample", "pa_decode_noalloc", "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
+           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample", "pa_norm_rope_store_kv", "pa_verify", "pa_decode_noalloc",
+           "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
            "pa_bm_destroy", "pa_bm_allocate", "pa_bm_can_allocate", "pa_bm_append",
            "pa_bm_release", "pa_bm_block_table", "pa_bm_num_tokens", "pa_bm_num_free",
            "pa_bm_refcount")
@@ -78,6 +79,11 @@ def load(path: Path | str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_chunk_attn.restype = I
     lib.pa_sample.argtypes = [P, P, L, I, I, I, P, P, P, P, P, P, P]
     lib.pa_sample.restype = I
+    lib.pa_norm_rope_store_kv.argtypes = [P, L, P, L, P, L, P, L, P, P, P, P, P, P, P, F, P, I, P, P, I, I, I, I, I, I, I,
+                                          I, I, I, I, P, P]
+    lib.pa_norm_rope_store_kv.restype = I
+    lib.pa_verify.argtypes = [P, P, P, P, L, P, L, P, P, I, I, I, I, P, P]
+    lib.pa_verify.restype = I
     lib.pa_decode_noalloc.argtypes = [P, P, P, P, P, I, P, I, I, I, I, I, I, F, I, P, P]
     lib.pa_decode_noalloc.restype = I
     lib.pa_decode_debug_tail_units.argtypes = [P, I, I, I, I, I, I]
@@ -118,7 +124,7 @@ def _load_args():
     mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_args", loader))
     loader.exec_module(mod)
     mod.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-               for name in ("pa_rope_store_kv", "pa_chunk_attn", "pa_sample")))
+               for name in ("pa_rope_store_kv", "pa_chunk_attn", "pa_sample", "pa_norm_rope_store_kv", "pa_verify")))
     _args = mod
     return mod
 
@@ -214,6 +220,19 @@ def pa_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, 
                                                       pair_axis, interleaved, err, stream)
     if status:
         raise PagedAttnError("pa_rope_store_kv", status)
+
+
+def pa_norm_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, q_weight=None, k_weight=None, eps: float = 1e-6,
+                          positions=None, cos_sin=None, pair_axis=None, interleaved: bool = False, k_scale=None,
+                          v_scale=None, err=None, stream=None) -> None:
+    """pa_rope_store_kv with root-mean-square norms of each head's queries and keys before the rotation (q_weight,
+    k_weight [D]; None: no norm), and with pools that may be of 8 bits: float8_e4m3fn, and then k_scale, v_scale
+    float32 [NB, Hkv, bs], a scale for each row. positions and cos_sin None: no rotation."""
+    status = (_args or _load_args()).pa_norm_rope_store_kv(q_out, q, k, v, k_cache, v_cache, slot_mapping, q_weight, k_weight,
+                                                           eps, positions, cos_sin, pair_axis, interleaved, k_scale, v_scale,
+                                                           err, stream)
+    if status:
+        raise PagedAttnError("pa_norm_rope_store_kv", status)
 
 
 def pa_decode_workspace_size(B: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,
@@ -384,6 +403,17 @@ def pa_sample(tokens, logits, u=None, temperature=None, top_k=None, top_p=None, 
     status = (_args or _load_args()).pa_sample(tokens, logits, u, temperature, top_k, top_p, min_p, err, stream)
     if status:
         raise PagedAttnError("pa_sample", status)
+
+
+def pa_verify(next_tokens, accepted, tokens, probs, cu_seqlens_q, u, draft_probs=None, err=None, stream=None) -> None:
+    """Drafts against the target's probabilities: sequence s has the chunk tokens[cu_seqlens_q[s] : cu_seqlens_q[s + 1]], its
+    last token and then its drafts, and probs [total_q, V] the target's distribution behind each of them. accepted [S]: how many
+    drafts stand; next_tokens [total_q]: those, the token that follows them, then -1. u [total_q]: a uniform number for each
+    draft's test, and in a sequence's last row for the token. draft_probs: the drafter's distributions, row for row (None: its
+    tokens are certain)."""
+    status = (_args or _load_args()).pa_verify(next_tokens, accepted, tokens, probs, cu_seqlens_q, u, draft_probs, err, stream)
+    if status:
+        raise PagedAttnError("pa_verify", status)
 
 
 # ---------------------------------------------------------------------------------------------

@@ -1,5 +1,5 @@
 // args.cpp: argument checks and marshalling of the calls that a step or a sampled token repeats
-// (pa_rope_store_kv, pa_chunk_attn, pa_sample), as an extension module of the binding.
+// (rotation, chunk attention, sampling, verification), as an extension module of the binding.
 //
 // The kernel of a decode step's rotation takes 2 us. Its eleven tensors checked in Python and 27 arguments passed
 // through ctypes made the call 10.4 us (4 tokens) and 11.1 us (256 tokens), back to back; checked here it is 4.1 us for
@@ -23,6 +23,8 @@ namespace {
 decltype(&::pa_rope_store_kv) call_rope_store_kv = nullptr;
 decltype(&::pa_chunk_attn) call_chunk_attn = nullptr;
 decltype(&::pa_sample) call_sample = nullptr;
+decltype(&::pa_norm_rope_store_kv) call_norm_rope_store_kv = nullptr;
+decltype(&::pa_verify) call_verify = nullptr;
 
 struct Refused {  // a Python exception has been set
 };
@@ -87,6 +89,16 @@ int64_t token_stride(const at::Tensor &t, int64_t T, int64_t H, int64_t D, const
     const auto s = t.strides();
     if (s[2] != 1 || (s[1] != D && H > 1)) refuse(PyExc_ValueError, what);
     return T > 1 ? s[0] : H * D;
+}
+
+// the scales of an 8-bit pool, fp32 [num_blocks, Hkv, block_size]
+float *scales_of(PyObject *o, int64_t NB, int64_t Hkv, int64_t bs, Device &dev) {
+    const at::Tensor &t = tensor(o, "the scales must be tensors");
+    if (t.scalar_type() != at::kFloat) refuse(PyExc_TypeError, "the scales must be float32");
+    if (t.dim() != 3 || t.size(0) != NB || t.size(1) != Hkv || t.size(2) != bs)
+        refuse(PyExc_ValueError, "the scales must be [num_blocks, Hkv, block_size]");
+    dev.add(t);
+    return const_cast<float *>(static_cast<const float *>(contiguous(t)));
 }
 
 int small(int64_t v) {  // a size as the C interface takes it
@@ -207,6 +219,92 @@ PyObject *rope_store_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// q_out, q, k, v, k_cache, v_cache, slot_mapping, q_weight, k_weight, eps, positions, cos_sin, pair_axis, interleaved, k_scale,
+// v_scale, err, stream
+PyObject *norm_rope_store_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 18, [&] {
+        bound(call_norm_rope_store_kv);
+        const at::Tensor &q_out = tensor(a[0], "q_out must be a tensor"), &q = tensor(a[1], "q must be a tensor"),
+                         &k = tensor(a[2], "k must be a tensor"), &v = tensor(a[3], "v must be a tensor"),
+                         &kc = tensor(a[4], "k_cache must be a tensor"), &vc = tensor(a[5], "v_cache must be a tensor"),
+                         &slots = tensor(a[6], "slot_mapping must be a tensor");
+        if (kc.dim() != 4 || q.dim() != 3 || k.dim() != 3) refuse(PyExc_ValueError, "shape mismatch");
+        const int64_t NB = kc.size(0), bs = kc.size(1), Hkv = kc.size(2), D = kc.size(3), T = q.size(0), Hq = q.size(1);
+        if (q.size(2) != D || q_out.sizes() != q.sizes() || k.size(0) != T || k.size(1) != Hkv || k.size(2) != D ||
+            v.sizes() != k.sizes() || vc.sizes() != kc.sizes())
+            refuse(PyExc_ValueError, "shape mismatch");
+        if (slots.dim() != 1 || slots.size(0) != T) refuse(PyExc_ValueError, "slot_mapping must be [T]");
+        const pa_dtype dt = dtype_of(q);
+        const auto type = q.scalar_type(), cached = kc.scalar_type();
+        if (q_out.scalar_type() != type || k.scalar_type() != type || v.scalar_type() != type)
+            refuse(PyExc_TypeError, "q, q_out, k and v must share a dtype");
+        const bool q8 = cached == at::kFloat8_e4m3fn;
+        if (vc.scalar_type() != cached || (!q8 && cached != type))
+            refuse(PyExc_TypeError, "the pools must share a dtype, that of q or float8_e4m3fn");
+        int32(slots, "slot_mapping must be int32");
+        Device dev;
+        for (const at::Tensor *t : {&q, &q_out, &k, &v, &kc, &vc, &slots}) dev.add(*t);
+        const void *weight[2] = {nullptr, nullptr};
+        for (int i = 0; i < 2; ++i) {
+            if (a[7 + i] == Py_None) continue;
+            const at::Tensor &w = tensor(a[7 + i], "a norm's weight must be a tensor");
+            if (w.scalar_type() != type) refuse(PyExc_TypeError, "a norm's weight must have the dtype of q");
+            if (w.dim() != 1 || w.size(0) != D) refuse(PyExc_ValueError, "a norm's weight must be [D]");
+            dev.add(w);
+            weight[i] = contiguous(w);
+        }
+        const double eps = PyFloat_AsDouble(a[9]);
+        if (eps == -1.0 && PyErr_Occurred()) throw Refused{};
+        const void *pp = nullptr, *tp = nullptr;
+        int64_t axes = 1, max_pos = 0, rot = 0;
+        if ((a[10] == Py_None) != (a[11] == Py_None)) refuse(PyExc_ValueError, "positions and cos_sin go together");
+        const uint8_t *pairs = nullptr;
+        if (a[10] != Py_None) {
+            const at::Tensor &pos = tensor(a[10], "positions must be a tensor"), &tab = tensor(a[11], "cos_sin must be a tensor");
+            if (pos.dim() < 1 || pos.dim() > 2 || pos.size(-1) != T)
+                refuse(PyExc_ValueError, "positions must be [T] or [axes, T]");
+            if (tab.scalar_type() != at::kFloat || tab.dim() != 2 || tab.size(1) == 0)
+                refuse(PyExc_TypeError, "cos_sin must be a float32 [max_pos, rot_dim] table");
+            int32(pos, "positions must be int32");
+            dev.add(pos);
+            dev.add(tab);
+            axes = pos.dim() == 1 ? 1 : pos.size(0), max_pos = tab.size(0), rot = tab.size(1);
+            pp = contiguous(pos), tp = contiguous(tab);
+        }
+        if (a[12] != Py_None) {
+            if (!PyBytes_CheckExact(a[12]) || PyBytes_GET_SIZE(a[12]) != rot / 2)
+                refuse(PyExc_ValueError, "pair_axis must be rot_dim / 2 bytes");
+            pairs = reinterpret_cast<const uint8_t *>(PyBytes_AS_STRING(a[12]));
+        }
+        const int interleaved = PyObject_IsTrue(a[13]);
+        if (interleaved < 0) throw Refused{};
+        float *scale[2] = {nullptr, nullptr};
+        for (int i = 0; i < 2; ++i) {
+            if (a[14 + i] == Py_None) {
+                if (q8) refuse(PyExc_ValueError, "8-bit pools have k_scale and v_scale");
+                continue;
+            }
+            if (!q8) refuse(PyExc_ValueError, "k_scale and v_scale go with 8-bit pools");
+            scale[i] = scales_of(a[14 + i], NB, Hkv, bs, dev);
+        }
+        int32_t *err = error_word(a[16], dev);
+        dev.check();
+        const int64_t sqo = token_stride(q_out, T, Hq, D, "q_out: the heads of a token must be contiguous"), sq = token_stride(q, T, Hq, D, "q: the heads of a token must be contiguous"),
+                      sk = token_stride(k, T, Hkv, D, "k: the heads of a token must be contiguous"), sv = token_stride(v, T, Hkv, D, "v: the heads of a token must be contiguous");
+        const void *kcp = contiguous(kc), *vcp = contiguous(vc), *sp = contiguous(slots);
+        const cudaStream_t stream = stream_of(a[17], dev.index);
+        const int axesi = small(axes), mp = small(max_pos), Ti = small(T), NBi = small(NB), bsi = small(bs), Hqi = small(Hq),
+                  Hkvi = small(Hkv), Di = small(D), roti = small(rot);
+        return run(dev.index, [&] {
+            return call_norm_rope_store_kv(q_out.data_ptr(), sqo, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
+                                           const_cast<void *>(kcp), const_cast<void *>(vcp), scale[0], scale[1],
+                                           static_cast<const int32_t *>(sp), weight[0], weight[1], static_cast<float>(eps),
+                                           static_cast<const int32_t *>(pp), axesi, pairs, static_cast<const float *>(tp), mp,
+                                           roti, interleaved, Ti, NBi, bsi, Hqi, Hkvi, Di, dt, q8 ? PA_E4M3 : dt, err, stream);
+        });
+    });
+}
+
 // out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_seqlen_q, scale, window, workspace, err, stream
 PyObject *chunk_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 13, [&] {
@@ -298,11 +396,62 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of pa_rope_store_kv, pa_chunk_attn, pa_sample)
+// next_tokens, accepted, tokens, probs, cu_seqlens_q, u, draft_probs, err, stream
+PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 9, [&] {
+        bound(call_verify);
+        const at::Tensor &next = tensor(a[0], "next_tokens must be a tensor"), &accepted = tensor(a[1], "accepted must be a tensor"),
+                         &tokens = tensor(a[2], "tokens must be a tensor"), &probs = tensor(a[3], "probs must be a tensor"),
+                         &cu = tensor(a[4], "cu_seqlens_q must be a tensor"), &u = tensor(a[5], "u must be a tensor");
+        if (probs.dim() != 2) refuse(PyExc_ValueError, "probs must be [total_q, V]");
+        const int64_t Tq = probs.size(0), V = probs.size(1);
+        if (accepted.dim() != 1 || cu.dim() != 1 || cu.size(0) != accepted.size(0) + 1)
+            refuse(PyExc_ValueError, "accepted must be [S], cu_seqlens_q [S + 1]");
+        if (next.dim() != 1 || next.size(0) != Tq || tokens.dim() != 1 || tokens.size(0) != Tq || u.dim() != 1 || u.size(0) != Tq)
+            refuse(PyExc_ValueError, "next_tokens, tokens and u must be [total_q]");
+        const pa_dtype dt = probs.scalar_type() == at::kFloat ? PA_F32 : dtype_of(probs);
+        int32(next, "next_tokens must be int32");
+        int32(accepted, "accepted must be int32");
+        int32(tokens, "tokens must be int32");
+        int32(cu, "cu_seqlens_q must be int32");
+        if (u.scalar_type() != at::kFloat) refuse(PyExc_TypeError, "u must be float32");
+        Device dev;
+        for (const at::Tensor *t : {&probs, &next, &accepted, &tokens, &cu, &u}) dev.add(*t);
+        const auto row_stride = [&](const at::Tensor &t) {
+            if (t.stride(1) != 1 && V > 1) refuse(PyExc_ValueError, "a row of probabilities must be contiguous");
+            return Tq > 1 ? t.stride(0) : V;
+        };
+        const int64_t ps = row_stride(probs);
+        const void *dp = nullptr;
+        int64_t ds = 0;
+        if (a[6] != Py_None) {
+            const at::Tensor &d = tensor(a[6], "draft_probs must be a tensor");
+            if (d.sizes() != probs.sizes()) refuse(PyExc_ValueError, "draft_probs must have the shape of probs");
+            if (d.scalar_type() != probs.scalar_type()) refuse(PyExc_TypeError, "draft_probs must have the dtype of probs");
+            dev.add(d);
+            ds = row_stride(d);
+            dp = d.data_ptr();
+        }
+        int32_t *err = error_word(a[7], dev);
+        dev.check();
+        const void *np = contiguous(next), *ap = contiguous(accepted), *tp = contiguous(tokens), *cp = contiguous(cu),
+                   *up = contiguous(u);
+        const cudaStream_t stream = stream_of(a[8], dev.index);
+        const int Si = small(accepted.size(0)), Tqi = small(Tq), Vi = small(V);
+        return run(dev.index, [&] {
+            return call_verify(static_cast<int32_t *>(const_cast<void *>(np)), static_cast<int32_t *>(const_cast<void *>(ap)),
+                               static_cast<const int32_t *>(tp), probs.data_ptr(), ps, dp, ds, static_cast<const int32_t *>(cp),
+                               static_cast<const float *>(up), Si, Tqi, Vi, dt, err, stream);
+        });
+    });
+}
+
+// bind(addresses of the entry points, in the order below)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 3, [&]() -> PyObject * {
-        uintptr_t at[3];
-        for (int i = 0; i < 3; ++i) {
+    constexpr int kEntries = 5;
+    return guarded(n, kEntries, [&]() -> PyObject * {
+        uintptr_t at[kEntries];
+        for (int i = 0; i < kEntries; ++i) {
             at[i] = static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(a[i]));
             if (PyErr_Occurred()) throw Refused{};
             if (!at[i]) refuse(PyExc_ValueError, "an entry point has no address");
@@ -310,6 +459,8 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
         call_rope_store_kv = reinterpret_cast<decltype(call_rope_store_kv)>(at[0]);
         call_chunk_attn = reinterpret_cast<decltype(call_chunk_attn)>(at[1]);
         call_sample = reinterpret_cast<decltype(call_sample)>(at[2]);
+        call_norm_rope_store_kv = reinterpret_cast<decltype(call_norm_rope_store_kv)>(at[3]);
+        call_verify = reinterpret_cast<decltype(call_verify)>(at[4]);
         Py_RETURN_NONE;
     });
 }
@@ -323,6 +474,8 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"pa_rope_store_kv", fast(rope_store_kv), METH_FASTCALL, nullptr},
                          {"pa_chunk_attn", fast(chunk_attn), METH_FASTCALL, nullptr},
                          {"pa_sample", fast(sample), METH_FASTCALL, nullptr},
+                         {"pa_norm_rope_store_kv", fast(norm_rope_store_kv), METH_FASTCALL, nullptr},
+                         {"pa_verify", fast(verify), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pa_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

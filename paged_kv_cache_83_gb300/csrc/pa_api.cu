@@ -64,6 +64,57 @@ HostStage host_stage(int B, int Hq, int Hkv, int D, int max_blocks, size_t ws_by
     return s;
 }
 
+// The checks of a step's rows that the calls of rotation + append share. with_norm: rot_dim may be 0 (no rotation, no
+// positions and no table then), and a row belongs to one warp. empty: nothing to do.
+pa_status check_rope_store(const pa::RopeStoreArgs &a, bool with_norm, bool &empty) {
+    const bool turns = !with_norm || a.rot_dim != 0;
+    if (a.T < 0 || a.num_blocks < 0 || a.block_size < 1 || a.Hq < 1 || a.Hkv < 1 || a.D < 1 || a.rot_dim < 0 ||
+        (turns && (a.n_axes < 1 || a.max_pos < 0)))
+        return PA_ERR_SHAPE;
+    if (a.D % 8 || a.rot_dim % 16 || (turns && (a.rot_dim < 16 || a.n_axes > 4)) || a.rot_dim > 256) return PA_ERR_UNSUPPORTED;
+    if (with_norm && a.D > 512) return PA_ERR_UNSUPPORTED;
+    if (a.rot_dim > a.D) return PA_ERR_SHAPE;
+    const int64_t qw = static_cast<int64_t>(a.Hq) * a.D, kw = static_cast<int64_t>(a.Hkv) * a.D;
+    // 2^24 elements a token and 2^40 a stride keep every byte offset below in 64 bits
+    if (a.Hq > 65535 || a.Hkv > 65535 || qw > (1 << 24) || kw > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    empty = a.T == 0;
+    if (empty) return PA_OK;
+    if (!a.q_out || !a.q || !a.k || !a.v || !a.k_cache || !a.v_cache || !a.slot_mapping ||
+        (turns && (!a.positions || !a.cos_sin)))
+        return PA_ERR_NULL;
+    if (a.q_stride < qw || a.q_out_stride < qw || a.k_stride < kw || a.v_stride < kw) return PA_ERR_SHAPE;
+    if ((a.q_stride | a.q_out_stride | a.k_stride | a.v_stride) % 8) return PA_ERR_UNSUPPORTED;
+    const int64_t most = int64_t{1} << 40;
+    if (a.q_stride > most / a.T || a.q_out_stride > most / a.T || a.k_stride > most / a.T || a.v_stride > most / a.T)
+        return PA_ERR_UNSUPPORTED;
+    if (!aligned16(a.q_out) || !aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.k_cache) ||
+        !aligned16(a.v_cache) || (turns && !aligned16(a.cos_sin)))
+        return PA_ERR_UNSUPPORTED;
+    for (int i = 0; turns && a.pair_axis && i < a.rot_dim / 2; ++i)
+        if (a.pair_axis[i] >= a.n_axes) return PA_ERR_SHAPE;
+    // threads of the launch: a row takes (D + 15) / 16 + 1 of them at most, or with norms the power of two from there
+    int per_row = (a.D + 15) / 16 + 1;
+    if (with_norm)
+        for (per_row = 1; per_row < (a.D + 15) / 16 + 1;) per_row *= 2;
+    if (static_cast<long long>(a.T) * (a.Hq + 2ll * a.Hkv) * per_row / 256 > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
+    // q_out is q itself or lies clear of everything that is read; in place, k and v lie clear of q, or beside it in the
+    // tokens of one tensor
+    auto span_meets = [&](const void *p, int64_t stride, int64_t width) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.q_out), y = reinterpret_cast<uintptr_t>(p);
+        return x < y + 2 * ((a.T - 1) * stride + width) && y < x + 2 * ((a.T - 1) * a.q_out_stride + qw);
+    };
+    auto beside_q = [&](const void *p, int64_t stride) {
+        const int64_t off = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.q))) / 2;
+        const int64_t d = (off % stride + stride) % stride;
+        return stride == a.q_stride && d >= qw && d + kw <= stride;
+    };
+    const bool in_place = a.q_out == a.q && a.q_out_stride == a.q_stride;
+    if (!in_place && span_meets(a.q, a.q_stride, qw)) return PA_ERR_UNSUPPORTED;
+    if (span_meets(a.k, a.k_stride, kw) && !(in_place && beside_q(a.k, a.k_stride))) return PA_ERR_UNSUPPORTED;
+    if (span_meets(a.v, a.v_stride, kw) && !(in_place && beside_q(a.v, a.v_stride))) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -104,71 +155,45 @@ pa_status pa_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int
                            int num_blocks, int block_size, int Hq, int Hkv, int D, pa_dtype dtype,
                            int32_t *err, cudaStream_t stream) {
     if (!dtype_ok(dtype)) return PA_ERR_DTYPE;
-    if (T < 0 || num_blocks < 0 || block_size < 1 || Hq < 1 || Hkv < 1 || D < 1 || n_axes < 1 || max_pos < 0 ||
-        rot_dim < 0 || (interleaved != 0 && interleaved != 1))
-        return PA_ERR_SHAPE;
-    if (D % 8 || rot_dim % 16 || rot_dim < 16 || rot_dim > 256 || n_axes > 4) return PA_ERR_UNSUPPORTED;
-    if (rot_dim > D) return PA_ERR_SHAPE;
-    const int64_t qw = static_cast<int64_t>(Hq) * D, kw = static_cast<int64_t>(Hkv) * D;
-    // 2^24 elements a token and 2^40 a stride keep every byte offset below in 64 bits
-    if (Hq > 65535 || Hkv > 65535 || qw > (1 << 24) || kw > (1 << 24)) return PA_ERR_UNSUPPORTED;
-    if (T == 0) return PA_OK;
-    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions || !cos_sin)
-        return PA_ERR_NULL;
-    if (q_stride < qw || q_out_stride < qw || k_stride < kw || v_stride < kw) return PA_ERR_SHAPE;
-    if ((q_stride | q_out_stride | k_stride | v_stride) % 8) return PA_ERR_UNSUPPORTED;
-    const int64_t most = int64_t{1} << 40;
-    if (q_stride > most / T || q_out_stride > most / T || k_stride > most / T || v_stride > most / T)
-        return PA_ERR_UNSUPPORTED;
-    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
-        !aligned16(v_cache) || !aligned16(cos_sin))
-        return PA_ERR_UNSUPPORTED;
-    for (int i = 0; pair_axis && i < rot_dim / 2; ++i)
-        if (pair_axis[i] >= n_axes) return PA_ERR_SHAPE;
-    if (static_cast<long long>(T) * (Hq + 2ll * Hkv) * ((D + 15) / 16 + 1) / 256 > INT_MAX / 2) return PA_ERR_UNSUPPORTED;
-    // q_out is q itself or lies clear of everything that is read; in place, k and v lie clear of q, or beside it in the
-    // tokens of one tensor
-    auto span_meets = [&](const void *p, int64_t stride, int64_t width) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(q_out), b = reinterpret_cast<uintptr_t>(p);
-        return a < b + 2 * ((T - 1) * stride + width) && b < a + 2 * ((T - 1) * q_out_stride + qw);
-    };
-    auto beside_q = [&](const void *p, int64_t stride) {
-        const int64_t off = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(q))) / 2;
-        const int64_t d = (off % stride + stride) % stride;
-        return stride == q_stride && d >= qw && d + kw <= stride;
-    };
-    const bool in_place = q_out == q && q_out_stride == q_stride;
-    if (!in_place && span_meets(q, q_stride, qw)) return PA_ERR_UNSUPPORTED;
-    if (span_meets(k, k_stride, kw) && !(in_place && beside_q(k, k_stride))) return PA_ERR_UNSUPPORTED;
-    if (span_meets(v, v_stride, kw) && !(in_place && beside_q(v, v_stride))) return PA_ERR_UNSUPPORTED;
-    pa::RopeStoreArgs a{};
-    a.q_out = q_out;
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.q_out_stride = q_out_stride;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.slot_mapping = slot_mapping;
-    a.positions = positions;
-    a.pair_axis = pair_axis;
-    a.cos_sin = cos_sin;
-    a.n_axes = n_axes;
-    a.max_pos = max_pos;
-    a.rot_dim = rot_dim;
-    a.interleaved = interleaved != 0;
-    a.T = T;
-    a.num_blocks = num_blocks;
-    a.block_size = block_size;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
-    a.D = D;
-    a.dtype = dtype;
-    a.err = err;
+    const pa::RopeStoreArgs a{q_out,   q,       k,           v,       q_out_stride, q_stride,         k_stride,
+                              v_stride, k_cache, v_cache,    slot_mapping, positions, pair_axis,       cos_sin,
+                              n_axes,  max_pos, rot_dim,     interleaved == 1, T,     num_blocks,      block_size,
+                              Hq,      Hkv,     D,           dtype,   err};
+    if (interleaved != 0 && interleaved != 1) return PA_ERR_SHAPE;
+    bool empty = false;
+    const pa_status st = check_rope_store(a, false, empty);
+    if (st != PA_OK || empty) return st;
     return from_cuda(pa::launch_rope_store_kv(a, stream));
+}
+
+pa_status pa_norm_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                                const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                const int32_t *slot_mapping, const void *q_weight, const void *k_weight,
+                                float eps, const int32_t *positions, int n_axes,
+                                const uint8_t *pair_axis, const float *cos_sin, int max_pos, int rot_dim,
+                                int interleaved, int T, int num_blocks, int block_size, int Hq, int Hkv,
+                                int D, pa_dtype dtype, pa_dtype cache_dtype, int32_t *err,
+                                cudaStream_t stream) {
+    if (!dtype_ok(dtype) || (cache_dtype != dtype && cache_dtype != PA_E4M3)) return PA_ERR_DTYPE;
+    pa::NormRopeStoreArgs n{};
+    n.rows = {q_out,   q,       k,           v,       q_out_stride, q_stride,         k_stride,
+              v_stride, k_cache, v_cache,    slot_mapping, positions, pair_axis,       cos_sin,
+              n_axes,  max_pos, rot_dim,     interleaved == 1, T,     num_blocks,      block_size,
+              Hq,      Hkv,     D,           dtype,   err};
+    n.q_weight = q_weight, n.k_weight = k_weight, n.eps = eps;
+    n.q8 = cache_dtype == PA_E4M3;
+    n.k_scale = k_scale, n.v_scale = v_scale;
+    if (interleaved != 0 && interleaved != 1) return PA_ERR_SHAPE;
+    if (!(eps >= 0.f && eps <= FLT_MAX)) return PA_ERR_SHAPE;
+    bool empty = false;
+    const pa_status st = check_rope_store(n.rows, true, empty);
+    if (st != PA_OK || empty) return st;
+    if (n.q8 && (!k_scale || !v_scale)) return PA_ERR_NULL;
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return PA_ERR_UNSUPPORTED;
+    if (n.q8 && ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)) return PA_ERR_UNSUPPORTED;
+    if (n.q8 && static_cast<long long>(num_blocks) * block_size > INT_MAX) return PA_ERR_UNSUPPORTED;
+    return from_cuda(pa::launch_norm_rope_store_kv(n, stream));
 }
 
 size_t pa_decode_workspace_size(int B, int Hq, int Hkv, int D, int max_blocks_per_seq,
@@ -465,6 +490,30 @@ pa_status pa_sample(int32_t *tokens, const void *logits, int64_t row_stride, int
     if (reinterpret_cast<uintptr_t>(logits) % (dtype == PA_F32 ? 4 : 2)) return PA_ERR_UNSUPPORTED;
     pa::SampleArgs a{tokens, logits, row_stride, B, V, dtype, u, temperature, top_k, top_p, min_p, err};
     return from_cuda(pa::launch_sample(a, stream));
+}
+
+pa_status pa_verify(int32_t *next_tokens, int32_t *accepted, const int32_t *tokens, const void *probs,
+                    int64_t probs_stride, const void *draft_probs, int64_t draft_stride,
+                    const int32_t *cu_seqlens_q, const float *u, int S, int total_q, int V,
+                    pa_dtype dtype, int32_t *err, cudaStream_t stream) {
+    if (!dtype_ok(dtype) && dtype != PA_F32) return PA_ERR_DTYPE;
+    if (S < 0 || total_q < 0 || V < 1 || probs_stride < V || (draft_probs && draft_stride < V)) return PA_ERR_SHAPE;
+    if (V > pa::kSampleMaxVocab || S > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    if (S == 0) return PA_OK;
+    if (!accepted || !cu_seqlens_q) return PA_ERR_NULL;
+    if (total_q > 0) {
+        if (probs_stride > (int64_t{1} << 40) / total_q || (draft_probs && draft_stride > (int64_t{1} << 40) / total_q))
+            return PA_ERR_UNSUPPORTED;
+        if (!next_tokens || !tokens || !probs || !u) return PA_ERR_NULL;
+        const uintptr_t bits = reinterpret_cast<uintptr_t>(probs) | reinterpret_cast<uintptr_t>(draft_probs);
+        if (bits % (dtype == PA_F32 ? 4 : 2)) return PA_ERR_UNSUPPORTED;
+        // every CTA of a sequence reads its drafts, one writes the tokens
+        const uintptr_t o = reinterpret_cast<uintptr_t>(next_tokens), x = reinterpret_cast<uintptr_t>(tokens);
+        if ((o < x ? x - o : o - x) < static_cast<uint64_t>(total_q) * 4) return PA_ERR_UNSUPPORTED;
+    }
+    const pa::VerifyArgs a{next_tokens, accepted, tokens, probs, draft_probs, probs_stride, draft_stride,
+                           cu_seqlens_q, u,       S,      total_q, V,       dtype,        err};
+    return from_cuda(pa::launch_verify(a, stream));
 }
 
 }  // extern "C"

@@ -50,6 +50,16 @@ struct RopeStoreArgs {
 };
 cudaError_t launch_rope_store_kv(const RopeStoreArgs &a, cudaStream_t stream);
 
+// The same with norms and an optional 8-bit cache (norm_rope_store_kv.cu). A weight of nullptr: no norm.
+struct NormRopeStoreArgs {
+    RopeStoreArgs rows;  // rot_dim 0: no rotation
+    const void *q_weight, *k_weight;
+    float eps;
+    bool q8;
+    float *k_scale, *v_scale;
+};
+cudaError_t launch_norm_rope_store_kv(const NormRopeStoreArgs &a, cudaStream_t stream);
+
 // ------------------------------------------------------------------------------------------
 // Decode: one persistent CTA per SM streams an equal share of the (sequence, kv head, tile)
 // space; pieces of a context shared by two CTAs are combined by a small merge kernel.
@@ -138,6 +148,21 @@ struct SampleArgs {
 // the longest rows that are tested; eight CTAs' shared memory would hold some 417,000 logits
 constexpr int kSampleMaxVocab = 1 << 18;
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
+
+// ------------------------------------------------------------------------------------------
+// Verification of drafted tokens (verify.cu).
+struct VerifyArgs {
+    int32_t *next_tokens, *accepted;
+    const int32_t *tokens;
+    const void *probs, *draft_probs;
+    long long p_stride, q_stride;  // elements
+    const int32_t *cu_q;
+    const float *u;
+    int S, total_q, V;
+    pa_dtype dtype;  // PA_F16, PA_BF16 or PA_F32
+    int32_t *err;
+};
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t stream);
 
 inline int log2_if_pow2(int x) {
     if (x <= 0 || (x & (x - 1))) return -1;
