@@ -412,6 +412,39 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
                         cudaStream_t stream);
 
 /*
+ * pa_chunk_attn_q8: pa_chunk_attn over 8-bit pools, as pa_norm_rope_store_kv writes them: single tokens, drafts, pieces of
+ * prompts, mixed, optionally within a sliding window.
+ *
+ * Source: as pa_chunk_attn.
+ *
+ *   K_j = k_scale_j * (k_cache row j),  V_j = v_scale_j * (v_cache row j) of the sequence and kv head, each with its own scale;
+ *   everything else as pa_chunk_attn.
+ *
+ * The e4m3 rows are operands of the tensor cores as they lie there; queries and softmax weights meet them as sums of e4m3 numbers.
+ * Scores, references, sums and accumulators are fp32. A query's element is exact where its magnitude is above 2^-14 of the
+ * largest of its row, below that to 2^-24 of the largest; a weight (times its value's scale) is rounded to within 2^-8 of itself, and
+ * to within 2^-19 of the largest that was seen when the first keys of a piece were; the output is rounded once.
+ *
+ * k_cache, v_cache  e4m3 pools [num_blocks, block_size, Hkv, D].
+ * k_scale, v_scale  fp32 [num_blocks, Hkv, block_size], 16-byte aligned. Positive; k_scale from 2^-126, v_scale from 2^-90 to 2^60. A
+ *               NaN or an infinity (a row that held one) makes the output of what sees it NaN.
+ * q, out, dtype fp16 or bf16; out may be q itself.
+ * max_seqlen_q  chooses the kernel for the whole call: up to 16 query rows a kv head (tokens * Hq / Hkv), up to 32, or
+ *               items of 64 of them.
+ * workspace     device scratch of at least pa_chunk_attn_q8_workspace_size(S, Hq, Hkv, D) bytes (10 MB on a GB300 at D = 128, 5 MB at
+ *               64). Its contents on entry do not matter; calls that share a workspace must not overlap on the GPU.
+ * A bad table entry leaves zero rows for up to 64 / (Hq / Hkv) tokens (cf. pa_chunk_attn). All else as pa_chunk_attn.
+ */
+size_t pa_chunk_attn_q8_workspace_size(int S, int Hq, int Hkv, int D);
+pa_status pa_chunk_attn_q8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                           int max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                           const int32_t *context_lens, int S, int total_q, int max_seqlen_q,
+                           int window, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                           float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                           int32_t *err, cudaStream_t stream);
+
+/*
  * pa_sample: one token per row of logits, from a given random number per row.
  *
  * Source: smzdm nano-vLLM deep dive (the sampler with each request's temperature); "nano-vLLM Part 4"

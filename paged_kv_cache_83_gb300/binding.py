@@ -25,7 +25,8 @@ PA_F16, PA_BF16, PA_F32, PA_E4M3 = 0, 1, 2, 3
 PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION, PA_DEVERR_ROW = 1, 2, 4, 8, 16, 32
 EXPORTS = ("pa_store_kv", "pa_rope_store_kv", "pa_decode_workspace_size", "pa_decode", "pa_store_decode",
            "pa_store_decode_host", "pa_store_decode_host_workspace_size", "pa_store_decode_host_layout",
-           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample", "pa_norm_rope_store_kv", "pa_verify", "pa_decode_noalloc",
+           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample", "pa_norm_rope_store_kv", "pa_verify", "pa_chunk_attn_q8",
+           "pa_chunk_attn_q8_workspace_size", "pa_decode_noalloc",
            "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
            "pa_bm_destroy", "pa_bm_allocate", "pa_bm_can_allocate", "pa_bm_append",
            "pa_bm_release", "pa_bm_block_table", "pa_bm_num_tokens", "pa_bm_num_free",
@@ -82,6 +83,10 @@ def load(path: Path | str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_norm_rope_store_kv.argtypes = [P, L, P, L, P, L, P, L, P, P, P, P, P, P, P, F, P, I, P, P, I, I, I, I, I, I, I,
                                           I, I, I, I, P, P]
     lib.pa_norm_rope_store_kv.restype = I
+    lib.pa_chunk_attn_q8_workspace_size.argtypes = [I, I, I, I]
+    lib.pa_chunk_attn_q8_workspace_size.restype = Z
+    lib.pa_chunk_attn_q8.argtypes = [P, P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, F, I, P, Z, P, P]
+    lib.pa_chunk_attn_q8.restype = I
     lib.pa_verify.argtypes = [P, P, P, P, L, P, L, P, P, I, I, I, I, P, P]
     lib.pa_verify.restype = I
     lib.pa_decode_noalloc.argtypes = [P, P, P, P, P, I, P, I, I, I, I, I, I, F, I, P, P]
@@ -124,7 +129,8 @@ def _load_args():
     mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_args", loader))
     loader.exec_module(mod)
     mod.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-               for name in ("pa_rope_store_kv", "pa_chunk_attn", "pa_sample", "pa_norm_rope_store_kv", "pa_verify")))
+               for name in ("pa_rope_store_kv", "pa_chunk_attn", "pa_sample", "pa_norm_rope_store_kv", "pa_verify",
+                            "pa_chunk_attn_q8")))
     _args = mod
     return mod
 
@@ -393,6 +399,21 @@ def pa_chunk_attn(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_
                                                    max_seqlen_q, scale, window, workspace, err, stream)
     if status:
         raise PagedAttnError("pa_chunk_attn", status)
+
+
+def pa_chunk_attn_q8_workspace_size(S: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of scratch pa_chunk_attn_q8 needs on the current device for these sizes."""
+    return int(load().pa_chunk_attn_q8_workspace_size(int(S), int(Hq), int(Hkv), int(D)))
+
+
+def pa_chunk_attn_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, cu_seqlens_q, context_lens, max_seqlen_q: int,
+                     scale: float, window: int = 0, workspace=None, err=None, stream=None) -> None:
+    """pa_chunk_attn over pools of 8 bits (float8_e4m3fn [NB, bs, Hkv, D], with k_scale, v_scale float32 [NB, Hkv, bs]), as
+    pa_norm_rope_store_kv writes them: one or more new tokens of each sequence."""
+    status = (_args or _load_args()).pa_chunk_attn_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, cu_seqlens_q,
+                                                      context_lens, max_seqlen_q, scale, window, workspace, err, stream)
+    if status:
+        raise PagedAttnError("pa_chunk_attn_q8", status)
 
 
 def pa_sample(tokens, logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None, err=None,

@@ -25,6 +25,7 @@ decltype(&::pa_chunk_attn) call_chunk_attn = nullptr;
 decltype(&::pa_sample) call_sample = nullptr;
 decltype(&::pa_norm_rope_store_kv) call_norm_rope_store_kv = nullptr;
 decltype(&::pa_verify) call_verify = nullptr;
+decltype(&::pa_chunk_attn_q8) call_chunk_attn_q8 = nullptr;
 
 struct Refused {  // a Python exception has been set
 };
@@ -305,13 +306,20 @@ PyObject *norm_rope_store_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// out, q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_seqlen_q, scale, window, workspace, err, stream
+// out, q, k_cache, v_cache, [k_scale, v_scale,] block_tables, cu_seqlens_q, context_lens, max_seqlen_q, scale, window, workspace,
+// err, stream; the scales over an 8-bit cache
+template <bool kQ8>
 PyObject *chunk_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 13, [&] {
-        bound(call_chunk_attn);
+    return guarded(n, kQ8 ? 15 : 13, [&] {
+        if constexpr (kQ8)
+            bound(call_chunk_attn_q8);
+        else
+            bound(call_chunk_attn);
         const at::Tensor &out = tensor(a[0], "out must be a tensor"), &q = tensor(a[1], "q must be a tensor"),
-                         &kc = tensor(a[2], "k_cache must be a tensor"), &vc = tensor(a[3], "v_cache must be a tensor"),
-                         &bt = tensor(a[4], "block_tables must be a tensor"), &cu = tensor(a[5], "cu_seqlens_q must be a tensor"),
+                         &kc = tensor(a[2], "k_cache must be a tensor"), &vc = tensor(a[3], "v_cache must be a tensor");
+        PyObject *const *const scales = a + 4;
+        if constexpr (kQ8) a += 2;
+        const at::Tensor &bt = tensor(a[4], "block_tables must be a tensor"), &cu = tensor(a[5], "cu_seqlens_q must be a tensor"),
                          &ctx = tensor(a[6], "context_lens must be a tensor");
         if (kc.dim() != 4 || q.dim() != 3 || bt.dim() != 2 || ctx.dim() != 1 || cu.dim() != 1)
             refuse(PyExc_ValueError, "shape mismatch");
@@ -320,9 +328,10 @@ PyObject *chunk_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (q.size(2) != D || out.sizes() != q.sizes() || vc.sizes() != kc.sizes() || bt.size(0) != S || cu.size(0) != S + 1)
             refuse(PyExc_ValueError, "shape mismatch");
         const pa_dtype dt = dtype_of(q);
-        const auto type = q.scalar_type();
-        if (out.scalar_type() != type || kc.scalar_type() != type || vc.scalar_type() != type)
-            refuse(PyExc_TypeError, "q, out and the pools must share a dtype");
+        const auto type = q.scalar_type(), cached = kQ8 ? at::kFloat8_e4m3fn : type;
+        if (out.scalar_type() != type || kc.scalar_type() != cached || vc.scalar_type() != cached)
+            refuse(PyExc_TypeError, kQ8 ? "q and out must share a dtype, and the pools be float8_e4m3fn"
+                                        : "q, out and the pools must share a dtype");
         int32(bt, "block_tables must be int32");
         int32(cu, "cu_seqlens_q must be int32");
         int32(ctx, "context_lens must be int32");
@@ -340,6 +349,8 @@ PyObject *chunk_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
             ws = const_cast<void *>(contiguous(w));
             ws_bytes = static_cast<size_t>(w.numel()) * w.element_size();
         }
+        const float *ks = nullptr, *vs = nullptr;
+        if constexpr (kQ8) ks = scales_of(scales[0], NB, Hkv, bs, dev), vs = scales_of(scales[1], NB, Hkv, bs, dev);
         int32_t *err = error_word(a[11], dev);
         dev.check();
         const void *op = contiguous(out), *qp = contiguous(q), *kcp = contiguous(kc), *vcp = contiguous(vc),
@@ -348,9 +359,15 @@ PyObject *chunk_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int maxb = small(bt.size(1)), Si = small(S), Tqi = small(Tq), Hqi = small(Hq), Hkvi = small(Hkv), Di = small(D),
                   bsi = small(bs), NBi = small(NB);
         return run(dev.index, [&] {
-            return call_chunk_attn(const_cast<void *>(op), qp, kcp, vcp, static_cast<const int32_t *>(btp), maxb,
-                                 static_cast<const int32_t *>(cup), static_cast<const int32_t *>(cxp), Si, Tqi, max_q, window,
-                                 Hqi, Hkvi, Di, bsi, NBi, static_cast<float>(scale), dt, ws, ws_bytes, err, stream);
+            if constexpr (kQ8)
+                return call_chunk_attn_q8(const_cast<void *>(op), qp, kcp, vcp, ks, vs, static_cast<const int32_t *>(btp), maxb,
+                                          static_cast<const int32_t *>(cup), static_cast<const int32_t *>(cxp), Si, Tqi, max_q,
+                                          window, Hqi, Hkvi, Di, bsi, NBi, static_cast<float>(scale), dt, ws, ws_bytes, err,
+                                          stream);
+            else
+                return call_chunk_attn(const_cast<void *>(op), qp, kcp, vcp, static_cast<const int32_t *>(btp), maxb,
+                                       static_cast<const int32_t *>(cup), static_cast<const int32_t *>(cxp), Si, Tqi, max_q,
+                                       window, Hqi, Hkvi, Di, bsi, NBi, static_cast<float>(scale), dt, ws, ws_bytes, err, stream);
         });
     });
 }
@@ -448,7 +465,7 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // bind(addresses of the entry points, in the order below)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    constexpr int kEntries = 5;
+    constexpr int kEntries = 6;
     return guarded(n, kEntries, [&]() -> PyObject * {
         uintptr_t at[kEntries];
         for (int i = 0; i < kEntries; ++i) {
@@ -461,6 +478,7 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
         call_sample = reinterpret_cast<decltype(call_sample)>(at[2]);
         call_norm_rope_store_kv = reinterpret_cast<decltype(call_norm_rope_store_kv)>(at[3]);
         call_verify = reinterpret_cast<decltype(call_verify)>(at[4]);
+        call_chunk_attn_q8 = reinterpret_cast<decltype(call_chunk_attn_q8)>(at[5]);
         Py_RETURN_NONE;
     });
 }
@@ -472,7 +490,8 @@ PyCFunction fast(F *f) {
 
 PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"pa_rope_store_kv", fast(rope_store_kv), METH_FASTCALL, nullptr},
-                         {"pa_chunk_attn", fast(chunk_attn), METH_FASTCALL, nullptr},
+                         {"pa_chunk_attn", fast(chunk_attn<false>), METH_FASTCALL, nullptr},
+                         {"pa_chunk_attn_q8", fast(chunk_attn<true>), METH_FASTCALL, nullptr},
                          {"pa_sample", fast(sample), METH_FASTCALL, nullptr},
                          {"pa_norm_rope_store_kv", fast(norm_rope_store_kv), METH_FASTCALL, nullptr},
                          {"pa_verify", fast(verify), METH_FASTCALL, nullptr},

@@ -1,0 +1,872 @@
+// chunk_attn_q8.cu: causal attention of one or more new tokens of each sequence over a paged cache of 8 bits
+// (pa_chunk_attn_q8) on the 5th-generation tensor cores.
+//
+// Source: as chunk_attn.cu ("nano-vLLM Part 4", section 3; smzdm nano-vLLM deep dive, "GPU执行优化").
+//
+// The mathematics: K_j = ks_j K8_j and V_j = vs_j V8_j with e4m3 rows and a scale for each row and kv head. The e4m3 rows go
+// to the tensor cores as they lie in the cache, without a conversion: keys are the 128 rows, query rows the
+// columns, as in chunk_attn_narrow.cu,
+//   S^T = K8 Q^T,   O^T += V8^T W^T,
+// and what meets them is split into e4m3 pieces, side by side as further columns of the same instruction:
+//   q = 2^e (q0 + q1 / 32 [+ q2 / 1024]): two pieces hold a bf16 number (8 bits) exactly, three an fp16 number (11 bits),
+//     where its magnitude is above 2^-14 of its row's largest; below that the error is at most 2^-24 (2^-29) of the largest;
+//   w = w0 + w1 / 32, a weight of the softmax, with an error of at most 2^-8 of itself (bf16's is 2^-9) and 2^-16 absolute.
+// A softmax thread owns one key, so that both scales are one number a thread. The values' scale goes into the
+// exponent: x_j = s_j + log2 vs_j, w_j = 2^(x_j - m), O = sum w_j V8_j, and the sum takes w_j / vs_j = 2^(s_j - m). The reference m is
+// 4 below the largest x of the first tile and moves when some x exceeds it by more than 8: a w is at most 256,
+// below e4m3's 448, and what is smaller than 2^-16 beside a largest w of 16 counts for nothing.
+//
+// Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. The loads run ahead in rings of tiles; two streams of softmax
+// warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a
+// segment. With more than 32 query rows a kv head an item is at most 64 of them, and the streams take half of the columns
+// each, of every key tile: a long chunk is many items, whose keys come from L2, and is bound by the softmax (exponentials
+// and conversions).
+//
+//   warp 3      scheduler, as in chunk_attn.cu; splits each segment's queries into pieces
+//   warp 0      producer: K and V tiles of the streams in turn, the scales with the K tile
+//   warps 1, 2  one MMA issuer per stream
+//   warps 4-7   softmax of stream A (tiles 0, 2, ... of a segment), warps 8-11 of stream B (1, 3, ...)
+//   TMEM columns: S_A, S_B (pieces x NT each), O_A, O_B (2 NT each); lanes are keys in S and head elements in O.
+#include <type_traits>
+
+#include "chunk_narrow.cuh"
+#include "tensor_map.h"
+
+namespace pa {
+
+namespace {
+
+using namespace chunk;
+
+struct Q8Params : ChunkParams {
+    const void *q;
+    const float *k_scale, *v_scale;  // [num_blocks, Hkv, block_size]
+};
+
+// NT columns a stream. kCols: the streams halve the query rows (2 NT of them) and both take every key tile, from
+// rings that they share; else they halve the key tiles, each with rings of its own. QP: pieces of a query.
+template <int HD, int NT, int QP, bool kCols>
+struct LayQ8 {
+    static constexpr int kNC = kCols ? 2 * NT : NT;         // query rows
+    static constexpr int PP = 2;                            // pieces of a weight
+    static constexpr int kKV = BN * HD;                     // bytes of a tile
+    static constexpr int kAtom = 8 * HD;                    // eight rows: the swizzle's period
+    static constexpr int kQ = kNC * QP * HD;
+    static constexpr int kP = BN * 128;                     // W^T: a 128-byte row a key, PP * NT of it used
+    static constexpr int kSlots = HD == 128 ? 4 : 8;        // K tiles held, and V tiles
+    static constexpr int kD = kCols ? kSlots : kSlots / 2;  // of a ring
+    static constexpr int kQf = 4;                           // segments whose queries' scales are held
+    // barriers; rings, S, F, P, O, WG: + stream
+    static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = B_KFULL + kSlots,
+                         B_VFULL = B_KEMPTY + kSlots, B_VEMPTY = B_VFULL + kSlots, B_S = B_VEMPTY + kSlots, B_F = B_S + 2,
+                         B_P = B_F + 2, B_WG = B_P + 2, B_O = B_WG + 2, B_OFREE = B_O + 2, B_BOTH = B_OFREE + 2,
+                         B_END = B_BOTH + 1, B_QS = B_END + 2, B_IFULL = B_QS + kQf, B_IEMPTY = B_IFULL + 4, NBAR = B_IEMPTY + 4;
+    // shared memory: V's rings before K's (at head dim 64 the V operand's unused upper half of rows reads
+    // one tile further)
+    static constexpr int OFF_V = 0, OFF_K = kSlots * kKV, OFF_Q = OFF_K + kSlots * kKV, OFF_P = OFF_Q + 2 * kQ,
+                         OFF_SCALE = OFF_P + 2 * kP;        // per K slot: the tile's scales of K, then of V
+    static constexpr int OFF_F = OFF_SCALE + kSlots * 2 * BN * 4;  // floats below
+    // per segment parity and stream: references [NT], sums by warp [4][NT], weights [NT]; scratch; the queries' scales
+    static constexpr int kMax = 0, kSum = 2 * 2 * NT, kWgt = kSum + 2 * 2 * 4 * NT, kRed = kWgt + 2 * 2 * NT,
+                         kFac = kRed + 2 * 4 * NT, kQs = kFac + 2 * NT, kFloats = kQs + kQf * kNC;
+    static constexpr int OFF_BAR = OFF_F + kFloats * 4 + 16;  // after the votes
+    static constexpr int OFF_ITEMS = OFF_BAR + NBAR * 8;
+    static constexpr int OFF_BAD = OFF_ITEMS + 4 * static_cast<int>(sizeof(SegInfo));
+    static constexpr int OFF_PLAN = (OFF_BAD + kBadRing * 4 + 15) / 16 * 16;
+    static constexpr int OFF_MISC = OFF_PLAN + 12 * 8 + static_cast<int>(sizeof(Share));
+    static constexpr int kSmem = OFF_MISC + 16 + 1024;
+    static_assert(kSmem <= 232448, "shared memory per CTA");
+    static_assert(kQ % 1024 == 0 && kKV % 1024 == 0 && OFF_BAR % 8 == 0);
+    static constexpr int kS = QP * NT, kO = PP * NT;        // columns of a stream's S and O
+    static constexpr int kNeed = 2 * (kS + kO);
+    static constexpr int kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+    static constexpr size_t kPieceFloats = piece_floats(kNC, HD);
+};
+
+// Shared-memory matrix descriptor of rows of HD bytes in groups of eight (128-byte swizzle at HD = 128, 64-byte at 64); lbo:
+// from one HD-element column block of an MN-major operand to the next.
+template <int HD>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = smem_desc_sw128(saddr, lbo, 8 * HD);
+    if constexpr (HD == 64) d = (d & ~(7ull << 61)) | 4ull << 61;
+    return d;
+}
+// where the swizzle puts 16-byte chunk c of row r of a tile with rows of HD bytes
+template <int HD>
+__device__ __forceinline__ int swizzled(int r, int c) {
+    return r * HD + ((HD == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+// D (+)= A B of e4m3 operands with fp32 accumulation
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// the types e4m3 x e4m3 -> fp32 of kind::f8f6f4 are those of fp16 x fp16 -> fp32 of kind::f16 in number: 0, 0 and 1
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool b_mn_major) { return idesc_f16(M, N, false, b_mn_major); }
+
+// two fp16 numbers -> two e4m3 (nearest even; beyond 448: 448), and back
+__device__ __forceinline__ uint32_t to_e4m3x2(__half2 v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t *>(&v)));
+    return r;
+}
+__device__ __forceinline__ __half2 from_e4m3x2(uint32_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+    return *reinterpret_cast<__half2 *>(&r);
+}
+// what a piece leaves of v, times 32 (exact: v has 11 bits)
+__device__ __forceinline__ __half2 left_of(__half2 v, uint32_t piece) {
+    const __half2 k = __float2half2_rn(32.f);
+    return __hfma2(from_e4m3x2(piece), __hneg2(k), __hmul2(v, k));
+}
+
+template <class E, int HD, int NT, bool kCols, bool kGather>
+__global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_constant__ Q8Params p) {
+    using T = typename E::T;
+    constexpr int QP = E::kIsBf16 ? 2 : 3;
+    using Lay = LayQ8<HD, NT, QP, kCols>;
+    constexpr int kStep = kCols ? 1 : 2;  // key tiles from one to the next of a stream
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_addr(smem);
+    SegInfo *items = reinterpret_cast<SegInfo *>(smem + Lay::OFF_ITEMS);
+    volatile int *bad_seg = reinterpret_cast<volatile int *>(smem + Lay::OFF_BAD);
+    long long *plan = reinterpret_cast<long long *>(smem + Lay::OFF_PLAN);
+    Share *share = reinterpret_cast<Share *>(plan + 12);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::OFF_MISC + 4);
+    float *fl = reinterpret_cast<float *>(smem + Lay::OFF_F);
+    auto bar = [&](int i) { return sbase + Lay::OFF_BAR + 8u * i; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    static_assert(Lay::NBAR <= kThreads);
+    if (tid < Lay::NBAR) {
+        uint32_t count = 1;
+        if (tid >= Lay::B_QEMPTY && tid < Lay::B_KFULL) count = 2;                    // both issuers
+        if (tid >= Lay::B_KEMPTY && tid < Lay::B_VFULL) count = kCols ? 2 + 8 : 1 + 4;  // issuers and softmax warps
+        if (kCols && tid >= Lay::B_VEMPTY && tid < Lay::B_S) count = 2;
+        if (tid >= Lay::B_F && tid < Lay::B_O) count = 4;                // F, P, WG: four warps
+        if (tid >= Lay::B_OFREE && tid < Lay::B_END) count = 8;
+        if (kCols && tid >= Lay::B_OFREE && tid < Lay::B_BOTH) count = 4;
+        if (tid >= Lay::B_IEMPTY) count = kItemReaders;
+        mbar_init(bar(tid), count);
+        fence_mbar_init();
+    }
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < kBadRing; ++i) bad_seg[i] = 0;
+        for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(fl + Lay::kFloats)[i] = 0;  // votes
+    }
+    // Launched beside what precedes it in the stream: nothing that it wrote is read, and nothing that it reads is
+    // written, before it has finished (the set-up above takes place meanwhile).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Tensor memory is taken only now, and the joining kernel (and with it what follows) let in only when it is
+    // there: no block holds tensor memory while it waits for another grid, whose blocks on this SM may want some.
+    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), Lay::kTmem);
+    if (tid == 0) p.recs[blockIdx.x].valid = 0;
+    plan_share(p, plan, share);
+    zero_bad_sequences<T, HD>(p);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for this grid itself
+    const uint32_t tmem = *tmem_slot;
+
+    // every role reads the segments in the same order: segment n sits in queue entry n % 4
+    auto read_seg = [&](int n, SegInfo &it) -> bool {
+        if (!warp_wait(bar(Lay::B_IFULL + (n & 3)), (n >> 2) & 1, abort_flag)) return false;
+        it = items[n & 3];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Lay::B_IEMPTY + (n & 3)));
+        return true;
+    };
+
+    if (warp == 3) {
+        // ================================== scheduler ==================================
+        int published = 0;
+        // The rows of segment n's queries as pieces: row r, times the power of two that brings its largest magnitude into
+        // [128, 256). The factor that takes scores back, with the softmax's scale, goes to the segment's entry of four:
+        // the softmax of segment n - 4 is over when the issuers have let go of segment n - 2's queries.
+        auto split_q = [&](const SegInfo &it, int n) -> bool {
+            if (!warp_wait(bar(Lay::B_QEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag)) return false;
+            constexpr int kEach = HD / 32;  // elements of a lane: 4 or 2
+            constexpr int kAhead = 4;       // rows in flight
+            const int rows = it.tok * p.G;
+            unsigned char *dst = smem + Lay::OFF_Q + (n & 1) * Lay::kQ;
+            float *qs = fl + Lay::kQs + (n & 3) * Lay::kNC;
+            const T *q = static_cast<const T *>(p.q);
+            for (int r0 = 0; r0 < rows; r0 += kAhead) {
+                uint32_t w[kAhead][kEach / 2];
+                uint32_t most[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int r = min(r0 + k, rows - 1), tok = p.div_g(r);
+                    const T *src = q + (static_cast<size_t>(it.tok0 + tok) * p.Hq + it.g * p.G + (r - tok * p.G)) * HD + lane * kEach;
+                    if constexpr (kEach == 4) {
+                        const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(src));
+                        w[k][0] = v.x, w[k][1] = v.y;
+                    } else {
+                        w[k][0] = __ldcg(reinterpret_cast<const uint32_t *>(src));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    most[k] = 0;
+#pragma unroll
+                    for (int e = 0; e < kEach / 2; ++e) {
+                        const float2 f = E::unpack2(w[k][e]);
+                        most[k] = max(most[k], max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+                    }
+                    most[k] = __reduce_max_sync(kFull, most[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int r = r0 + k;
+                    if (r >= rows) break;
+                    const uint32_t e8 = max(most[k] >> 23, 8u);  // exponent, kept where both factors are normal
+                    const float up = __uint_as_float((261u - e8) << 23);
+                    // a row that is not finite gives scores that are not
+                    const float down = e8 == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e8 - 7u) << 23) * p.scale_log2;
+                    __half2 v[kEach / 2];
+#pragma unroll
+                    for (int e = 0; e < kEach / 2; ++e) {
+                        const float2 f = E::unpack2(w[k][e]);
+                        v[e] = __floats2half2_rn(f.x * up, f.y * up);  // exact down to 2^-17 of the largest
+                    }
+                    const int stream = r / NT, row0 = stream * QP * NT + r % NT;
+#pragma unroll
+                    for (int i = 0; i < QP; ++i) {
+                        uint32_t piece[kEach / 2];
+#pragma unroll
+                        for (int e = 0; e < kEach / 2; ++e) {
+                            piece[e] = to_e4m3x2(v[e]);
+                            v[e] = left_of(v[e], piece[e]);
+                        }
+                        unsigned char *at = dst + swizzled<HD>(row0 + i * NT, lane * kEach >> 4) + (lane * kEach & 15);
+                        if constexpr (kEach == 4)
+                            *reinterpret_cast<uint32_t *>(at) = piece[0] | piece[1] << 16;
+                        else
+                            *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(piece[0]);
+                    }
+                    if (lane == 0) qs[r] = down;
+                }
+            }
+            // columns without a query row: their scores count for nothing, whatever the pieces there hold
+            for (int r = rows + lane; r < Lay::kNC; r += 32) qs[r] = 0.f;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(Lay::B_QFULL + (n & 1)));
+                mbar_arrive(bar(Lay::B_QS + (n & 3)));
+            }
+            return true;
+        };
+        const bool ok = walk_share(p, *share, [&](const SegInfo &it) {
+            if (!warp_wait(bar(Lay::B_IEMPTY + (published & 3)), ((published >> 2) & 1) ^ 1, abort_flag)) return false;
+            if (lane == 0) {
+                items[published & 3] = it;
+                mbar_arrive(bar(Lay::B_IFULL + (published & 3)));
+            }
+            __syncwarp();
+            const bool r = it.j0 == it.j1 || split_q(it, published);
+            ++published;
+            return r;
+        });
+        if (!ok && lane == 0) give_up(p.err, abort_flag);
+    } else if (warp == 0) {
+        // =================================== producer ===================================
+        if constexpr (!kGather) {
+            prefetch_tmap(&p.tm_k);
+            prefetch_tmap(&p.tm_v);
+        }
+        const int R = p.box_rows, nbox = BN / R;
+        constexpr int kRowsLane = kGather ? BN / 32 : 1;
+        struct Rows {
+            long long r[kRowsLane];
+            int g;
+        };
+        auto rows_of = [&](const SegInfo &it, int j, int seg_no) {
+            Rows w;
+            w.g = it.g;
+#pragma unroll
+            for (int i = 0; i < kRowsLane; ++i) {
+                const int pos = j * BN + (kGather ? lane + 32 * i : lane * R);
+                w.r[i] = kGather || lane < nbox ? pool_row(p, it, pos, kGather ? pos : pos + R - 1, bad_seg, seg_no) : -1;
+            }
+            return w;
+        };
+        // where pool row r's scale lies
+        auto scale_at = [&](long long r, int g) {
+            const int row = static_cast<int>(r), block = p.geom.block_of(row);
+            return (static_cast<size_t>(block) * p.Hkv + g) * p.geom.block_size + p.geom.offset_of(row);
+        };
+        uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};  // tiles loaded, by stream
+        // gathered tiles are announced one load late, when their copies have landed
+        uint32_t owed = 0;  // the barrier of the tile whose copies are in flight
+        auto announce = [&](uint32_t b) {
+            if constexpr (kGather) {
+                if (owed) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(owed);
+                }
+                owed = b;
+            }
+        };
+        auto flush = [&]() {
+            if constexpr (kGather) {
+                cp_async_wait<0>();
+                announce(0);
+            }
+        };
+        auto load = [&](const Rows &w, bool is_v, auto stream) -> bool {
+            constexpr int h = decltype(stream)::value;
+            const uint32_t i = is_v ? nv[h]++ : nk[h]++;
+            const int slot = h * Lay::kD + static_cast<int>(i % Lay::kD);
+            const uint32_t full = bar((is_v ? Lay::B_VFULL : Lay::B_KFULL) + slot);
+            const uint32_t dst = sbase + (is_v ? Lay::OFF_V : Lay::OFF_K) + slot * Lay::kKV;
+            const uint32_t sc = sbase + Lay::OFF_SCALE + slot * 2 * BN * 4;
+            const uint32_t empty = bar((is_v ? Lay::B_VEMPTY : Lay::B_KEMPTY) + slot), par = ((i / Lay::kD) & 1) ^ 1;
+            // a gathered tile is not held back while this one waits for its slot
+            if (kGather && !__all_sync(kFull, mbar_try_wait(empty, par))) flush();
+            if (!warp_wait(empty, par, abort_flag)) return false;
+            if constexpr (kGather) {
+                const unsigned char *pool = static_cast<const unsigned char *>(is_v ? p.v_cache : p.k_cache);
+#pragma unroll
+                for (int e = 0; e < kRowsLane; ++e) {
+                    const int k = lane + 32 * e;
+                    const bool there = w.r[e] >= 0;
+                    const unsigned char *src = pool + (static_cast<size_t>(there ? w.r[e] : 0) * p.Hkv + w.g) * HD;
+#pragma unroll
+                    for (int c = 0; c < HD / 16; ++c) cp_async16(dst + swizzled<HD>(k, c), src + c * 16, there ? 16 : 0);
+                    if (!is_v && there) {
+                        const size_t at = scale_at(w.r[e], w.g);
+                        cp_async4(sc + k * 4, p.k_scale + at);
+                        cp_async4(sc + (BN + k) * 4, p.v_scale + at);
+                    }
+                }
+                cp_async_commit();
+                cp_async_wait<1>();
+                announce(full);
+            } else {
+                const uint32_t bytes = static_cast<uint32_t>(R) * (is_v ? HD : HD + 8);
+                const uint32_t boxes = __popc(__ballot_sync(kFull, w.r[0] >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(full, boxes * bytes);
+                __syncwarp();
+                if (w.r[0] >= 0) {
+                    tma_load_3d(dst + lane * R * HD, is_v ? &p.tm_v : &p.tm_k, 0, w.g, static_cast<int>(w.r[0]), full);
+                    if (!is_v) {
+                        const size_t at = scale_at(w.r[0], w.g);
+                        bulk_load(sc + lane * R * 4, p.k_scale + at, R * 4, full);
+                        bulk_load(sc + (BN + lane * R) * 4, p.v_scale + at, R * 4, full);
+                    }
+                }
+            }
+            return true;
+        };
+        int n = 0;  // segments taken
+        bool ok = true;
+        SegInfo cur{};
+        Rows pend[2]{}, next{};
+        bool has[2] = {false, false};
+        // The last tile of each stream whose V is still to come: loaded after the stream's next K, and
+        // those of the segment before as soon as a segment's first K is under way. An issuer takes the first
+        // K of a segment only when the V of the segment before has been used, and a K slot is free when the softmax has read
+        // the scales in it, at the start of the tile: no load waits for a tile whose predecessors' Vs are outstanding.
+        using A = std::integral_constant<int, 0>;
+        using B = std::integral_constant<int, 1>;
+        auto pending = [&](auto stream) -> bool {
+            constexpr int h = decltype(stream)::value;
+            const bool r = !has[h] || load(pend[h], true, stream);
+            has[h] = false;
+            return r;
+        };
+        while (ok) {
+            if (!(ok = read_seg(n, cur)) || cur.j0 == cur.j1) break;
+            flush();
+            next = rows_of(cur, cur.j0, n);
+            auto tile = [&](int j, auto stream) -> bool {
+                constexpr int h = decltype(stream)::value;
+                const Rows w = next;
+                if (j + 1 < cur.j1) next = rows_of(cur, j + 1, n);  // in flight while this tile is loaded
+                if (!load(w, false, stream) || !pending(stream) || (j == cur.j0 && !pending(B{}))) return false;
+                pend[h] = w;
+                has[h] = true;
+                return true;
+            };
+            for (int j = cur.j0; ok && j < cur.j1; j += kStep)
+                ok = tile(j, A{}) && (kCols || j + 1 == cur.j1 || tile(j + 1, B{}));
+            ++n;
+        }
+        ok = ok && pending(A{}) && pending(B{});
+        flush();
+        if (!ok && lane == 0) give_up(p.err, abort_flag);
+        // no copy may still be in flight at exit: the last load of every slot
+        if (lane == 0 && !kGather) {
+#pragma unroll
+            for (int h = 0; h < (kCols ? 1 : 2); ++h)
+#pragma unroll
+                for (uint32_t back = 1; back <= Lay::kD; ++back) {
+                    if (nk[h] >= back) {
+                        const uint32_t i = nk[h] - back;
+                        if (!mbar_wait(bar(Lay::B_KFULL + h * Lay::kD + i % Lay::kD), (i / Lay::kD) & 1)) give_up(p.err, abort_flag);
+                    }
+                    if (nv[h] >= back) {
+                        const uint32_t i = nv[h] - back;
+                        if (!mbar_wait(bar(Lay::B_VFULL + h * Lay::kD + i % Lay::kD), (i / Lay::kD) & 1)) give_up(p.err, abort_flag);
+                    }
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+        // ============================ MMA issuer of one stream =============================
+        const int h = warp - 1;
+        constexpr uint32_t IQK = idesc_e4m3(BM, Lay::kS, false);             // A = K rows, B = Q pieces, both K-major
+        constexpr uint32_t IPV = idesc_a_mn(idesc_e4m3(BM, Lay::kO, true));  // A = V^T, B = W^T pieces, both MN-major
+        const int ring = kCols ? 0 : h * Lay::kD, first = kCols ? 0 : h;     // the stream's first slot, and key tile
+        const uint64_t dq0 = desc_rows<HD>(sbase + Lay::OFF_Q + (kCols ? h * Lay::kS * HD : 0), 16);
+        const uint64_t dk0 = desc_rows<HD>(sbase + Lay::OFF_K + ring * Lay::kKV, 16);
+        const uint64_t dv0 = desc_rows<HD>(sbase + Lay::OFF_V + ring * Lay::kKV, Lay::kKV);
+        const uint64_t dp = smem_desc_sw128(sbase + Lay::OFF_P + h * Lay::kP, 16, 1024);
+        const uint32_t s_tm = tmem + h * Lay::kS, o_tm = tmem + 2 * Lay::kS + h * Lay::kO;
+        auto qk = [&](int slot, int q) {  // S^T = K Q^T, 32 elements an instruction
+            const uint64_t a = dk0 + slot * (Lay::kKV >> 4), b = dq0 + q * (Lay::kQ >> 4);
+#pragma unroll
+            for (int kk = 0; kk < HD / 32; ++kk) tc_mma_e4m3(s_tm, a + kk * 2, b + kk * 2, IQK, kk > 0);
+        };
+        auto pv = [&](int slot, bool acc) {  // O^T += V^T W^T, 32 keys an instruction
+            const uint64_t a = dv0 + slot * (Lay::kKV >> 4);
+#pragma unroll
+            for (int kk = 0; kk < BN / 32; ++kk)
+                tc_mma_e4m3(o_tm, a + ((kk * 32 * HD) >> 4), dp + ((kk * 32 * 128) >> 4), IPV, (acc || kk > 0));
+        };
+        uint32_t t = 0;  // key tiles of this stream: QKs issued
+        bool ok = true;
+        SegInfo it{};
+        // QK of the stream's next tile once S has been read; `last`: of the segment
+        auto issue_qk = [&](int n, bool last) -> bool {
+            const int slot = static_cast<int>(t % Lay::kD);
+            if (t > 0 && !warp_wait(bar(Lay::B_F + h), (t - 1) & 1, abort_flag)) return false;
+            if (!warp_wait(bar(Lay::B_KFULL + ring + slot), (t / Lay::kD) & 1, abort_flag)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                qk(slot, n & 1);
+                tc_commit(bar(Lay::B_S + h));
+                tc_commit(bar(Lay::B_KEMPTY + ring + slot));
+                if (last) tc_commit(bar(Lay::B_QEMPTY + (n & 1)));
+            }
+            __syncwarp();
+            ++t;
+            return true;
+        };
+        uint32_t done = 0;  // PVs issued
+        for (int n = 0; ok; ++n) {
+            if (!(ok = read_seg(n, it)) || it.j0 == it.j1) break;
+            const int cnt = it.j1 - it.j0;
+            if (!(ok = warp_wait(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, abort_flag))) break;
+            if (first >= cnt) {  // a segment of one tile has none for stream B
+                if (lane == 0) mbar_arrive(bar(Lay::B_QEMPTY + (n & 1)));
+                __syncwarp();
+                continue;
+            }
+            if (!(ok = issue_qk(n, first + kStep >= cnt))) break;
+            for (int i = first; i < cnt; i += kStep, ++done) {
+                if (i + kStep < cnt && !(ok = issue_qk(n, i + 2 * kStep >= cnt))) break;
+                const int slot = static_cast<int>(done % Lay::kD);
+                if (!(ok = warp_wait(bar(Lay::B_VFULL + ring + slot), (done / Lay::kD) & 1, abort_flag))) break;
+                const int n0 = (it.j0 + i) * BN, z0 = max(it.n_lo - n0, 0), z1 = min(it.n_end - n0, BN);
+                // rows outside [z0, z1) are zeroed: their weights are zero, but 0 * NaN is not
+                // (streams that share the tile both write the zeros)
+                if (z0 > 0 || z1 < BN) {
+                    uint4 *tile = reinterpret_cast<uint4 *>(smem + Lay::OFF_V + (ring + slot) * Lay::kKV);
+                    for (int x = lane; x < z0 * (HD / 16); x += 32) tile[x] = make_uint4(0, 0, 0, 0);
+                    for (int x = z1 * (HD / 16) + lane; x < BN * (HD / 16); x += 32) tile[x] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (!(ok = warp_wait(bar(Lay::B_P + h), done & 1, abort_flag))) break;
+                // the previous segment's output must be out of TMEM before its O is overwritten. (B may have
+                // had no tile in it; its softmax warps have then passed the end of that segment with A's.)
+                if (i == first && n > 0 && !(ok = warp_wait(bar(Lay::B_OFREE + (kCols ? h : 0)), (n - 1) & 1, abort_flag)))
+                    break;
+                tc_fence_after();
+                if (lane == 0) {
+                    pv(slot, i > first);
+                    tc_commit(bar(Lay::B_O + h));
+                    tc_commit(bar(Lay::B_VEMPTY + ring + slot));
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) give_up(p.err, abort_flag);
+        if (lane == 0) {  // every MMA this thread issued has finished before the TMEM is freed
+            tc_commit(bar(Lay::B_END + h));
+            if (!mbar_wait(bar(Lay::B_END + h), 0)) give_up(p.err, abort_flag);
+        }
+        __syncwarp();
+    } else {
+        // =================================== softmax ===================================
+        const int h = warp >= 8 ? 1 : 0;
+        const int quarter = warp & 3, wt = tid & 127;  // thread of the stream = key of the tile
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t s_row = tmem + lane_off + h * Lay::kS, o_row = tmem + lane_off + 2 * Lay::kS + h * Lay::kO;
+        unsigned char *prow = smem + Lay::OFF_P + h * Lay::kP + wt * 128;
+        const int ring = kCols ? 0 : h * Lay::kD;
+        const int first = kCols ? 0 : h;         // the stream's first key tile of a segment
+        const int col0 = kCols ? h * NT : 0;     // the query row of its first column
+        float *red = fl + Lay::kRed + h * 4 * NT, *fac = fl + Lay::kFac + h * NT;
+        volatile uint32_t *votes = reinterpret_cast<volatile uint32_t *>(fl + Lay::kFloats) + h * 2;
+        uint32_t t = 0;                  // key tiles of this stream before this one
+        uint32_t syncs = 0;              // of the stream's warps so far
+        bool ok = true;
+        SegInfo it{};
+        // All warps of the stream meet (shared memory written before is visible after); true in `any` if one
+        // of them voted. A bounded wait like every other: false ends the role. A warp can be one meeting
+        // ahead of another at most, so the votes of two suffice.
+        auto meet = [&](bool vote, bool &any) -> bool {
+            if (__any_sync(kFull, vote) && lane == 0) votes[syncs & 1] = syncs + 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Lay::B_WG + h));
+            const bool r = warp_wait(bar(Lay::B_WG + h), syncs & 1, abort_flag);
+            any = votes[syncs & 1] == syncs + 1;
+            ++syncs;
+            return r;
+        };
+        bool any = false;
+        for (int n = 0; ok; ++n) {
+            if (!(ok = read_seg(n, it)) || it.j0 == it.j1) break;
+            const int cnt = it.j1 - it.j0, rows = it.tok * p.G, par = n & 1;
+            float *mx = fl + Lay::kMax + (par * 2 + h) * NT;
+            const float *qs = fl + Lay::kQs + (n & 3) * Lay::kNC + col0;
+            // columns without a query row have a reference that leaves them no weight
+            if (wt < NT) mx[wt] = col0 + wt < rows ? kUnset : INFINITY;
+            if (!(ok = meet(false, any))) break;
+            if (!(ok = warp_wait(bar(Lay::B_QS + (n & 3)), (n >> 2) & 1, abort_flag))) break;  // the queries' scales
+            float l[NT];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) l[c] = 0.f;
+            const int last_pos = it.p0 + it.tok - 1;
+            for (int i = first; i < cnt; i += kStep, ++t) {
+                const int key = (it.j0 + i) * BN + wt, n0 = (it.j0 + i) * BN;
+                const int slot = ring + static_cast<int>(t % Lay::kD);
+                if (!(ok = warp_wait(bar(Lay::B_KFULL + slot), (t / Lay::kD) & 1, abort_flag))) break;
+                const float *sc = reinterpret_cast<const float *>(smem + Lay::OFF_SCALE + slot * 2 * BN * 4);
+                float ks = sc[wt], vs = sc[BN + wt];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Lay::B_KEMPTY + slot));  // the scales have been read
+                if (key < it.n_lo || key >= it.n_end) ks = vs = 1.f;    // no row sees it: whatever lies there
+                const float lv = __log2f(vs), inv_vs = __frcp_rn(vs);
+                if (!(ok = warp_wait(bar(Lay::B_S + h), t & 1, abort_flag))) break;
+                tc_fence_after();
+                // every row sees every key of the tile?
+                const bool masked = n0 + BN > it.p0 + 1 || (p.window > 0 && n0 < last_pos - p.window + 1);
+                float x[NT];
+                auto read_s = [&]() {  // x = log2 of the weight before the reference
+#pragma unroll
+                    for (int c = 0; c < NT; c += 16) {
+                        uint32_t s0[16], s1[16];
+                        tmem_ld<16>(s_row + c, s0);
+                        tmem_ld<16>(s_row + NT + c, s1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[c + e] = fmaf(__uint_as_float(s1[e]), 0x1p-5f, __uint_as_float(s0[e]));
+                        if constexpr (QP == 3) {
+                            tmem_ld<16>(s_row + 2 * NT + c, s0);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) x[c + e] = fmaf(__uint_as_float(s0[e]), 0x1p-10f, x[c + e]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 f4 = *reinterpret_cast<const float4 *>(qs + c + e);
+                            x[c + e] = fmaf(x[c + e] * f4.x, ks, lv), x[c + e + 1] = fmaf(x[c + e + 1] * f4.y, ks, lv);
+                            x[c + e + 2] = fmaf(x[c + e + 2] * f4.z, ks, lv), x[c + e + 3] = fmaf(x[c + e + 3] * f4.w, ks, lv);
+                        }
+                    }
+                    if (masked) {
+                        const int tok_c = p.div_g(col0);
+                        int pos = it.p0 + tok_c, in_tok = col0 - tok_c * p.G;
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) {
+                            if (key > pos || (p.window > 0 && key <= pos - p.window)) x[c] = -INFINITY;
+                            if (++in_tok == p.G) in_tok = 0, ++pos;
+                        }
+                    }
+                };
+                auto shift = [&]() {  // less the reference; the largest
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < NT; c += 4) {
+                        const float4 m4 = *reinterpret_cast<const float4 *>(mx + c);
+                        x[c] -= m4.x, x[c + 1] -= m4.y, x[c + 2] -= m4.z, x[c + 3] -= m4.w;
+                        most = fmaxf(most, fmaxf(fmaxf(x[c], x[c + 1]), fmaxf(x[c + 2], x[c + 3])));
+                    }
+                    return most;
+                };
+                read_s();
+                any = true;  // the segment's first tile sets the references
+                if (i > first) {
+                    // A reference moves when some x exceeds it by more than 8: the sum uses the same
+                    // reference, so the result is exact, and the weights stay at most 2^8.
+                    if (!(ok = meet(shift() > 8.f, any))) break;
+                }
+                if (any) {
+                    if (i > first) read_s();
+                    float v[NT];
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) v[c] = x[c];
+                    const float top = fold(v, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < NT) red[quarter * NT + lane] = top;
+                    if (!(ok = meet(false, any))) break;
+                    if (wt < NT) {
+                        const float most = fmaxf(fmaxf(red[wt], red[NT + wt]), fmaxf(red[2 * NT + wt], red[3 * NT + wt]));
+                        const float old = mx[wt];
+                        const bool move = most > old + 8.f;  // never where old is +inf, or the largest -inf
+                        fac[wt] = move ? fast_exp2(old - (most - 4.f)) : 1.f;
+                        if (move) mx[wt] = most - 4.f;
+                    }
+                    if (!(ok = meet(false, any))) break;
+#pragma unroll
+                    for (int c = 0; c < NT; c += 4) {
+                        const float4 f4 = *reinterpret_cast<const float4 *>(fac + c);
+                        l[c] *= f4.x, l[c + 1] *= f4.y, l[c + 2] *= f4.z, l[c + 3] *= f4.w;
+                    }
+                    if (i > first) {
+                        if (!(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < Lay::kO; c += 16) {
+                            uint32_t ov[16];
+                            tmem_ld<16>(o_row + c, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * fac[c % NT + e]);
+                            tmem_st16(o_row + c, ov);
+                        }
+                        tmem_wait_st();
+                    }
+                    shift();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Lay::B_F + h));  // S has been read
+                // the stream's previous PV has read W
+                if (t > 0 && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+#pragma unroll
+                for (int q = 0; q < NT / 16; ++q) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int c = q * 16 + e * 2;
+                        const float w0 = fast_exp2(x[c]), w1 = fast_exp2(x[c + 1]);
+                        l[c] = fmaf(w0, inv_vs, l[c]);
+                        l[c + 1] = fmaf(w1, inv_vs, l[c + 1]);
+                        // the weights as the tensor cores take them, two e4m3 numbers each; the sum is of the weights themselves
+                        const __half2 w = __floats2half2_rn(w0, w1);
+                        const uint32_t a = to_e4m3x2(w), b = to_e4m3x2(left_of(w, a));
+                        hi[e >> 1] = e & 1 ? hi[e >> 1] | a << 16 : a;
+                        lo[e >> 1] = e & 1 ? lo[e >> 1] | b << 16 : b;
+                    }
+                    // 16-byte chunk c of a key's row sits at c ^ (key % 8)
+                    *reinterpret_cast<uint4 *>(prow + ((q ^ (wt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(prow + (((NT / 16 + q) ^ (wt & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Lay::B_P + h));
+            }
+            if (!ok) break;
+            // ---- the segment's end: sums over the warp's keys
+            float *sums = fl + Lay::kSum + ((par * 2 + h) * 4 + quarter) * NT;
+            const float sum_c = fold(l, [](float a, float b) { return a + b; });
+            if (lane < NT) sums[lane] = sum_c;
+            const int cnt_b = kCols ? 0 : cnt / 2;  // tiles of the other stream's accumulator to be joined with A's
+            // this stream's products are complete; then, where the streams halve the keys, both streams', with
+            // their references and sums
+            if (cnt > first && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+            if constexpr (kCols) {
+                if (!(ok = meet(false, any))) break;
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(Lay::B_BOTH));
+                if (!(ok = warp_wait(bar(Lay::B_BOTH), n & 1, abort_flag))) break;
+            }
+            tc_fence_after();
+            // this stream writes the query rows [c_lo, c_lo + kMine): its own, or half of the streams' common ones
+            constexpr int kMine = kCols ? NT : NT / 2;
+            const int c_lo = h * kMine, acc = kCols ? h : 0;  // the stream whose state counts as A's
+            const bool bad = bad_seg[n & (kBadRing - 1)] == n + 1;  // a table entry of the segment was bad
+            float *piece = it.part < 0 ? nullptr
+                                       : p.pieces + (static_cast<size_t>(blockIdx.x) * 2 + it.part) * Lay::kPieceFloats;
+            float *wa = fl + Lay::kWgt + par * 2 * NT, *wb = wa + NT;
+            if (wt < kMine) {
+                const int c = c_lo + wt, ca = c - (kCols ? col0 : 0);  // its column in the stream
+                const float *sa = fl + Lay::kSum + (par * 2 + acc) * 4 * NT + ca, *sb = fl + Lay::kSum + (par * 2 + 1) * 4 * NT + ca;
+                const float ma = fl[Lay::kMax + (par * 2 + acc) * NT + ca], mb = cnt_b > 0 ? fl[Lay::kMax + (par * 2 + 1) * NT + ca] : kUnset;
+                const float la = (sa[0] + sa[NT]) + (sa[2 * NT] + sa[3 * NT]);
+                const float lb = cnt_b > 0 ? (sb[0] + sb[NT]) + (sb[2 * NT] + sb[3 * NT]) : 0.f;
+                const float m = fmaxf(ma, mb), fa = fast_exp2(ma - m), fb = cnt_b > 0 ? fast_exp2(mb - m) : 0.f;
+                const float sum = fa * la + fb * lb;
+                float scale = 1.f;  // a piece: O unnormalised, with its reference and sum (sum -1: bad)
+                if (!piece) scale = sum > 0.f ? 1.f / sum : sum == sum ? 0.f : sum;
+                wa[c] = fa * scale;
+                if (!kCols) wb[c] = fb * scale;
+                if (piece) {
+                    piece[c] = m;
+                    piece[Lay::kNC + c] = bad ? -1.f : sum;
+                }
+            }
+            if (!(ok = meet(false, any))) break;
+            const uint32_t oa = tmem + lane_off + 2 * Lay::kS + acc * Lay::kO - (kCols ? col0 : 0), ob = oa + Lay::kO;  // at column c: + c
+            const int d = wt;  // element of the head
+            T *out = static_cast<T *>(p.out);
+            constexpr int W = 8;
+#pragma unroll 1
+            for (int c0 = c_lo; c0 < c_lo + kMine && c0 < rows; c0 += W) {
+                uint32_t a[W], a1[W], b[W], b1[W];
+                tmem_ld<W>(oa + c0, a);
+                tmem_ld<W>(oa + NT + c0, a1);
+                if (cnt_b > 0) {
+                    tmem_ld<W>(ob + c0, b);
+                    tmem_ld<W>(ob + NT + c0, b1);
+                }
+                tmem_wait_ld();
+                float o[W];
+#pragma unroll
+                for (int e = 0; e < W; ++e) o[e] = fmaf(__uint_as_float(a1[e]), 0x1p-5f, __uint_as_float(a[e])) * wa[c0 + e];
+                if (cnt_b > 0)
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        o[e] = fmaf(fmaf(__uint_as_float(b1[e]), 0x1p-5f, __uint_as_float(b[e])), wb[c0 + e], o[e]);
+                if (d >= HD) continue;
+                if (piece) {
+                    float *pc = piece + 2 * Lay::kNC + c0 * HD + d;  // columns behind the rows: room, never read
+#pragma unroll
+                    for (int e = 0; e < W; ++e) pc[e * HD] = o[e];
+                } else {
+                    const int tk = p.div_g(c0);
+                    int in_tok = c0 - tk * p.G;
+                    T *oc = out + (static_cast<size_t>(it.tok0 + tk) * p.Hq + it.g * p.G + in_tok) * HD + d;
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        if (c0 + e < rows) *oc = T(bad ? 0.f : o[e]);
+                        oc += HD;
+                        if (++in_tok == p.G) in_tok = 0, oc += (p.Hq - p.G) * HD;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Lay::B_OFREE + acc));
+        }
+        if (!ok && lane == 0) give_up(p.err, abort_flag);
+    }
+    // ------------------------------------------------------------------------------------------
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, Lay::kTmem);
+    }
+}
+
+template <class E, int HD, int NT, bool kCols, bool kGather>
+cudaError_t launch_typed(const Q8Params &prm, cudaStream_t stream) {
+    using Lay = LayQ8<HD, NT, E::kIsBf16 ? 2 : 3, kCols>;
+    auto kern = chunk_q8_kernel<E, HD, NT, kCols, kGather>;
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem);
+        if (e != cudaSuccess) return e;
+        configured[dev] = 1;
+    }
+    const unsigned P = device_sm_count();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(P);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay::kSmem;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, prm)) != cudaSuccess) return e;  // as in chunk_attn.cu
+    cfg.dynamicSmemBytes = 0;
+    const int rows = (prm.max_seqlen_q < prm.item_tok ? prm.max_seqlen_q : prm.item_tok) * prm.G;
+    cfg.gridDim = dim3(P, (rows * (HD / 4) + kJoinWork - 1) / kJoinWork);
+    cfg.blockDim = dim3(kJoinWork * kJoinGroups);
+    return cudaLaunchKernelEx(&cfg, chunk_narrow_join_kernel<E, HD, Lay::kNC>, static_cast<const ChunkParams &>(prm));
+}
+
+constexpr int kMostRows = 64;  // query rows of an item
+
+size_t piece_bytes(int D) { return piece_floats(kMostRows, D) * 4; }
+
+}  // namespace
+
+size_t chunk_q8_workspace(int D) {
+    const size_t P = device_sm_count();
+    return P * 2 * piece_bytes(D) + P * sizeof(PieceRec);
+}
+
+cudaError_t launch_chunk_q8(const ChunkQ8Args &x, cudaStream_t stream) {
+    const ChunkArgs &a = x.chunk;
+    Q8Params prm{};
+    int R = 1;  // rows per K/V box: the largest power of two dividing the block size, at most 128
+    while (R < 128 && a.block_size % (2 * R) == 0) R *= 2;
+    const bool gather = R < 8;  // less than a swizzle atom of 8 rows
+    prm.G = a.Hq / a.Hkv;
+    prm.inv_g = (65536 + prm.G - 1) / prm.G;
+    const long long rows = static_cast<long long>(a.max_seqlen_q) * prm.G;
+    // gathered keys are bound by the one warp that copies them, whatever the columns: one form for all
+    const int form = gather || rows > 32 ? 64 : rows > 16 ? 32 : 16;
+    prm.tt = prm.item_tok = form / prm.G;
+    const long long krows = static_cast<long long>(a.num_blocks) * a.block_size;
+    if (!gather && (!encode_rows_e4m3(&prm.tm_k, a.k_cache, a.Hkv, a.D, krows, R) ||
+                    !encode_rows_e4m3(&prm.tm_v, a.v_cache, a.Hkv, a.D, krows, R)))
+        return cudaErrorInvalidValue;
+    prm.cu_q = a.cu_q;
+    prm.ctx = a.ctx;
+    prm.block_tables = a.block_tables;
+    prm.q = a.q;
+    prm.k_cache = a.k_cache;
+    prm.v_cache = a.v_cache;
+    prm.k_scale = x.k_scale;
+    prm.v_scale = x.v_scale;
+    prm.out = a.out;
+    prm.err = a.err;
+    const size_t P = device_sm_count();
+    prm.pieces = static_cast<float *>(a.workspace);
+    prm.recs = reinterpret_cast<PieceRec *>(static_cast<char *>(a.workspace) + P * 2 * piece_bytes(a.D));
+    prm.S = a.S, prm.Hq = a.Hq, prm.Hkv = a.Hkv;
+    prm.max_blocks = a.max_blocks, prm.num_blocks = a.num_blocks;
+    prm.total_q = a.total_q, prm.max_seqlen_q = a.max_seqlen_q, prm.window = a.window;
+    prm.box_rows = gather ? 1 : R;
+    prm.geom.block_size = a.block_size;
+    prm.geom.shift = log2_if_pow2(a.block_size);
+    prm.scale_log2 = a.scale * kLog2e;
+    auto go = [&](auto e, auto hd) {
+        using E = decltype(e);
+        constexpr int HD = decltype(hd)::value;
+        if (gather) return launch_typed<E, HD, 32, true, true>(prm, stream);
+        if (form == 16) return launch_typed<E, HD, 16, false, false>(prm, stream);
+        if (form == 32) return launch_typed<E, HD, 32, false, false>(prm, stream);
+        return launch_typed<E, HD, 32, true, false>(prm, stream);
+    };
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    if (a.dtype == PA_BF16) return a.D == 64 ? go(BF16{}, I64{}) : go(BF16{}, I128{});
+    return a.D == 64 ? go(F16{}, I64{}) : go(F16{}, I128{});
+}
+
+}  // namespace pa

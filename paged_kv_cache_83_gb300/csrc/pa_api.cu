@@ -115,6 +115,33 @@ pa_status check_rope_store(const pa::RopeStoreArgs &a, bool with_norm, bool &emp
     return PA_OK;
 }
 
+// The checks that the calls of chunk attention share. q8: over an 8-bit cache. empty: nothing to do.
+pa_status check_chunk(const pa::ChunkArgs &a, size_t workspace_bytes, bool q8, bool &empty) {
+    if (!dtype_ok(a.dtype)) return PA_ERR_DTYPE;
+    if (a.S < 0 || a.total_q < 0 || a.max_seqlen_q < 0 || a.window < 0 || a.block_size < 1 || a.num_blocks < 0 ||
+        a.max_blocks < 0 || !(a.scale >= FLT_MIN && a.scale <= FLT_MAX / 2))
+        return PA_ERR_SHAPE;
+    const pa_status st = check_heads(a.Hq, a.Hkv, a.D);
+    if (st != PA_OK) return st;
+    if (static_cast<long long>(a.max_blocks) * a.block_size > INT_MAX) return PA_ERR_SHAPE;
+    // positions and tile bounds stay below 2^31 - 256 in 32 bits
+    if (a.S > 65535 || static_cast<long long>(a.num_blocks) * a.block_size > INT_MAX ||
+        static_cast<long long>(a.max_blocks) * a.block_size > INT_MAX - 1024 || a.total_q > INT_MAX - 1024)
+        return PA_ERR_UNSUPPORTED;
+    empty = a.S == 0 || a.max_seqlen_q == 0 || a.total_q == 0;
+    if (empty) return PA_OK;
+    if (a.max_blocks < 1 || a.num_blocks < 1) return PA_ERR_SHAPE;
+    if (!a.out || !a.q || !a.k_cache || !a.v_cache || !a.block_tables || !a.cu_q || !a.ctx) return PA_ERR_NULL;
+    if (!aligned16(a.out) || !aligned16(a.q) || !aligned16(a.k_cache) || !aligned16(a.v_cache)) return PA_ERR_UNSUPPORTED;
+    // out is q itself (an item's queries are read before its rows are written) or lies clear of it
+    const uintptr_t o = reinterpret_cast<uintptr_t>(a.out), x = reinterpret_cast<uintptr_t>(a.q), apart = o < x ? x - o : o - x;
+    if (apart != 0 && apart < static_cast<uint64_t>(a.total_q) * a.Hq * a.D * 2) return PA_ERR_UNSUPPORTED;
+    if (!a.workspace || workspace_bytes < (q8 ? pa::chunk_q8_workspace(a.D) : pa::chunk_attn_workspace(a.D)) ||
+        !aligned16(a.workspace))
+        return PA_ERR_WORKSPACE;
+    return PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -432,49 +459,40 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
                         int block_size, int num_blocks, float scale, pa_dtype dtype,
                         void *workspace, size_t workspace_bytes, int32_t *err,
                         cudaStream_t stream) {
-    if (!dtype_ok(dtype)) return PA_ERR_DTYPE;
-    if (S < 0 || total_q < 0 || max_seqlen_q < 0 || window < 0 || block_size < 1 || num_blocks < 0 ||
-        max_blocks_per_seq < 0 || !(scale >= FLT_MIN && scale <= FLT_MAX / 2))
-        return PA_ERR_SHAPE;
-    const pa_status st = check_heads(Hq, Hkv, D);
-    if (st != PA_OK) return st;
-    if (static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX) return PA_ERR_SHAPE;
-    // positions and tile bounds stay below 2^31 - 256 in 32 bits
-    if (S > 65535 || static_cast<long long>(num_blocks) * block_size > INT_MAX ||
-        static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX - 1024 || total_q > INT_MAX - 1024)
-        return PA_ERR_UNSUPPORTED;
-    if (S == 0 || max_seqlen_q == 0 || total_q == 0) return PA_OK;
-    if (max_blocks_per_seq < 1 || num_blocks < 1) return PA_ERR_SHAPE;
-    if (!out || !q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !context_lens) return PA_ERR_NULL;
-    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_UNSUPPORTED;
-    // out is q itself (an item's queries are read before its rows are written) or lies clear of it
-    const uintptr_t o = reinterpret_cast<uintptr_t>(out), x = reinterpret_cast<uintptr_t>(q), apart = o < x ? x - o : o - x;
-    if (apart != 0 && apart < static_cast<uint64_t>(total_q) * Hq * D * 2) return PA_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < pa::chunk_attn_workspace(D) || !aligned16(workspace))
-        return PA_ERR_WORKSPACE;
-    pa::ChunkArgs a{};
-    a.out = out;
-    a.q = q;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.cu_q = cu_seqlens_q;
-    a.ctx = context_lens;
-    a.block_tables = block_tables;
-    a.S = S;
-    a.total_q = total_q;
-    a.max_seqlen_q = max_seqlen_q;
-    a.max_blocks = max_blocks_per_seq;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
-    a.D = D;
-    a.block_size = block_size;
-    a.num_blocks = num_blocks;
-    a.window = window;
-    a.scale = scale;
-    a.dtype = dtype;
-    a.workspace = workspace;
-    a.err = err;
+    const pa::ChunkArgs a{out,          q,          k_cache,  v_cache, cu_seqlens_q, context_lens,
+                          block_tables, S,          total_q,  max_seqlen_q, max_blocks_per_seq, Hq,
+                          Hkv,          D,          block_size, num_blocks, window, scale,
+                          dtype,        workspace,  err};
+    bool empty = false;
+    const pa_status st = check_chunk(a, workspace_bytes, false, empty);
+    if (st != PA_OK || empty) return st;
     return from_cuda(pa::launch_chunk_attn(a, stream));
+}
+
+size_t pa_chunk_attn_q8_workspace_size(int S, int Hq, int Hkv, int D) {
+    if (S <= 0 || check_heads(Hq, Hkv, D) != PA_OK) return 0;
+    return pa::chunk_q8_workspace(D);
+}
+
+pa_status pa_chunk_attn_q8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                           int max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                           const int32_t *context_lens, int S, int total_q, int max_seqlen_q,
+                           int window, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                           float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                           int32_t *err, cudaStream_t stream) {
+    const pa::ChunkQ8Args a{{out,          q,          k_cache,  v_cache, cu_seqlens_q, context_lens,
+                             block_tables, S,          total_q,  max_seqlen_q, max_blocks_per_seq, Hq,
+                             Hkv,          D,          block_size, num_blocks, window, scale,
+                             dtype,        workspace,  err},
+                            k_scale,
+                            v_scale};
+    bool empty = false;
+    const pa_status st = check_chunk(a.chunk, workspace_bytes, true, empty);
+    if (st != PA_OK || empty) return st;
+    if (!k_scale || !v_scale) return PA_ERR_NULL;
+    if (!aligned16(k_scale) || !aligned16(v_scale)) return PA_ERR_UNSUPPORTED;
+    return from_cuda(pa::launch_chunk_q8(a, stream));
 }
 
 pa_status pa_sample(int32_t *tokens, const void *logits, int64_t row_stride, int B, int V,

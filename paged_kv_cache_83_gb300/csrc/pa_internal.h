@@ -131,6 +131,13 @@ struct ChunkArgs {
 };
 size_t chunk_attn_workspace(int D);
 cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream);
+// The same over an 8-bit cache (chunk_attn_q8.cu).
+struct ChunkQ8Args {
+    ChunkArgs chunk;
+    const float *k_scale, *v_scale;
+};
+size_t chunk_q8_workspace(int D);
+cudaError_t launch_chunk_q8(const ChunkQ8Args &a, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------------------
 // Sampling (sample.cu).

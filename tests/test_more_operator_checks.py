@@ -1,4 +1,4 @@
-"""What norms + rotation + append and verification refuse, without a GPU: the status codes of the C entry points and the
+"""What norms + rotation + append, attention over the 8-bit cache and verification refuse, without a GPU: the status codes of the C entry points and the
 exceptions of the binding. Every call here fails a host-side check or is an empty no-op."""
 import pytest
 import torch
@@ -139,4 +139,51 @@ def test_verify_binding_refusals():
         _raises(TypeError, call, **kw)
     for kw in (dict(probs=torch.zeros(10)), dict(u=torch.zeros(5)), dict(tokens=torch.zeros(3, dtype=torch.int32)),
                dict(cu_seqlens_q=torch.zeros(4, dtype=torch.int32)), dict(draft_probs=torch.zeros(4, 9)), {}):
+        _raises(ValueError, call, **kw)
+
+
+def _q8(lib, **kw):
+    a = dict(out=FAR, q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, bt=FAKE, maxb=8, cu=FAKE, ctx=FAKE, S=2, Tq=8, max_q=4, window=0,
+             Hq=4, Hkv=2, D=64, bs=16, nb=16, scale=0.125, dt=0, ws=FAKE, ws_bytes=1 << 30, err=None, stream=None)
+    a.update(kw)
+    return lib.pa_chunk_attn_q8(*a.values())
+
+
+def test_chunk_attn_q8_refusals(lib):
+    for dt in (2, 3):
+        assert _q8(lib, dt=dt) == DTYPE
+    for kw in (dict(S=-1), dict(Tq=-1), dict(max_q=-1), dict(window=-1), dict(bs=0), dict(nb=-1), dict(nb=0), dict(maxb=0), dict(Hq=3),
+               dict(maxb=1 << 28), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert _q8(lib, **kw) == SHAPE, kw
+    for kw in (dict(D=80), dict(Hq=18), dict(S=65536), dict(nb=1 << 28), dict(out=FAR + 8), dict(q=FAKE + 2), dict(kc=FAKE + 8),
+               dict(ks=FAKE + 4), dict(vs=FAKE + 8), dict(out=FAKE + 512)):
+        assert _q8(lib, **kw) == UNSUPPORTED, kw
+    for name in ("out", "q", "kc", "vc", "ks", "vs", "bt", "cu", "ctx"):
+        assert _q8(lib, **{name: None}) == NULL, name
+    need = pa.pa_chunk_attn_q8_workspace_size(2, 4, 2, 64)
+    assert need > 0 and pa.pa_chunk_attn_q8_workspace_size(2, 4, 2, 80) == 0 and pa.pa_chunk_attn_q8_workspace_size(0, 4, 2, 64) == 0
+    for kw in (dict(ws=None), dict(ws_bytes=need - 1), dict(ws=FAKE + 8)):
+        assert _q8(lib, **kw) == WORKSPACE, kw
+    for kw in (dict(S=0), dict(Tq=0), dict(max_q=0)):
+        assert _q8(lib, **kw) == 0
+
+
+def test_chunk_attn_q8_binding_refusals():
+    S, Tq, Hq, Hkv, D, nb, bs = 2, 5, 4, 2, 64, 3, 16
+    h, e, i = torch.float16, torch.float8_e4m3fn, torch.int32
+
+    def call(**kw):
+        a = dict(out=torch.empty(Tq, Hq, D, dtype=h), q=torch.empty(Tq, Hq, D, dtype=h), k_cache=torch.empty(nb, bs, Hkv, D, dtype=e),
+                 v_cache=torch.empty(nb, bs, Hkv, D, dtype=e), k_scale=torch.ones(nb, Hkv, bs), v_scale=torch.ones(nb, Hkv, bs),
+                 block_tables=torch.zeros(S, 2, dtype=i), cu_seqlens_q=torch.zeros(S + 1, dtype=i),
+                 context_lens=torch.zeros(S, dtype=i), max_seqlen_q=3, scale=0.1)
+        a.update(kw)
+        pa.pa_chunk_attn_q8(**a)
+
+    for kw in (dict(k_cache=torch.empty(nb, bs, Hkv, D, dtype=h)), dict(v_cache=torch.empty(nb, bs, Hkv, D, dtype=torch.float8_e5m2)),
+               dict(q=torch.empty(Tq, Hq, D)), dict(k_scale=torch.ones(nb, Hkv, bs, dtype=h)), dict(k_scale=None),
+               dict(cu_seqlens_q=torch.zeros(S + 1)), dict(scale="x")):
+        _raises(TypeError, call, **kw)
+    for kw in (dict(k_scale=torch.ones(nb, bs, Hkv)), dict(v_scale=torch.ones(nb, Hkv)), dict(out=torch.empty(Tq + 1, Hq, D, dtype=h)),
+               dict(cu_seqlens_q=torch.zeros(S, dtype=i)), dict(window=-1), dict(max_seqlen_q=1 << 31), {}):
         _raises(ValueError, call, **kw)
