@@ -422,8 +422,8 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
  *
  * The e4m3 rows are operands of the tensor cores as they lie there; queries and softmax weights meet them as sums of e4m3 numbers.
  * Scores, references, sums and accumulators are fp32. A query's element is exact where its magnitude is above 2^-14 of the
- * largest of its row, below that to 2^-24 of the largest; a weight (times its value's scale) is rounded to within 2^-8 of itself, and
- * to within 2^-19 of the largest that was seen when the first keys of a piece were; the output is rounded once.
+ * largest of its row, below that to 2^-24 of the largest; a weight (times its value's scale) is rounded to within 2^-8 (bf16) or 2^-11 (fp16) of itself, and
+ * to within 2^-19 (2^-24) of the largest that was seen when the first keys of a piece were; the output is rounded once.
  *
  * k_cache, v_cache  e4m3 pools [num_blocks, block_size, Hkv, D].
  * k_scale, v_scale  fp32 [num_blocks, Hkv, block_size], 16-byte aligned. Positive; k_scale from 2^-126, v_scale from 2^-90 to 2^60. A

@@ -10,11 +10,12 @@
 // and what meets them is split into e4m3 pieces, side by side as further columns of the same instruction:
 //   q = 2^e (q0 + q1 / 32 [+ q2 / 1024]): two pieces hold a bf16 number (8 bits) exactly, three an fp16 number (11 bits),
 //     where its magnitude is above 2^-14 of its row's largest; below that the error is at most 2^-24 (2^-29) of the largest;
-//   w = w0 + w1 / 32, a weight of the softmax, with an error of at most 2^-8 of itself (bf16's is 2^-9) and 2^-16 absolute.
+//   w = w0 + w1 / 32 [+ w2 / 1024], a weight of the softmax, with an error of at most 2^-8 (2^-12) of itself, where bf16's (fp16's)
+//     is 2^-9 (2^-12), and 2^-16 (2^-21) absolute.
 // A softmax thread owns one key, so that both scales are one number a thread. The values' scale goes into the
 // exponent: x_j = s_j + log2 vs_j, w_j = 2^(x_j - m), O = sum w_j V8_j, and the sum takes w_j / vs_j = 2^(s_j - m). The reference m is
 // 4 below the largest x of the first tile and moves when some x exceeds it by more than 8: a w is at most 256,
-// below e4m3's 448, and what is smaller than 2^-16 beside a largest w of 16 counts for nothing.
+// below e4m3's 448, and what is smaller than 2^-16 (2^-21) beside a largest w of 16 counts for nothing.
 //
 // Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. The loads run ahead in rings of tiles; two streams of softmax
 // warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a
@@ -26,7 +27,7 @@
 //   warp 0      producer: K and V tiles of the streams in turn, the scales with the K tile
 //   warps 1, 2  one MMA issuer per stream
 //   warps 4-7   softmax of stream A (tiles 0, 2, ... of a segment), warps 8-11 of stream B (1, 3, ...)
-//   TMEM columns: S_A, S_B (pieces x NT each), O_A, O_B (2 NT each); lanes are keys in S and head elements in O.
+//   TMEM columns: S_A, S_B (NT for each piece), O_A, O_B (likewise); lanes are keys in S and head elements in O.
 #include <type_traits>
 
 #include "chunk_narrow.cuh"
@@ -44,11 +45,11 @@ struct Q8Params : ChunkParams {
 };
 
 // NT columns a stream. kCols: the streams halve the query rows (2 NT of them) and both take every key tile, from
-// rings that they share; else they halve the key tiles, each with rings of its own. QP: pieces of a query.
+// rings that they share; else they halve the key tiles, each with rings of its own. QP: pieces of a number.
 template <int HD, int NT, int QP, bool kCols>
 struct LayQ8 {
     static constexpr int kNC = kCols ? 2 * NT : NT;         // query rows
-    static constexpr int PP = 2;                            // pieces of a weight
+    static constexpr int PP = QP;                           // pieces of a weight
     static constexpr int kKV = BN * HD;                     // bytes of a tile
     static constexpr int kAtom = 8 * HD;                    // eight rows: the swizzle's period
     static constexpr int kQ = kNC * QP * HD;
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         auto split_q = [&](const SegInfo &it, int n) -> bool {
             if (!warp_wait(bar(Lay::B_QEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag)) return false;
             constexpr int kEach = HD / 32;  // elements of a lane: 4 or 2
-            constexpr int kAhead = 4;       // rows in flight
+            constexpr int kAhead = 16;      // rows in flight
             const int rows = it.tok * p.G;
             unsigned char *dst = smem + Lay::OFF_Q + (n & 1) * Lay::kQ;
             float *qs = fl + Lay::kQs + (n & 3) * Lay::kNC;
@@ -658,22 +659,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 if (t > 0 && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
 #pragma unroll
                 for (int q = 0; q < NT / 16; ++q) {
-                    uint32_t hi[4], lo[4];
+                    uint32_t piece[Lay::PP][4];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int c = q * 16 + e * 2;
                         const float w0 = fast_exp2(x[c]), w1 = fast_exp2(x[c + 1]);
                         l[c] = fmaf(w0, inv_vs, l[c]);
                         l[c + 1] = fmaf(w1, inv_vs, l[c + 1]);
-                        // the weights as the tensor cores take them, two e4m3 numbers each; the sum is of the weights themselves
-                        const __half2 w = __floats2half2_rn(w0, w1);
-                        const uint32_t a = to_e4m3x2(w), b = to_e4m3x2(left_of(w, a));
-                        hi[e >> 1] = e & 1 ? hi[e >> 1] | a << 16 : a;
-                        lo[e >> 1] = e & 1 ? lo[e >> 1] | b << 16 : b;
+                        // the weights as the tensor cores take them, two or three e4m3 numbers each; the sum is of the weights
+                        // themselves
+                        __half2 w = __floats2half2_rn(w0, w1);
+#pragma unroll
+                        for (int i = 0; i < Lay::PP; ++i) {
+                            const uint32_t a = to_e4m3x2(w);
+                            if (i + 1 < Lay::PP) w = left_of(w, a);
+                            piece[i][e >> 1] = e & 1 ? piece[i][e >> 1] | a << 16 : a;
+                        }
                     }
                     // 16-byte chunk c of a key's row sits at c ^ (key % 8)
-                    *reinterpret_cast<uint4 *>(prow + ((q ^ (wt & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(prow + (((NT / 16 + q) ^ (wt & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int i = 0; i < Lay::PP; ++i)
+                        *reinterpret_cast<uint4 *>(prow + (((i * (NT / 16) + q) ^ (wt & 7)) << 4)) =
+                            make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -728,21 +735,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             constexpr int W = 8;
 #pragma unroll 1
             for (int c0 = c_lo; c0 < c_lo + kMine && c0 < rows; c0 += W) {
-                uint32_t a[W], a1[W], b[W], b1[W];
-                tmem_ld<W>(oa + c0, a);
-                tmem_ld<W>(oa + NT + c0, a1);
-                if (cnt_b > 0) {
-                    tmem_ld<W>(ob + c0, b);
-                    tmem_ld<W>(ob + NT + c0, b1);
-                }
-                tmem_wait_ld();
                 float o[W];
+                // the pieces of column c0 + e of an accumulator, joined
+                auto read_o = [&](uint32_t at, float (&v)[W]) {
+                    uint32_t part[Lay::PP][W];
 #pragma unroll
-                for (int e = 0; e < W; ++e) o[e] = fmaf(__uint_as_float(a1[e]), 0x1p-5f, __uint_as_float(a[e])) * wa[c0 + e];
-                if (cnt_b > 0)
+                    for (int i = 0; i < Lay::PP; ++i) tmem_ld<W>(at + i * NT + c0, part[i]);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        o[e] = fmaf(fmaf(__uint_as_float(b1[e]), 0x1p-5f, __uint_as_float(b[e])), wb[c0 + e], o[e]);
+                    for (int e = 0; e < W; ++e) {
+                        v[e] = __uint_as_float(part[Lay::PP - 1][e]);
+#pragma unroll
+                        for (int i = Lay::PP - 2; i >= 0; --i) v[e] = fmaf(v[e], 0x1p-5f, __uint_as_float(part[i][e]));
+                    }
+                };
+                read_o(oa, o);
+#pragma unroll
+                for (int e = 0; e < W; ++e) o[e] *= wa[c0 + e];
+                if (cnt_b > 0) {
+                    float v[W];
+                    read_o(ob, v);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) o[e] = fmaf(v[e], wb[c0 + e], o[e]);
+                }
                 if (d >= HD) continue;
                 if (piece) {
                     float *pc = piece + 2 * Lay::kNC + c0 * HD + d;  // columns behind the rows: room, never read

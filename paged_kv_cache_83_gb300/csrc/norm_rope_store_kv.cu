@@ -19,8 +19,11 @@ namespace pa {
 
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 128;
 constexpr int kNormRotUnits = 16;  // rot_dim <= 256
+constexpr int kAhead = 2;       // steps in flight
+constexpr int kNormBlocks = 8;  // of an SM
+constexpr int kFullWarps = 8;   // of an SM: tokens from which on a warp takes a whole one
 
 struct NormRopeParams {
     const unsigned char *q, *k, *v;  // token strides below, in bytes
@@ -33,7 +36,8 @@ struct NormRopeParams {
     int32_t *err;
     long long num_slots;
     BlockGeom geom;
-    int T, Hq, Hkv, D, rot, n_axes, max_pos, units, lanes, row_par;
+    int T, Hq, Hkv, D, rot, n_axes, max_pos, units, lanes, lanes_log2;
+    int qk_steps, steps, parts, part_steps;
     float inv_d, eps;
     uint32_t axis[kNormRotUnits];  // four bits per pair: the axis of each of a unit's eight pairs
 };
@@ -46,182 +50,231 @@ __device__ __forceinline__ uint4 ld_row(const void *p) {
                  : "l"(p));
     return v;
 }
+__device__ __forceinline__ float max_nan3(float a, float b, float c) {  // NaN where one is NaN
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// eight numbers of a row in fp32, as four pairs
+struct Eight {
+    uint64_t p[4];
+};
 template <class E>
-__device__ __forceinline__ float squares(const uint4 &x, float sum) {
-    float f[8];
-    unpack8<E>(x, f);
+__device__ __forceinline__ Eight widen8(const uint4 &x) {
+    return {{unpack_pair<E>(x.x), unpack_pair<E>(x.y), unpack_pair<E>(x.z), unpack_pair<E>(x.w)}};
+}
+template <class E>
+__device__ __forceinline__ uint4 pack8(const Eight &f) {
+    return make_uint4(E::pack2(f2_lo(f.p[0]), f2_hi(f.p[0])), E::pack2(f2_lo(f.p[1]), f2_hi(f.p[1])),
+                      E::pack2(f2_lo(f.p[2]), f2_hi(f.p[2])), E::pack2(f2_lo(f.p[3]), f2_hi(f.p[3])));
+}
+__device__ __forceinline__ float largest(const Eight &f, float most) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
-    return sum;
+    for (int e = 0; e < 4; ++e) most = max_nan3(most, fabsf(f2_lo(f.p[e])), fabsf(f2_hi(f.p[e])));
+    return most;
 }
-template <class E>
-__device__ __forceinline__ uint4 pack8(const float *f) {
-    return make_uint4(E::pack2(f[0], f[1]), E::pack2(f[2], f[3]), E::pack2(f[4], f[5]), E::pack2(f[6], f[7]));
-}
-// eight quotients f / s, each correctly rounded, then rounded to e4m3 (nearest even, beyond 448: 448, NaN stays NaN)
-__device__ __forceinline__ uint2 quantise8(const float *f, float s) {
+// f * inv, rounded to e4m3 (nearest even, beyond 448: 448, NaN stays NaN)
+__device__ __forceinline__ uint2 quantise8(const Eight &f, float inv) {
+    const uint64_t by = f2_pack(inv, inv);
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+        const uint64_t x = f2_mul(f.p[e], by);
         uint16_t two;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(__fdiv_rn(f[2 * e + 1], s)), "f"(__fdiv_rn(f[2 * e], s)));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(f2_hi(x)), "f"(f2_lo(x)));
         w[e] = two;
     }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// kRows head rows per thread, loaded together before any is stored.
-template <class E, int kRows, bool kPairs, bool kQ8>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_store_kv_kernel(const __grid_constant__ NormRopeParams p) {
-    asm volatile("griddepcontrol.launch_dependents;");  // the attention's set-up may run beside this grid
-    const int per_token = p.lanes * p.row_par;
-    const long long idx = static_cast<long long>(blockIdx.x) * kNormThreads + threadIdx.x;
-    const int t = static_cast<int>(idx / per_token);
-    const int in_token = static_cast<int>(idx - static_cast<long long>(t) * per_token);
-    const int row0 = in_token / p.lanes, u = in_token & (p.lanes - 1);
-    // Every lane stays for the shuffles; those of a token that is not there, padding or refused load and store nothing.
-    bool live = t < p.T;
-    const long long slot = live ? __ldg(p.slot_mapping + t) : -1;
-    live = slot >= 0;
-    int pos[4] = {0, 0, 0, 0};  // of each axis; those that are not there hold the first's
-    bool bad_pos = false;
-    if (p.rot > 0 && live) {
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            pos[a] = a == 0 || a < p.n_axes ? __ldg(p.positions + static_cast<size_t>(a) * p.T + t) : pos[0];
-            bad_pos |= static_cast<unsigned>(pos[a]) >= static_cast<unsigned>(p.max_pos);
-        }
-    }
-    if (live && (slot >= p.num_slots || bad_pos)) {
-        if (in_token == 0)
-            raise_err(p.err, (slot >= p.num_slots ? PA_DEVERR_SLOT : 0) | (bad_pos ? PA_DEVERR_POSITION : 0));
-        live = false;
-    }
-    live = live && u < p.units;
+// A warp takes a token, or a part of it. It goes over the token's rows 32 / lanes at a time (a step): first queries and keys
+// side by side, then values. kAhead steps are loaded together before any is stored.
+template <class E, bool kPairs, bool kQ8>
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_kernel(const __grid_constant__ NormRopeParams p) {
+    const int lane = threadIdx.x & 31;
+    const unsigned warp = blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32;
+    const int t = static_cast<int>(warp / static_cast<unsigned>(p.parts)), part = static_cast<int>(warp) - t * p.parts;
+    const int u = lane & (p.lanes - 1), row_of_lane = lane >> p.lanes_log2;
     const int n8 = p.rot / 16;  // units that hold rotated pairs
-    const int rows = p.Hq + 2 * p.Hkv;
+    const int n_qk = p.Hq + p.Hkv;
     // The unit's two chunks of 8 elements in a head row of q or k, and of v. The last unit of a row may have one only.
-    int e0, e1;
-    if (u < n8) {
-        e0 = kPairs ? u * 16 : u * 8;
-        e1 = kPairs ? u * 16 + 8 : p.rot / 2 + u * 8;
-    } else {
-        e0 = p.rot + (u - n8) * 16;
-        e1 = e0 + 8;
-    }
-    const int v0 = u * 16, v1 = v0 + 8;
-
-    uint4 x0[kRows], x1[kRows];
+    const int e0 = u < n8 ? kPairs ? u * 16 : u * 8 : p.rot + (u - n8) * 16;
+    const int e1 = u < n8 && !kPairs ? p.rot / 2 + u * 8 : e0 + 8;
+    const bool there0 = u < p.units && e0 < p.D, there1 = u < p.units && e1 < p.D;
+    // launched beside what precedes it in the stream, whose results are read and written from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");  // the attention's set-up may run beside this grid
+    if (t >= p.T) return;
+    // slot and positions side by side; the axes that are not there hold the first's position
+    const int slot = *(p.slot_mapping + t);
+    int pos[4] = {0, 0, 0, 0};
+    if (p.rot > 0) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = row0 + i * p.row_par;
-        x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
-        if (!live || r >= rows) continue;
-        const bool is_v = r >= p.Hq + p.Hkv;
-        const unsigned char *src = r < p.Hq ? p.q + t * p.q_stride + static_cast<size_t>(r) * p.D * 2
-                                   : is_v   ? p.v + t * p.v_stride + static_cast<size_t>(r - p.Hq - p.Hkv) * p.D * 2
-                                            : p.k + t * p.k_stride + static_cast<size_t>(r - p.Hq) * p.D * 2;
-        const int a = is_v ? v0 : e0, b = is_v ? v1 : e1;
-        if (a < p.D) x0[i] = ld_row(src + a * 2);
-        if (b < p.D) x1[i] = ld_row(src + b * 2);
+        for (int a = 0; a < 4; ++a) pos[a] = a == 0 || a < p.n_axes ? *(p.positions + static_cast<size_t>(a) * p.T + t) : pos[0];
     }
-    float c[8], s[8];
-    if (live && u < n8 && row0 < p.Hq + p.Hkv) {
+    if (slot < 0) return;  // padding: none of this token's rows is read or written
+    const unsigned top = max(max(static_cast<unsigned>(pos[0]), static_cast<unsigned>(pos[1])),
+                             max(static_cast<unsigned>(pos[2]), static_cast<unsigned>(pos[3])));
+    const bool bad_pos = p.rot > 0 && top >= static_cast<unsigned>(p.max_pos);
+    if (slot >= p.num_slots || bad_pos) {
+        if (part == 0 && lane == 0)
+            raise_err(p.err, (slot >= p.num_slots ? PA_DEVERR_SLOT : 0) | (bad_pos ? PA_DEVERR_POSITION : 0));
+        return;
+    }
+    // cosines and sines of the unit's pairs: pair e is element e of both chunks, or elements 2e and 2e + 1
+    uint64_t c[4], s[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = f2_pack(1.f, 1.f), s[e] = f2_pack(0.f, 0.f);
+    if (u < n8) {
         const uint32_t axes = p.axis[u];
         const int half = p.rot / 2;
         const auto pos_of = [&](uint32_t a) { return a & 2u ? a & 1u ? pos[3] : pos[2] : a & 1u ? pos[1] : pos[0]; };
         if (axes == (axes & 15u) * 0x11111111u) {
             // one position for the unit: four 16-byte loads
-            const float4 *row =
-                reinterpret_cast<const float4 *>(p.cos_sin + static_cast<size_t>(pos_of(axes & 3u)) * p.rot + u * 8);
-            const float4 *srow = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(row) + half);
-            const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(srow), s1 = __ldg(srow + 1);
-            c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-            s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+            const float *row = p.cos_sin + static_cast<size_t>(pos_of(axes & 3u)) * p.rot + u * 8;
+            const float4 c0 = *reinterpret_cast<const float4 *>(row), c1 = *reinterpret_cast<const float4 *>(row + 4),
+                         s0 = *reinterpret_cast<const float4 *>(row + half), s1 = *reinterpret_cast<const float4 *>(row + half + 4);
+            c[0] = f2_pack(c0.x, c0.y), c[1] = f2_pack(c0.z, c0.w), c[2] = f2_pack(c1.x, c1.y), c[3] = f2_pack(c1.z, c1.w);
+            s[0] = f2_pack(s0.x, s0.y), s[1] = f2_pack(s0.z, s0.w), s[2] = f2_pack(s1.x, s1.y), s[3] = f2_pack(s1.z, s1.w);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float *row = p.cos_sin + static_cast<size_t>(pos_of((axes >> (4 * e)) & 3u)) * p.rot + u * 8 + e;
-                c[e] = __ldg(row);
-                s[e] = __ldg(row + half);
+            for (int e = 0; e < 4; ++e) {
+                const float *x = p.cos_sin + static_cast<size_t>(pos_of((axes >> (8 * e)) & 3u)) * p.rot + u * 8 + 2 * e;
+                const float *y = p.cos_sin + static_cast<size_t>(pos_of((axes >> (8 * e + 4)) & 3u)) * p.rot + u * 8 + 2 * e + 1;
+                c[e] = f2_pack(*x, *y);
+                s[e] = f2_pack(x[half], y[half]);
             }
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
     }
-    // the rows' sums of squares, all rows side by side
-    float rstd[kRows];
+    const unsigned char *const q_row = p.q + t * p.q_stride + e0 * 2, *const k_row = p.k + t * p.k_stride + e0 * 2,
+                        *const v_row = p.v + t * p.v_stride + u * 32;
+    const int row_bytes = p.D * 2, next = (e1 - e0) * 2, per_step = 32 >> p.lanes_log2;
+    const size_t cache_row = static_cast<size_t>(slot) * p.Hkv;
+    size_t scale_row = 0;  // index of the slot's scale of kv head 0
+    if constexpr (kQ8) scale_row = static_cast<size_t>(p.geom.block_of(slot)) * p.Hkv * p.geom.block_size + p.geom.offset_of(slot);
+    // a row of keys or values in 8 bits; the warp's lanes all come here
+    const auto store8 = [&](const Eight &f, const Eight &g, unsigned char *dst, float *scales, int h, bool on0, bool on1, int apart) {
+        float most = largest(g, largest(f, 0.f));
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) rstd[i] = squares<E>(x1[i], squares<E>(x0[i], 0.f));
-    for (int o = 1; o < p.lanes; o <<= 1)
+        for (int o = 1; o < 32; o <<= 1)
+            if (o < p.lanes) most = max_nan3(most, most, __shfl_xor_sync(0xffffffffu, most, o));
+        float scale = __fdiv_rn(most, 448.f);
+        if (scale < 0x1p-90f) scale = 0x1p-90f;
+        const float inv = __frcp_rn(scale);
+        if (on0) *reinterpret_cast<uint2 *>(dst) = quantise8(f, inv);
+        if (on1) *reinterpret_cast<uint2 *>(dst + apart) = quantise8(g, inv);
+        if (on0 && u == 0) scales[scale_row + static_cast<size_t>(h) * p.geom.block_size] = scale;
+    };
+    const int end = min((part + 1) * p.part_steps, p.steps);
+    for (int step = part * p.part_steps; step < end; step += kAhead) {
+        uint4 x0[kAhead], x1[kAhead];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) rstd[i] += __shfl_xor_sync(0xffffffffu, rstd[i], o);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = row0 + i * p.row_par;
-        const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv, there = live && r < rows;
-        const int a = is_v ? v0 : e0, b = is_v ? v1 : e1;
-        float f[16];
-        unpack8<E>(x0[i], *reinterpret_cast<float(*)[8]>(f));
-        unpack8<E>(x1[i], *reinterpret_cast<float(*)[8]>(f + 8));
-        const unsigned char *w = is_q ? p.q_weight : is_v ? nullptr : p.k_weight;
-        if (w && there) {
-            const float m = rsqrtf(fmaf(rstd[i], p.inv_d, p.eps));
-            float g[8];
-            unpack8<E>(a < p.D ? __ldg(reinterpret_cast<const uint4 *>(w + a * 2)) : make_uint4(0, 0, 0, 0), g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f[e] * m * g[e];
-            unpack8<E>(b < p.D ? __ldg(reinterpret_cast<const uint4 *>(w + b * 2)) : make_uint4(0, 0, 0, 0), g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[8 + e] = f[8 + e] * m * g[e];
-        }
-        if (!is_v && u < n8) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float &y0 = kPairs ? f[2 * e] : f[e], &y1 = kPairs ? f[2 * e + 1] : f[8 + e];
-                const float z0 = y0 * c[e] - y1 * s[e], z1 = y1 * c[e] + y0 * s[e];
-                y0 = z0, y1 = z1;
+        for (int i = 0; i < kAhead; ++i) {
+            x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
+            if (step + i < p.qk_steps) {
+                const int r = (step + i) * per_step + row_of_lane;
+                const unsigned char *src = r < p.Hq ? q_row + r * row_bytes : k_row + (r - p.Hq) * row_bytes;
+                if (there0 && r < n_qk) x0[i] = ld_row(src);
+                if (there1 && r < n_qk) x1[i] = ld_row(src + next);
+            } else {
+                const int r = (step + i - p.qk_steps) * per_step + row_of_lane;
+                const unsigned char *src = v_row + r * row_bytes;
+                const bool mine = step + i < end && r < p.Hkv;
+                if (mine && u * 16 < p.D) x0[i] = ld_row(src);
+                if (mine && u * 16 + 8 < p.D) x1[i] = ld_row(src + 16);
             }
         }
-        if (!kQ8 || is_q) {
-            if (there) {
-                unsigned char *dst = is_q   ? p.q_out + t * p.qo_stride + static_cast<size_t>(r) * p.D * 2
-                                     : is_v ? p.v_cache + (static_cast<size_t>(slot) * p.Hkv + (r - p.Hq - p.Hkv)) * p.D * 2
-                                            : p.k_cache + (static_cast<size_t>(slot) * p.Hkv + (r - p.Hq)) * p.D * 2;
-                if (a < p.D) stg128(dst + a * 2, is_v ? x0[i] : pack8<E>(f));  // values are bit copies
-                if (b < p.D) stg128(dst + b * 2, is_v ? x1[i] : pack8<E>(f + 8));
-            }
-        }
-        if constexpr (kQ8) {
-            // magnitudes as whole numbers, so that a NaN is the largest
-            uint32_t most = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) most = max(most, __float_as_uint(f[e]) & 0x7fffffffu);
-            for (int o = 1; o < p.lanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-            float scale = __fdiv_rn(__uint_as_float(most), 448.f);
-            if (scale < 0x1p-90f) scale = 0x1p-90f;
-            if (there && !is_q) {
-                const int g = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
-                unsigned char *dst = (is_v ? p.v_cache : p.k_cache) + (static_cast<size_t>(slot) * p.Hkv + g) * p.D;
-                if (a < p.D) *reinterpret_cast<uint2 *>(dst + a) = quantise8(f, scale);
-                if (b < p.D) *reinterpret_cast<uint2 *>(dst + b) = quantise8(f + 8, scale);
-                const int s32 = static_cast<int>(slot), block = p.geom.block_of(s32);
-                if (u == 0)
-                    (is_v ? p.v_scale : p.k_scale)[(static_cast<size_t>(block) * p.Hkv + g) * p.geom.block_size +
-                                                   p.geom.offset_of(s32)] = scale;
+        for (int i = 0; i < kAhead; ++i) {
+            if (step + i >= end) break;
+            if (step + i >= p.qk_steps) {
+                const int r = (step + i - p.qk_steps) * per_step + row_of_lane;
+                const bool on0 = r < p.Hkv && u * 16 < p.D, on1 = r < p.Hkv && u * 16 + 8 < p.D;
+                if constexpr (kQ8) {
+                    store8(widen8<E>(x0[i]), widen8<E>(x1[i]), p.v_cache + (cache_row + r) * p.D + u * 16, p.v_scale, r, on0, on1, 8);
+                } else {
+                    unsigned char *dst = p.v_cache + (cache_row + r) * row_bytes + u * 32;  // values are bit copies
+                    if (on0) stg128(dst, x0[i]);
+                    if (on1) stg128(dst + 16, x1[i]);
+                }
+                continue;
+            }
+            const int r = (step + i) * per_step + row_of_lane;
+            const bool is_q = r < p.Hq, on0 = there0 && r < n_qk, on1 = there1 && r < n_qk;
+            Eight f = widen8<E>(x0[i]), g = widen8<E>(x1[i]);
+            if (p.q_weight || p.k_weight) {
+                uint64_t sum = f2_mul(f.p[0], f.p[0]);
+#pragma unroll
+                for (int e = 1; e < 4; ++e) sum = f2_fma(f.p[e], f.p[e], sum);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum = f2_fma(g.p[e], g.p[e], sum);
+                float squares = f2_lo(sum) + f2_hi(sum);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+                    if (o < p.lanes) squares += __shfl_xor_sync(0xffffffffu, squares, o);
+                const unsigned char *w = is_q ? p.q_weight : p.k_weight;
+                if (w) {
+                    const float m1 = rsqrtf(fmaf(squares, p.inv_d, p.eps));
+                    const uint64_t m = f2_pack(m1, m1);
+                    const uint4 w0 = on0 ? *reinterpret_cast<const uint4 *>(w + e0 * 2) : make_uint4(0, 0, 0, 0),
+                                w1 = on1 ? *reinterpret_cast<const uint4 *>(w + e1 * 2) : make_uint4(0, 0, 0, 0);
+                    const Eight wf = widen8<E>(w0), wg = widen8<E>(w1);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f.p[e] = f2_mul(f2_mul(f.p[e], m), wf.p[e]);
+                        g.p[e] = f2_mul(f2_mul(g.p[e], m), wg.p[e]);
+                    }
+                }
+            }
+            if (u < n8) {
+                if constexpr (kPairs) {
+                    // pairs lie side by side: (x0, x1) c + (-x1, x0) s, the latter product rounded (as in the rotation without norms)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const auto turn = [](uint64_t x, float cc, float ss) {
+                            return f2_fma(x, f2_pack(cc, cc), f2_mul(f2_pack(-f2_hi(x), f2_lo(x)), f2_pack(ss, ss)));
+                        };
+                        uint64_t &lo = f.p[e], &hi = g.p[e];
+                        lo = turn(lo, e & 1 ? f2_hi(c[e >> 1]) : f2_lo(c[e >> 1]), e & 1 ? f2_hi(s[e >> 1]) : f2_lo(s[e >> 1]));
+                        hi = turn(hi, e & 1 ? f2_hi(c[2 + (e >> 1)]) : f2_lo(c[2 + (e >> 1)]),
+                                  e & 1 ? f2_hi(s[2 + (e >> 1)]) : f2_lo(s[2 + (e >> 1)]));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint64_t minus = f2_pack(-f2_lo(g.p[e]), -f2_hi(g.p[e]));
+                        const uint64_t y0 = f2_fma(f.p[e], c[e], f2_mul(minus, s[e])), y1 = f2_fma(g.p[e], c[e], f2_mul(f.p[e], s[e]));
+                        f.p[e] = y0, g.p[e] = y1;
+                    }
+                }
+            }
+            if (!kQ8 || is_q) {
+                unsigned char *dst = is_q ? p.q_out + t * p.qo_stride + r * row_bytes : p.k_cache + (cache_row + (r - p.Hq)) * row_bytes;
+                if (on0) stg128(dst + e0 * 2, pack8<E>(f));
+                if (on1) stg128(dst + e1 * 2, pack8<E>(g));
+            }
+            if constexpr (kQ8) {
+                // (steps of queries alone have nothing for the cache)
+                if ((step + i + 1) * per_step > p.Hq)
+                    store8(f, g, p.k_cache + (cache_row + (r - p.Hq)) * p.D + e0, p.k_scale, r - p.Hq, on0 && !is_q, on1 && !is_q, e1 - e0);
             }
         }
     }
 }
 
-template <class E, int kRows, bool kQ8>
+template <class E, bool kQ8>
 cudaError_t launch_norm_typed(const NormRopeParams &prm, bool pairs, unsigned grid, cudaStream_t stream) {
-    if (pairs)
-        norm_rope_store_kv_kernel<E, kRows, true, kQ8><<<grid, kNormThreads, 0, stream>>>(prm);
-    else
-        norm_rope_store_kv_kernel<E, kRows, false, kQ8><<<grid, kNormThreads, 0, stream>>>(prm);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kNormThreads);
+    return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, true, kQ8>, prm)
+                 : cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, false, kQ8>, prm);
 }
 
 }  // namespace
@@ -254,22 +307,21 @@ cudaError_t launch_norm_rope_store_kv(const NormRopeStoreArgs &n, cudaStream_t s
     prm.inv_d = 1.f / a.D, prm.eps = n.eps;
     // a row's rotated units, then its other chunks in pairs; v rows, all chunks in pairs, never need more
     prm.units = a.rot_dim / 16 + (a.D - a.rot_dim + 15) / 16;
-    for (prm.lanes = 1; prm.lanes < prm.units;) prm.lanes *= 2;
+    for (prm.lanes = 1; prm.lanes < prm.units; prm.lanes *= 2) ++prm.lanes_log2;
     for (int i = 0; a.pair_axis && i < a.rot_dim / 2; ++i)
         prm.axis[i / 8] |= static_cast<uint32_t>(a.pair_axis[i]) << (4 * (i % 8));
-    const int rows = a.Hq + 2 * a.Hkv;
-    const long long all = static_cast<long long>(a.T) * prm.lanes * rows;
-    const int each = all > static_cast<long long>(device_sm_count()) * 2048 ? 4 : 1;
-    prm.row_par = (rows + each - 1) / each;
-    const long long threads = static_cast<long long>(a.T) * prm.lanes * prm.row_par;
-    const unsigned grid = static_cast<unsigned>((threads + kNormThreads - 1) / kNormThreads);
+    const int per_step = 32 >> prm.lanes_log2;
+    prm.qk_steps = (a.Hq + a.Hkv + per_step - 1) / per_step;
+    prm.steps = prm.qk_steps + (a.Hkv + per_step - 1) / per_step;
+    // A warp a token where that leaves the SMs full, else a step each: the time is then one chain of dependent loads.
+    prm.part_steps = a.T > device_sm_count() * kFullWarps ? prm.steps : 1;
+    prm.parts = (prm.steps + prm.part_steps - 1) / prm.part_steps;
+    const long long warps = static_cast<long long>(a.T) * prm.parts;
+    const unsigned grid = static_cast<unsigned>((warps + kNormThreads / 32 - 1) / (kNormThreads / 32));
     auto go = [&](auto e) {
         using E = decltype(e);
-        if (n.q8)
-            return each == 4 ? launch_norm_typed<E, 4, true>(prm, a.interleaved, grid, stream)
-                             : launch_norm_typed<E, 1, true>(prm, a.interleaved, grid, stream);
-        return each == 4 ? launch_norm_typed<E, 4, false>(prm, a.interleaved, grid, stream)
-                         : launch_norm_typed<E, 1, false>(prm, a.interleaved, grid, stream);
+        return n.q8 ? launch_norm_typed<E, true>(prm, a.interleaved, grid, stream)
+                    : launch_norm_typed<E, false>(prm, a.interleaved, grid, stream);
     };
     return a.dtype == PA_BF16 ? go(BF16{}) : go(F16{});
 }
