@@ -97,6 +97,14 @@ template <int HD>
 __device__ __forceinline__ int swizzled(int r, int c) {
     return r * HD + ((HD == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
+// warp_wait with one copy of its loop for the whole kernel: the roles' code has to stay in the instruction cache (inlined
+// everywhere, fetching instructions bounded the kernel: 305 us for 256 single tokens over 100-4096 keys)
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return warp_wait(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return __all_sync(kFull, mbar_try_wait(bar, parity)) || wait_on(bar, parity, abort_flag);
+}
 // D (+)= A B of e4m3 operands with fp32 accumulation
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -148,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
     if (tid < Lay::NBAR) {
         uint32_t count = 1;
         if (tid >= Lay::B_QEMPTY && tid < Lay::B_KFULL) count = 2;                    // both issuers
+        if (!kGather && tid >= Lay::B_KFULL && tid < Lay::B_KEMPTY) count = 1 + 32;  // the tile, and each lane's scales
         if (tid >= Lay::B_KEMPTY && tid < Lay::B_VFULL) count = kCols ? 2 + 8 : 1 + 4;  // issuers and softmax warps
         if (kCols && tid >= Lay::B_VEMPTY && tid < Lay::B_S) count = 2;
         if (tid >= Lay::B_F && tid < Lay::B_O) count = 4;                // F, P, WG: four warps
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
 
     // every role reads the segments in the same order: segment n sits in queue entry n % 4
     auto read_seg = [&](int n, SegInfo &it) -> bool {
-        if (!warp_wait(bar(Lay::B_IFULL + (n & 3)), (n >> 2) & 1, abort_flag)) return false;
+        if (!wait_for(bar(Lay::B_IFULL + (n & 3)), (n >> 2) & 1, abort_flag)) return false;
         it = items[n & 3];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Lay::B_IEMPTY + (n & 3)));
@@ -193,67 +202,58 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         // [128, 256). The factor that takes scores back, with the softmax's scale, goes to the segment's entry of four:
         // the softmax of segment n - 4 is over when the issuers have let go of segment n - 2's queries.
         auto split_q = [&](const SegInfo &it, int n) -> bool {
-            if (!warp_wait(bar(Lay::B_QEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag)) return false;
-            constexpr int kEach = HD / 32;  // elements of a lane: 4 or 2
-            constexpr int kAhead = 16;      // rows in flight
-            const int rows = it.tok * p.G;
+            if (!wait_for(bar(Lay::B_QEMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag)) return false;
+            // 16 elements a lane, one 16-byte chunk of each piece; kStepRows rows at a time, two such steps in flight
+            constexpr int kLanes = HD / 16, kStepRows = 32 / kLanes;
+            const int rows = it.tok * p.G, c16 = lane % kLanes;
             unsigned char *dst = smem + Lay::OFF_Q + (n & 1) * Lay::kQ;
             float *qs = fl + Lay::kQs + (n & 3) * Lay::kNC;
-            const T *q = static_cast<const T *>(p.q);
-            for (int r0 = 0; r0 < rows; r0 += kAhead) {
-                uint32_t w[kAhead][kEach / 2];
-                uint32_t most[kAhead];
+            auto load = [&](int r, uint4 (&w)[2]) {
+                r = min(r, rows - 1);
+                const int tok = p.div_g(r);
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const T *>(p.q) + (static_cast<size_t>(it.tok0 + tok) * p.Hq + it.g * p.G + (r - tok * p.G)) * HD + c16 * 16);
+                w[0] = __ldcg(src), w[1] = __ldcg(src + 1);
+            };
+            uint4 ahead[2];
+            load(lane / kLanes, ahead);
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += kStepRows) {
+                const int r = r0 + lane / kLanes;
+                const uint4 w0 = ahead[0], w1 = ahead[1];
+                load(r + kStepRows, ahead);
+                const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                uint32_t most = 0;
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const int r = min(r0 + k, rows - 1), tok = p.div_g(r);
-                    const T *src = q + (static_cast<size_t>(it.tok0 + tok) * p.Hq + it.g * p.G + (r - tok * p.G)) * HD + lane * kEach;
-                    if constexpr (kEach == 4) {
-                        const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(src));
-                        w[k][0] = v.x, w[k][1] = v.y;
-                    } else {
-                        w[k][0] = __ldcg(reinterpret_cast<const uint32_t *>(src));
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = E::unpack2(w[e]);
+                    most = max(most, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
                 }
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    most[k] = 0;
+                for (int o = 1; o < kLanes; o <<= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+                const uint32_t e8 = max(most >> 23, 8u);  // exponent, kept where both factors are normal
+                const float up = __uint_as_float((261u - e8) << 23);
+                // a row that is not finite gives scores that are not
+                const float down = e8 == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e8 - 7u) << 23) * p.scale_log2;
+                uint32_t piece[QP][4];
 #pragma unroll
-                    for (int e = 0; e < kEach / 2; ++e) {
-                        const float2 f = E::unpack2(w[k][e]);
-                        most[k] = max(most[k], max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-                    }
-                    most[k] = __reduce_max_sync(kFull, most[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const int r = r0 + k;
-                    if (r >= rows) break;
-                    const uint32_t e8 = max(most[k] >> 23, 8u);  // exponent, kept where both factors are normal
-                    const float up = __uint_as_float((261u - e8) << 23);
-                    // a row that is not finite gives scores that are not
-                    const float down = e8 == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((e8 - 7u) << 23) * p.scale_log2;
-                    __half2 v[kEach / 2];
-#pragma unroll
-                    for (int e = 0; e < kEach / 2; ++e) {
-                        const float2 f = E::unpack2(w[k][e]);
-                        v[e] = __floats2half2_rn(f.x * up, f.y * up);  // exact down to 2^-17 of the largest
-                    }
-                    const int stream = r / NT, row0 = stream * QP * NT + r % NT;
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = E::unpack2(w[e]);
+                    __half2 v = __floats2half2_rn(f.x * up, f.y * up);  // exact down to 2^-17 of the largest
 #pragma unroll
                     for (int i = 0; i < QP; ++i) {
-                        uint32_t piece[kEach / 2];
-#pragma unroll
-                        for (int e = 0; e < kEach / 2; ++e) {
-                            piece[e] = to_e4m3x2(v[e]);
-                            v[e] = left_of(v[e], piece[e]);
-                        }
-                        unsigned char *at = dst + swizzled<HD>(row0 + i * NT, lane * kEach >> 4) + (lane * kEach & 15);
-                        if constexpr (kEach == 4)
-                            *reinterpret_cast<uint32_t *>(at) = piece[0] | piece[1] << 16;
-                        else
-                            *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(piece[0]);
+                        const uint32_t a = to_e4m3x2(v);
+                        if (i + 1 < QP) v = left_of(v, a);
+                        piece[i][e >> 1] = e & 1 ? piece[i][e >> 1] | a << 16 : a;
                     }
-                    if (lane == 0) qs[r] = down;
+                }
+                if (r < rows) {
+                    const int row0 = r / NT * QP * NT + r % NT;
+#pragma unroll
+                    for (int i = 0; i < QP; ++i)
+                        *reinterpret_cast<uint4 *>(dst + swizzled<HD>(row0 + i * NT, c16)) =
+                            make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+                    if (c16 == 0) qs[r] = down;
                 }
             }
             // columns without a query row: their scores count for nothing, whatever the pieces there hold
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             return true;
         };
         const bool ok = walk_share(p, *share, [&](const SegInfo &it) {
-            if (!warp_wait(bar(Lay::B_IEMPTY + (published & 3)), ((published >> 2) & 1) ^ 1, abort_flag)) return false;
+            if (!wait_for(bar(Lay::B_IEMPTY + (published & 3)), ((published >> 2) & 1) ^ 1, abort_flag)) return false;
             if (lane == 0) {
                 items[published & 3] = it;
                 mbar_arrive(bar(Lay::B_IFULL + (published & 3)));
@@ -286,26 +286,56 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         }
         const int R = p.box_rows, nbox = BN / R;
         constexpr int kRowsLane = kGather ? BN / 32 : 1;
+        // The table entries of the boxes (rows) that this lane loads of a key tile: fetched a tile ahead, looked at when
+        // the tile is loaded.
+        struct Entries {
+            int id[kRowsLane];
+            bool needed[kRowsLane];
+        };
         struct Rows {
-            long long r[kRowsLane];
+            int r[kRowsLane], id[kRowsLane];  // pool rows, -1: not read; their blocks
             int g;
         };
-        auto rows_of = [&](const SegInfo &it, int j, int seg_no) {
+        const int box = 4 * lane / R, in_box = 4 * lane - box * R;  // of the four keys whose scales this lane copies
+        auto pos_of = [&](int j, int i) { return j * BN + (kGather ? lane + 32 * i : lane * R); };
+        auto fetch = [&](const SegInfo &it, int j) {
+            Entries e;
+            const int32_t *table = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks;
+#pragma unroll
+            for (int i = 0; i < kRowsLane; ++i) {
+                const int pos = pos_of(j, i);
+                e.needed[i] = (kGather || lane < nbox) && pos < it.n_end && pos + (kGather ? 0 : R - 1) >= it.n_lo;
+                e.id[i] = e.needed[i] ? ld_index(table + p.geom.block_of(pos)) : 0;
+            }
+            return e;
+        };
+        auto rows_of = [&](const SegInfo &it, int j, const Entries &e, int seg_no) {
             Rows w;
             w.g = it.g;
 #pragma unroll
             for (int i = 0; i < kRowsLane; ++i) {
-                const int pos = j * BN + (kGather ? lane + 32 * i : lane * R);
-                w.r[i] = kGather || lane < nbox ? pool_row(p, it, pos, kGather ? pos : pos + R - 1, bad_seg, seg_no) : -1;
+                w.id[i] = e.id[i];
+                w.r[i] = e.needed[i] ? e.id[i] * p.geom.block_size + p.geom.offset_of(pos_of(j, i)) : -1;
+                if (e.needed[i] && static_cast<unsigned>(e.id[i]) >= static_cast<unsigned>(p.num_blocks)) {
+                    w.r[i] = -1;
+                    bad_seg[seg_no & (kBadRing - 1)] = seg_no + 1;
+                    raise_err(p.err, PA_DEVERR_TABLE);
+                }
             }
             return w;
         };
-        // where pool row r's scale lies
-        auto scale_at = [&](long long r, int g) {
-            const int row = static_cast<int>(r), block = p.geom.block_of(row);
-            return (static_cast<size_t>(block) * p.Hkv + g) * p.geom.block_size + p.geom.offset_of(row);
+        // where the scale of pool row r of a block lies
+        auto scale_at = [&](int r, int id, int g) {
+            return r + (static_cast<long long>(id) * (p.Hkv - 1) + g) * p.geom.block_size;
         };
-        uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};  // tiles loaded, by stream
+        // where the next tile goes in a stream's ring: slot, and times round before
+        struct At {
+            uint32_t slot, lap;
+        };
+        At ak[2] = {}, av[2] = {};
+        auto advance = [&](At &x) {
+            if (++x.slot == static_cast<uint32_t>(Lay::kD)) x.slot = 0, ++x.lap;
+        };
         // gathered tiles are announced one load late, when their copies have landed
         uint32_t owed = 0;  // the barrier of the tile whose copies are in flight
         auto announce = [&](uint32_t b) {
@@ -324,17 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 announce(0);
             }
         };
-        auto load = [&](const Rows &w, bool is_v, auto stream) -> bool {
-            constexpr int h = decltype(stream)::value;
-            const uint32_t i = is_v ? nv[h]++ : nk[h]++;
-            const int slot = h * Lay::kD + static_cast<int>(i % Lay::kD);
-            const uint32_t full = bar((is_v ? Lay::B_VFULL : Lay::B_KFULL) + slot);
+        // One tile of K with its scales, or of V, into its slot once that is free.
+        auto load = [&](const Rows &w, auto v, int h, At &at) -> bool {
+            constexpr bool is_v = decltype(v)::value;
+            const uint32_t slot = h * Lay::kD + at.slot, par = (at.lap & 1) ^ 1;
+            const uint32_t full = bar((is_v ? Lay::B_VFULL : Lay::B_KFULL)) + 8 * slot, empty = bar(is_v ? Lay::B_VEMPTY : Lay::B_KEMPTY) + 8 * slot;
             const uint32_t dst = sbase + (is_v ? Lay::OFF_V : Lay::OFF_K) + slot * Lay::kKV;
             const uint32_t sc = sbase + Lay::OFF_SCALE + slot * 2 * BN * 4;
-            const uint32_t empty = bar((is_v ? Lay::B_VEMPTY : Lay::B_KEMPTY) + slot), par = ((i / Lay::kD) & 1) ^ 1;
             // a gathered tile is not held back while this one waits for its slot
             if (kGather && !__all_sync(kFull, mbar_try_wait(empty, par))) flush();
-            if (!warp_wait(empty, par, abort_flag)) return false;
+            if (!wait_for(empty, par, abort_flag)) return false;
             if constexpr (kGather) {
                 const unsigned char *pool = static_cast<const unsigned char *>(is_v ? p.v_cache : p.k_cache);
 #pragma unroll
@@ -345,80 +374,92 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
 #pragma unroll
                     for (int c = 0; c < HD / 16; ++c) cp_async16(dst + swizzled<HD>(k, c), src + c * 16, there ? 16 : 0);
                     if (!is_v && there) {
-                        const size_t at = scale_at(w.r[e], w.g);
-                        cp_async4(sc + k * 4, p.k_scale + at);
-                        cp_async4(sc + (BN + k) * 4, p.v_scale + at);
+                        const long long from = scale_at(w.r[e], w.id[e], w.g);
+                        cp_async4(sc + k * 4, p.k_scale + from);
+                        cp_async4(sc + (BN + k) * 4, p.v_scale + from);
                     }
                 }
                 cp_async_commit();
                 cp_async_wait<1>();
                 announce(full);
             } else {
-                const uint32_t bytes = static_cast<uint32_t>(R) * (is_v ? HD : HD + 8);
                 const uint32_t boxes = __popc(__ballot_sync(kFull, w.r[0] >= 0));
-                if (lane == 0) mbar_arrive_expect_tx(full, boxes * bytes);
+                if (lane == 0) mbar_arrive_expect_tx(full, boxes * static_cast<uint32_t>(R) * HD);
                 __syncwarp();
-                if (w.r[0] >= 0) {
-                    tma_load_3d(dst + lane * R * HD, is_v ? &p.tm_v : &p.tm_k, 0, w.g, static_cast<int>(w.r[0]), full);
-                    if (!is_v) {
-                        const size_t at = scale_at(w.r[0], w.g);
-                        bulk_load(sc + lane * R * 4, p.k_scale + at, R * 4, full);
-                        bulk_load(sc + (BN + lane * R) * 4, p.v_scale + at, R * 4, full);
+                if (w.r[0] >= 0) tma_load_3d(dst + lane * R * HD, is_v ? &p.tm_v : &p.tm_k, 0, w.g, w.r[0], full);
+                if constexpr (!is_v) {
+                    // the scales of four keys a lane, of the box that holds them; the barrier counts every lane's copies
+                    const int row = __shfl_sync(kFull, w.r[0], box), id = __shfl_sync(kFull, w.id[0], box);
+                    if (row >= 0) {
+                        const long long from = scale_at(row, id, w.g) + in_box;
+                        cp_async16(sc + lane * 16, p.k_scale + from, 16);
+                        cp_async16(sc + BN * 4 + lane * 16, p.v_scale + from, 16);
                     }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
                 }
             }
+            advance(at);
             return true;
         };
-        int n = 0;  // segments taken
-        bool ok = true;
         SegInfo cur{};
-        Rows pend[2]{}, next{};
+        Rows pend[2]{};                // the last tile of each stream whose V is still to come
         bool has[2] = {false, false};
-        // The last tile of each stream whose V is still to come: loaded after the stream's next K, and
+        // The V of a stream's tile is loaded after the stream's next K, and
         // those of the segment before as soon as a segment's first K is under way. An issuer takes the first
         // K of a segment only when the V of the segment before has been used, and a K slot is free when the softmax has read
         // the scales in it, at the start of the tile: no load waits for a tile whose predecessors' Vs are outstanding.
-        using A = std::integral_constant<int, 0>;
-        using B = std::integral_constant<int, 1>;
-        auto pending = [&](auto stream) -> bool {
-            constexpr int h = decltype(stream)::value;
-            const bool r = !has[h] || load(pend[h], true, stream);
-            has[h] = false;
-            return r;
-        };
-        while (ok) {
-            if (!(ok = read_seg(n, cur)) || cur.j0 == cur.j1) break;
+        bool ok = read_seg(0, cur);
+        Entries next{};
+        if (ok && cur.j0 < cur.j1) next = fetch(cur, cur.j0);
+        for (int n = 0; ok && cur.j0 < cur.j1; ++n) {
             flush();
-            next = rows_of(cur, cur.j0, n);
-            auto tile = [&](int j, auto stream) -> bool {
+            SegInfo after{};
+            const auto late = [&](auto stream) {  // the V that a stream owes
                 constexpr int h = decltype(stream)::value;
-                const Rows w = next;
-                if (j + 1 < cur.j1) next = rows_of(cur, j + 1, n);  // in flight while this tile is loaded
-                if (!load(w, false, stream) || !pending(stream) || (j == cur.j0 && !pending(B{}))) return false;
-                pend[h] = w;
+                if (!has[h]) return true;
+                has[h] = false;
+                return load(pend[h], std::true_type{}, h, av[h]);
+            };
+            const auto tile = [&](int j, auto stream) {
+                constexpr int h = decltype(stream)::value;
+                const Rows mine = rows_of(cur, j, next, n);
+                if (j + 1 < cur.j1) {  // in flight while this tile is loaded
+                    next = fetch(cur, j + 1);
+                } else {
+                    if (!read_seg(n + 1, after)) return false;
+                    if (after.j0 < after.j1) next = fetch(after, after.j0);
+                }
+                if (!load(mine, std::false_type{}, h, ak[h]) || !late(stream)) return false;
+                pend[h] = mine;
                 has[h] = true;
                 return true;
             };
-            for (int j = cur.j0; ok && j < cur.j1; j += kStep)
-                ok = tile(j, A{}) && (kCols || j + 1 == cur.j1 || tile(j + 1, B{}));
-            ++n;
+            using A = std::integral_constant<int, 0>;
+            using B = std::integral_constant<int, kCols ? 0 : 1>;
+            for (int j = cur.j0; ok && j < cur.j1; j += kStep) {
+                ok = tile(j, A{});
+                if (!kCols && ok && j == cur.j0) ok = late(B{});
+                if (!kCols && ok && j + 1 < cur.j1) ok = tile(j + 1, B{});
+            }
+            cur = after;
         }
-        ok = ok && pending(A{}) && pending(B{});
+#pragma unroll
+        for (int h = 0; h < (kCols ? 1 : 2); ++h)
+            if (ok && has[h]) ok = load(pend[h], std::true_type{}, h, av[h]);
         flush();
         if (!ok && lane == 0) give_up(p.err, abort_flag);
-        // no copy may still be in flight at exit: the last load of every slot
+        // no copy may still be in flight at exit: the last load of every slot, of this lap or the one before
         if (lane == 0 && !kGather) {
 #pragma unroll
             for (int h = 0; h < (kCols ? 1 : 2); ++h)
 #pragma unroll
-                for (uint32_t back = 1; back <= Lay::kD; ++back) {
-                    if (nk[h] >= back) {
-                        const uint32_t i = nk[h] - back;
-                        if (!mbar_wait(bar(Lay::B_KFULL + h * Lay::kD + i % Lay::kD), (i / Lay::kD) & 1)) give_up(p.err, abort_flag);
-                    }
-                    if (nv[h] >= back) {
-                        const uint32_t i = nv[h] - back;
-                        if (!mbar_wait(bar(Lay::B_VFULL + h * Lay::kD + i % Lay::kD), (i / Lay::kD) & 1)) give_up(p.err, abort_flag);
+                for (int v = 0; v < 2; ++v) {
+                    const At x = v ? av[h] : ak[h];
+#pragma unroll 1
+                    for (uint32_t i = 0; i < static_cast<uint32_t>(Lay::kD); ++i) {
+                        const uint32_t loads = x.lap + (i < x.slot);
+                        if (loads > 0 && !mbar_wait(bar((v ? Lay::B_VFULL : Lay::B_KFULL) + h * Lay::kD) + 8 * i, (loads - 1) & 1))
+                            give_up(p.err, abort_flag);
                     }
                 }
         }
@@ -451,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         // QK of the stream's next tile once S has been read; `last`: of the segment
         auto issue_qk = [&](int n, bool last) -> bool {
             const int slot = static_cast<int>(t % Lay::kD);
-            if (t > 0 && !warp_wait(bar(Lay::B_F + h), (t - 1) & 1, abort_flag)) return false;
-            if (!warp_wait(bar(Lay::B_KFULL + ring + slot), (t / Lay::kD) & 1, abort_flag)) return false;
+            if (t > 0 && !wait_for(bar(Lay::B_F + h), (t - 1) & 1, abort_flag)) return false;
+            if (!wait_for(bar(Lay::B_KFULL + ring + slot), (t / Lay::kD) & 1, abort_flag)) return false;
             tc_fence_after();
             if (lane == 0) {
                 qk(slot, n & 1);
@@ -468,17 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         for (int n = 0; ok; ++n) {
             if (!(ok = read_seg(n, it)) || it.j0 == it.j1) break;
             const int cnt = it.j1 - it.j0;
-            if (!(ok = warp_wait(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, abort_flag))) break;
+            if (!(ok = wait_for(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, abort_flag))) break;
             if (first >= cnt) {  // a segment of one tile has none for stream B
                 if (lane == 0) mbar_arrive(bar(Lay::B_QEMPTY + (n & 1)));
                 __syncwarp();
                 continue;
             }
-            if (!(ok = issue_qk(n, first + kStep >= cnt))) break;
-            for (int i = first; i < cnt; i += kStep, ++done) {
+#pragma unroll 1
+            for (int i = first - kStep; i < cnt; i += kStep) {  // the next tile's QK, then this one's PV
                 if (i + kStep < cnt && !(ok = issue_qk(n, i + 2 * kStep >= cnt))) break;
+                if (i < first) continue;
                 const int slot = static_cast<int>(done % Lay::kD);
-                if (!(ok = warp_wait(bar(Lay::B_VFULL + ring + slot), (done / Lay::kD) & 1, abort_flag))) break;
+                if (!(ok = wait_for(bar(Lay::B_VFULL + ring + slot), (done / Lay::kD) & 1, abort_flag))) break;
                 const int n0 = (it.j0 + i) * BN, z0 = max(it.n_lo - n0, 0), z1 = min(it.n_end - n0, BN);
                 // rows outside [z0, z1) are zeroed: their weights are zero, but 0 * NaN is not
                 // (streams that share the tile both write the zeros)
@@ -489,10 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (!(ok = warp_wait(bar(Lay::B_P + h), done & 1, abort_flag))) break;
+                if (!(ok = wait_for(bar(Lay::B_P + h), done & 1, abort_flag))) break;
                 // the previous segment's output must be out of TMEM before its O is overwritten. (B may have
                 // had no tile in it; its softmax warps have then passed the end of that segment with A's.)
-                if (i == first && n > 0 && !(ok = warp_wait(bar(Lay::B_OFREE + (kCols ? h : 0)), (n - 1) & 1, abort_flag)))
+                if (i == first && n > 0 && !(ok = wait_for(bar(Lay::B_OFREE + (kCols ? h : 0)), (n - 1) & 1, abort_flag)))
                     break;
                 tc_fence_after();
                 if (lane == 0) {
@@ -501,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                     tc_commit(bar(Lay::B_VEMPTY + ring + slot));
                 }
                 __syncwarp();
+                ++done;
             }
         }
         if (!ok && lane == 0) give_up(p.err, abort_flag);
@@ -532,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             if (__any_sync(kFull, vote) && lane == 0) votes[syncs & 1] = syncs + 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(Lay::B_WG + h));
-            const bool r = warp_wait(bar(Lay::B_WG + h), syncs & 1, abort_flag);
+            const bool r = wait_for(bar(Lay::B_WG + h), syncs & 1, abort_flag);
             any = votes[syncs & 1] == syncs + 1;
             ++syncs;
             return r;
@@ -546,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             // columns without a query row have a reference that leaves them no weight
             if (wt < NT) mx[wt] = col0 + wt < rows ? kUnset : INFINITY;
             if (!(ok = meet(false, any))) break;
-            if (!(ok = warp_wait(bar(Lay::B_QS + (n & 3)), (n >> 2) & 1, abort_flag))) break;  // the queries' scales
+            if (!(ok = wait_for(bar(Lay::B_QS + (n & 3)), (n >> 2) & 1, abort_flag))) break;  // the queries' scales
             float l[NT];
 #pragma unroll
             for (int c = 0; c < NT; ++c) l[c] = 0.f;
@@ -554,17 +597,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             for (int i = first; i < cnt; i += kStep, ++t) {
                 const int key = (it.j0 + i) * BN + wt, n0 = (it.j0 + i) * BN;
                 const int slot = ring + static_cast<int>(t % Lay::kD);
-                if (!(ok = warp_wait(bar(Lay::B_KFULL + slot), (t / Lay::kD) & 1, abort_flag))) break;
+                if (!(ok = wait_for(bar(Lay::B_KFULL + slot), (t / Lay::kD) & 1, abort_flag))) break;
                 const float *sc = reinterpret_cast<const float *>(smem + Lay::OFF_SCALE + slot * 2 * BN * 4);
                 float ks = sc[wt], vs = sc[BN + wt];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(Lay::B_KEMPTY + slot));  // the scales have been read
                 if (key < it.n_lo || key >= it.n_end) ks = vs = 1.f;    // no row sees it: whatever lies there
                 const float lv = __log2f(vs), inv_vs = __frcp_rn(vs);
-                if (!(ok = warp_wait(bar(Lay::B_S + h), t & 1, abort_flag))) break;
+                if (!(ok = wait_for(bar(Lay::B_S + h), t & 1, abort_flag))) break;
                 tc_fence_after();
                 // every row sees every key of the tile?
                 const bool masked = n0 + BN > it.p0 + 1 || (p.window > 0 && n0 < last_pos - p.window + 1);
+                // the columns that see the key are [see0, see1): tokens from the key's own on, up to the window's
+                const int since = key - it.p0;  // the first token that sees it
+                const int see0 = min(max(since, 0), Lay::kNC) * p.G - col0;
+                const int until = p.window > 0 && since < Lay::kNC - p.window ? max(since + p.window, 0) : Lay::kNC;
+                const int see1 = max(until * p.G - col0, see0);
                 float x[NT];
                 auto read_s = [&]() {  // x = log2 of the weight before the reference
 #pragma unroll
@@ -589,13 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                         }
                     }
                     if (masked) {
-                        const int tok_c = p.div_g(col0);
-                        int pos = it.p0 + tok_c, in_tok = col0 - tok_c * p.G;
 #pragma unroll
-                        for (int c = 0; c < NT; ++c) {
-                            if (key > pos || (p.window > 0 && key <= pos - p.window)) x[c] = -INFINITY;
-                            if (++in_tok == p.G) in_tok = 0, ++pos;
-                        }
+                        for (int c = 0; c < NT; ++c)
+                            if (static_cast<unsigned>(c - see0) >= static_cast<unsigned>(see1 - see0)) x[c] = -INFINITY;
                     }
                 };
                 auto shift = [&]() {  // less the reference; the largest
@@ -608,19 +652,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                     }
                     return most;
                 };
-                read_s();
-                any = true;  // the segment's first tile sets the references
-                if (i > first) {
-                    // A reference moves when some x exceeds it by more than 8: the sum uses the same
-                    // reference, so the result is exact, and the weights stay at most 2^8.
-                    if (!(ok = meet(shift() > 8.f, any))) break;
-                }
-                if (any) {
-                    if (i > first) read_s();
-                    float v[NT];
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) v[c] = x[c];
-                    const float top = fold(v, [](float a, float b) { return fmaxf(a, b); });
+                // A reference moves when some x exceeds it by more than 8: the sum uses the same
+                // reference, so the result is exact, and the weights stay at most 2^8. The segment's first tile sets the
+                // references. (Where they move the scores are read once more, by the same code.)
+                any = i == first;
+#pragma unroll 1
+                for (bool set = false;;) {
+                    read_s();
+                    if (!any) {
+                        const float most = shift();
+                        if (set || !(ok = meet(most > 8.f, any)) || !any) break;
+                        continue;
+                    }
+                    const float top = fold(x, [](float a, float b) { return fmaxf(a, b); });
                     if (lane < NT) red[quarter * NT + lane] = top;
                     if (!(ok = meet(false, any))) break;
                     if (wt < NT) {
@@ -637,9 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                         l[c] *= f4.x, l[c + 1] *= f4.y, l[c + 2] *= f4.z, l[c + 3] *= f4.w;
                     }
                     if (i > first) {
-                        if (!(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+                        if (!(ok = wait_for(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < Lay::kO; c += 16) {
                             uint32_t ov[16];
                             tmem_ld<16>(o_row + c, ov);
@@ -650,13 +694,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                         }
                         tmem_wait_st();
                     }
-                    shift();
+                    any = false;
+                    set = true;
                 }
+                if (!ok) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(Lay::B_F + h));  // S has been read
                 // the stream's previous PV has read W
-                if (t > 0 && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+                if (t > 0 && !(ok = wait_for(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
 #pragma unroll
                 for (int q = 0; q < NT / 16; ++q) {
                     uint32_t piece[Lay::PP][4];
@@ -695,13 +741,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             const int cnt_b = kCols ? 0 : cnt / 2;  // tiles of the other stream's accumulator to be joined with A's
             // this stream's products are complete; then, where the streams halve the keys, both streams', with
             // their references and sums
-            if (cnt > first && !(ok = warp_wait(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+            if (cnt > first && !(ok = wait_for(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
             if constexpr (kCols) {
                 if (!(ok = meet(false, any))) break;
             } else {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(Lay::B_BOTH));
-                if (!(ok = warp_wait(bar(Lay::B_BOTH), n & 1, abort_flag))) break;
+                if (!(ok = wait_for(bar(Lay::B_BOTH), n & 1, abort_flag))) break;
             }
             tc_fence_after();
             // this stream writes the query rows [c_lo, c_lo + kMine): its own, or half of the streams' common ones
