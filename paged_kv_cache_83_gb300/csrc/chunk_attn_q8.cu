@@ -51,25 +51,26 @@ struct LayQ8 {
     static constexpr int kNC = kCols ? 2 * NT : NT;         // query rows
     static constexpr int PP = QP;                           // pieces of a weight
     static constexpr int kKV = BN * HD;                     // bytes of a tile
-    static constexpr int kAtom = 8 * HD;                    // eight rows: the swizzle's period
     static constexpr int kQ = kNC * QP * HD;
     static constexpr int kP = BN * 128;                     // W^T: a 128-byte row a key, PP * NT of it used
-    static constexpr int kSlots = HD == 128 ? 4 : 8;        // K tiles held, and V tiles
-    static constexpr int kD = kCols ? kSlots : kSlots / 2;  // of a ring
+    static constexpr int kTiles = HD == 128 ? 4 : 8;        // V tiles held; of K half as many more where there is room
+    static constexpr bool kMoreK = !kCols && (NT == 16 || QP == 2);
+    static constexpr int kVSlots = kTiles, kKSlots = kMoreK ? kTiles * 3 / 2 : kTiles;
+    static constexpr int kVD = kCols ? kVSlots : kVSlots / 2, kKD = kCols ? kKSlots : kKSlots / 2;  // of a ring
     static constexpr int kQf = 4;                           // segments whose queries' scales are held
     // barriers; rings, S, F, P, O, WG: + stream
-    static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = B_KFULL + kSlots,
-                         B_VFULL = B_KEMPTY + kSlots, B_VEMPTY = B_VFULL + kSlots, B_S = B_VEMPTY + kSlots, B_F = B_S + 2,
+    static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = B_KFULL + kKSlots,
+                         B_VFULL = B_KEMPTY + kKSlots, B_VEMPTY = B_VFULL + kVSlots, B_S = B_VEMPTY + kVSlots, B_F = B_S + 2,
                          B_P = B_F + 2, B_WG = B_P + 2, B_O = B_WG + 2, B_OFREE = B_O + 2, B_BOTH = B_OFREE + 2,
                          B_END = B_BOTH + 1, B_QS = B_END + 2, B_IFULL = B_QS + kQf, B_IEMPTY = B_IFULL + 4, NBAR = B_IEMPTY + 4;
     // shared memory: V's rings before K's (at head dim 64 the V operand's unused upper half of rows reads
     // one tile further)
-    static constexpr int OFF_V = 0, OFF_K = kSlots * kKV, OFF_Q = OFF_K + kSlots * kKV, OFF_P = OFF_Q + 2 * kQ,
+    static constexpr int OFF_V = 0, OFF_K = kVSlots * kKV, OFF_Q = OFF_K + kKSlots * kKV, OFF_P = OFF_Q + 2 * kQ,
                          OFF_SCALE = OFF_P + 2 * kP;        // per K slot: the tile's scales of K, then of V
-    static constexpr int OFF_F = OFF_SCALE + kSlots * 2 * BN * 4;  // floats below
+    static constexpr int OFF_F = OFF_SCALE + kKSlots * 2 * BN * 4;  // floats below
     // per segment parity and stream: references [NT], sums by warp [4][NT], weights [NT]; scratch; the queries' scales
     static constexpr int kMax = 0, kSum = 2 * 2 * NT, kWgt = kSum + 2 * 2 * 4 * NT, kRed = kWgt + 2 * 2 * NT,
-                         kFac = kRed + 2 * 4 * NT, kQs = kFac + 2 * NT, kFloats = kQs + kQf * kNC;
+                         kFac = kRed + 2 * 4 * NT, kQs = kFac + 2 * NT, kZero = kQs + kQf * kNC, kFloats = kZero + NT;
     static constexpr int OFF_BAR = OFF_F + kFloats * 4 + 16;  // after the votes
     static constexpr int OFF_ITEMS = OFF_BAR + NBAR * 8;
     static constexpr int OFF_BAD = OFF_ITEMS + 4 * static_cast<int>(sizeof(SegInfo));
@@ -133,6 +134,17 @@ __device__ __forceinline__ __half2 left_of(__half2 v, uint32_t piece) {
     return __hfma2(from_e4m3x2(piece), __hneg2(k), __hmul2(v, k));
 }
 
+__device__ __forceinline__ float max_of(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float warp_most(float v) {  // the largest over the warp, in every lane
+    float d;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    return d;
+}
+
 template <class E, int HD, int NT, bool kCols, bool kGather>
 __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_constant__ Q8Params p) {
     using T = typename E::T;
@@ -171,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         for (int i = 0; i < kBadRing; ++i) bad_seg[i] = 0;
         for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(fl + Lay::kFloats)[i] = 0;  // votes
     }
+    if (tid < NT) fl[Lay::kZero + tid] = 0.f;
     // Launched beside what precedes it in the stream: nothing that it wrote is read, and nothing that it reads is
     // written, before it has finished (the set-up above takes place meanwhile).
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -333,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             uint32_t slot, lap;
         };
         At ak[2] = {}, av[2] = {};
-        auto advance = [&](At &x) {
-            if (++x.slot == static_cast<uint32_t>(Lay::kD)) x.slot = 0, ++x.lap;
+        auto advance = [&](At &x, int slots) {
+            if (++x.slot == static_cast<uint32_t>(slots)) x.slot = 0, ++x.lap;
         };
         // gathered tiles are announced one load late, when their copies have landed
         uint32_t owed = 0;  // the barrier of the tile whose copies are in flight
@@ -357,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         // One tile of K with its scales, or of V, into its slot once that is free.
         auto load = [&](const Rows &w, auto v, int h, At &at) -> bool {
             constexpr bool is_v = decltype(v)::value;
-            const uint32_t slot = h * Lay::kD + at.slot, par = (at.lap & 1) ^ 1;
+            constexpr int kD = is_v ? Lay::kVD : Lay::kKD;
+            const uint32_t slot = h * kD + at.slot, par = (at.lap & 1) ^ 1;
             const uint32_t full = bar((is_v ? Lay::B_VFULL : Lay::B_KFULL)) + 8 * slot, empty = bar(is_v ? Lay::B_VEMPTY : Lay::B_KEMPTY) + 8 * slot;
             const uint32_t dst = sbase + (is_v ? Lay::OFF_V : Lay::OFF_K) + slot * Lay::kKV;
             const uint32_t sc = sbase + Lay::OFF_SCALE + slot * 2 * BN * 4;
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
                 }
             }
-            advance(at);
+            advance(at, kD);
             return true;
         };
         SegInfo cur{};
@@ -455,10 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     const At x = v ? av[h] : ak[h];
+                    const int slots = v ? Lay::kVD : Lay::kKD;
 #pragma unroll 1
-                    for (uint32_t i = 0; i < static_cast<uint32_t>(Lay::kD); ++i) {
-                        const uint32_t loads = x.lap + (i < x.slot);
-                        if (loads > 0 && !mbar_wait(bar((v ? Lay::B_VFULL : Lay::B_KFULL) + h * Lay::kD) + 8 * i, (loads - 1) & 1))
+                    for (int i = 0; i < slots; ++i) {
+                        const uint32_t loads = x.lap + (i < static_cast<int>(x.slot));
+                        if (loads > 0 && !mbar_wait(bar((v ? Lay::B_VFULL : Lay::B_KFULL) + h * slots + i), (loads - 1) & 1))
                             give_up(p.err, abort_flag);
                     }
                 }
@@ -469,10 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         const int h = warp - 1;
         constexpr uint32_t IQK = idesc_e4m3(BM, Lay::kS, false);             // A = K rows, B = Q pieces, both K-major
         constexpr uint32_t IPV = idesc_a_mn(idesc_e4m3(BM, Lay::kO, true));  // A = V^T, B = W^T pieces, both MN-major
-        const int ring = kCols ? 0 : h * Lay::kD, first = kCols ? 0 : h;     // the stream's first slot, and key tile
+        const int k_ring = kCols ? 0 : h * Lay::kKD, v_ring = kCols ? 0 : h * Lay::kVD;  // the stream's first slots
+        const int first = kCols ? 0 : h;                                      // and key tile
         const uint64_t dq0 = desc_rows<HD>(sbase + Lay::OFF_Q + (kCols ? h * Lay::kS * HD : 0), 16);
-        const uint64_t dk0 = desc_rows<HD>(sbase + Lay::OFF_K + ring * Lay::kKV, 16);
-        const uint64_t dv0 = desc_rows<HD>(sbase + Lay::OFF_V + ring * Lay::kKV, Lay::kKV);
+        const uint64_t dk0 = desc_rows<HD>(sbase + Lay::OFF_K + k_ring * Lay::kKV, 16);
+        const uint64_t dv0 = desc_rows<HD>(sbase + Lay::OFF_V + v_ring * Lay::kKV, Lay::kKV);
         const uint64_t dp = smem_desc_sw128(sbase + Lay::OFF_P + h * Lay::kP, 16, 1024);
         const uint32_t s_tm = tmem + h * Lay::kS, o_tm = tmem + 2 * Lay::kS + h * Lay::kO;
         auto qk = [&](int slot, int q) {  // S^T = K Q^T, 32 elements an instruction
@@ -491,14 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         SegInfo it{};
         // QK of the stream's next tile once S has been read; `last`: of the segment
         auto issue_qk = [&](int n, bool last) -> bool {
-            const int slot = static_cast<int>(t % Lay::kD);
+            const int slot = static_cast<int>(t % Lay::kKD);
             if (t > 0 && !wait_for(bar(Lay::B_F + h), (t - 1) & 1, abort_flag)) return false;
-            if (!wait_for(bar(Lay::B_KFULL + ring + slot), (t / Lay::kD) & 1, abort_flag)) return false;
+            if (!wait_for(bar(Lay::B_KFULL + k_ring + slot), (t / Lay::kKD) & 1, abort_flag)) return false;
             tc_fence_after();
             if (lane == 0) {
                 qk(slot, n & 1);
                 tc_commit(bar(Lay::B_S + h));
-                tc_commit(bar(Lay::B_KEMPTY + ring + slot));
+                tc_commit(bar(Lay::B_KEMPTY + k_ring + slot));
                 if (last) tc_commit(bar(Lay::B_QEMPTY + (n & 1)));
             }
             __syncwarp();
@@ -519,13 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             for (int i = first - kStep; i < cnt; i += kStep) {  // the next tile's QK, then this one's PV
                 if (i + kStep < cnt && !(ok = issue_qk(n, i + 2 * kStep >= cnt))) break;
                 if (i < first) continue;
-                const int slot = static_cast<int>(done % Lay::kD);
-                if (!(ok = wait_for(bar(Lay::B_VFULL + ring + slot), (done / Lay::kD) & 1, abort_flag))) break;
+                const int slot = static_cast<int>(done % Lay::kVD);
+                if (!(ok = wait_for(bar(Lay::B_VFULL + v_ring + slot), (done / Lay::kVD) & 1, abort_flag))) break;
                 const int n0 = (it.j0 + i) * BN, z0 = max(it.n_lo - n0, 0), z1 = min(it.n_end - n0, BN);
                 // rows outside [z0, z1) are zeroed: their weights are zero, but 0 * NaN is not
                 // (streams that share the tile both write the zeros)
                 if (z0 > 0 || z1 < BN) {
-                    uint4 *tile = reinterpret_cast<uint4 *>(smem + Lay::OFF_V + (ring + slot) * Lay::kKV);
+                    uint4 *tile = reinterpret_cast<uint4 *>(smem + Lay::OFF_V + (v_ring + slot) * Lay::kKV);
                     for (int x = lane; x < z0 * (HD / 16); x += 32) tile[x] = make_uint4(0, 0, 0, 0);
                     for (int x = z1 * (HD / 16) + lane; x < BN * (HD / 16); x += 32) tile[x] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
@@ -540,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 if (lane == 0) {
                     pv(slot, i > first);
                     tc_commit(bar(Lay::B_O + h));
-                    tc_commit(bar(Lay::B_VEMPTY + ring + slot));
+                    tc_commit(bar(Lay::B_VEMPTY + v_ring + slot));
                 }
                 __syncwarp();
                 ++done;
@@ -559,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t s_row = tmem + lane_off + h * Lay::kS, o_row = tmem + lane_off + 2 * Lay::kS + h * Lay::kO;
         unsigned char *prow = smem + Lay::OFF_P + h * Lay::kP + wt * 128;
-        const int ring = kCols ? 0 : h * Lay::kD;
+        const int ring = kCols ? 0 : h * Lay::kKD;
         const int first = kCols ? 0 : h;         // the stream's first key tile of a segment
         const int col0 = kCols ? h * NT : 0;     // the query row of its first column
         float *red = fl + Lay::kRed + h * 4 * NT, *fac = fl + Lay::kFac + h * NT;
@@ -596,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             const int last_pos = it.p0 + it.tok - 1;
             for (int i = first; i < cnt; i += kStep, ++t) {
                 const int key = (it.j0 + i) * BN + wt, n0 = (it.j0 + i) * BN;
-                const int slot = ring + static_cast<int>(t % Lay::kD);
-                if (!(ok = wait_for(bar(Lay::B_KFULL + slot), (t / Lay::kD) & 1, abort_flag))) break;
+                const int slot = ring + static_cast<int>(t % Lay::kKD);
+                if (!(ok = wait_for(bar(Lay::B_KFULL + slot), (t / Lay::kKD) & 1, abort_flag))) break;
                 const float *sc = reinterpret_cast<const float *>(smem + Lay::OFF_SCALE + slot * 2 * BN * 4);
                 float ks = sc[wt], vs = sc[BN + wt];
                 __syncwarp();
@@ -614,26 +630,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 const int until = p.window > 0 && since < Lay::kNC - p.window ? max(since + p.window, 0) : Lay::kNC;
                 const int see1 = max(until * p.G - col0, see0);
                 float x[NT];
-                auto read_s = [&]() {  // x = log2 of the weight before the reference
+                const uint64_t ks2 = f2_pack(ks, ks), lv2 = f2_pack(lv, lv);
+                // x = log2 of the weights, less `less` (the references, or 0); the largest
+                auto read_s = [&](const float *less) {
 #pragma unroll
                     for (int c = 0; c < NT; c += 16) {
                         uint32_t s0[16], s1[16];
                         tmem_ld<16>(s_row + c, s0);
                         tmem_ld<16>(s_row + NT + c, s1);
                         tmem_wait_ld();
+                        uint64_t y[8];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) x[c + e] = fmaf(__uint_as_float(s1[e]), 0x1p-5f, __uint_as_float(s0[e]));
+                        for (int e = 0; e < 8; ++e)
+                            y[e] = f2_fma(u2_pack(s1[2 * e], s1[2 * e + 1]), f2_pack(0x1p-5f, 0x1p-5f), u2_pack(s0[2 * e], s0[2 * e + 1]));
                         if constexpr (QP == 3) {
                             tmem_ld<16>(s_row + 2 * NT + c, s0);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) x[c + e] = fmaf(__uint_as_float(s0[e]), 0x1p-10f, x[c + e]);
+                            for (int e = 0; e < 8; ++e)
+                                y[e] = f2_fma(u2_pack(s0[2 * e], s0[2 * e + 1]), f2_pack(0x1p-10f, 0x1p-10f), y[e]);
                         }
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
-                            const float4 f4 = *reinterpret_cast<const float4 *>(qs + c + e);
-                            x[c + e] = fmaf(x[c + e] * f4.x, ks, lv), x[c + e + 1] = fmaf(x[c + e + 1] * f4.y, ks, lv);
-                            x[c + e + 2] = fmaf(x[c + e + 2] * f4.z, ks, lv), x[c + e + 3] = fmaf(x[c + e + 3] * f4.w, ks, lv);
+                            const float4 f4 = *reinterpret_cast<const float4 *>(qs + c + e), m4 = *reinterpret_cast<const float4 *>(less + c + e);
+                            const uint64_t a = f2_fma(f2_mul(y[e >> 1], f2_pack(f4.x, f4.y)), ks2, lv2),
+                                           b = f2_fma(f2_mul(y[(e >> 1) + 1], f2_pack(f4.z, f4.w)), ks2, lv2);
+                            x[c + e] = f2_lo(a) - m4.x, x[c + e + 1] = f2_hi(a) - m4.y;
+                            x[c + e + 2] = f2_lo(b) - m4.z, x[c + e + 3] = f2_hi(b) - m4.w;
                         }
                     }
                     if (masked) {
@@ -641,15 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                         for (int c = 0; c < NT; ++c)
                             if (static_cast<unsigned>(c - see0) >= static_cast<unsigned>(see1 - see0)) x[c] = -INFINITY;
                     }
-                };
-                auto shift = [&]() {  // less the reference; the largest
                     float most = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < NT; c += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4 *>(mx + c);
-                        x[c] -= m4.x, x[c + 1] -= m4.y, x[c + 2] -= m4.z, x[c + 3] -= m4.w;
-                        most = fmaxf(most, fmaxf(fmaxf(x[c], x[c + 1]), fmaxf(x[c + 2], x[c + 3])));
-                    }
+                    for (int c = 0; c < NT; c += 2) most = max_of(most, x[c], x[c + 1]);
                     return most;
                 };
                 // A reference moves when some x exceeds it by more than 8: the sum uses the same
@@ -658,14 +675,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 any = i == first;
 #pragma unroll 1
                 for (bool set = false;;) {
-                    read_s();
+                    const float most = read_s(any ? fl + Lay::kZero : mx);
                     if (!any) {
-                        const float most = shift();
                         if (set || !(ok = meet(most > 8.f, any)) || !any) break;
                         continue;
                     }
-                    const float top = fold(x, [](float a, float b) { return fmaxf(a, b); });
-                    if (lane < NT) red[quarter * NT + lane] = top;
+#pragma unroll
+                    for (int c = 0; c < NT; c += 4) {
+                        const float4 top = make_float4(warp_most(x[c]), warp_most(x[c + 1]), warp_most(x[c + 2]), warp_most(x[c + 3]));
+                        if (lane == 0) *reinterpret_cast<float4 *>(red + quarter * NT + c) = top;
+                    }
                     if (!(ok = meet(false, any))) break;
                     if (wt < NT) {
                         const float most = fmaxf(fmaxf(red[wt], red[NT + wt]), fmaxf(red[2 * NT + wt], red[3 * NT + wt]));
