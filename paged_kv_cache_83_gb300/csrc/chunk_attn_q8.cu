@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "chunk_narrow.cuh"
+#include "chunk_wide.cuh"
 #include "tensor_map.h"
 
 namespace pa {
@@ -888,9 +889,8 @@ cudaError_t launch_typed(const Q8Params &prm, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, chunk_narrow_join_kernel<E, HD, Lay::kNC>, static_cast<const ChunkParams &>(prm));
 }
 
-constexpr int kMostRows = 64;  // query rows of an item
-
-size_t piece_bytes(int D) { return piece_floats(kMostRows, D) * 4; }
+// room for the pieces of every form: two row tiles of chunk_attn_q8_wide.cu are the largest
+size_t piece_bytes(int D) { return wide_piece_floats(D) * 4; }
 
 }  // namespace
 
@@ -911,10 +911,6 @@ cudaError_t launch_chunk_q8(const ChunkQ8Args &x, cudaStream_t stream) {
     // gathered keys are bound by the one warp that copies them, whatever the columns: one form for all
     const int form = gather || rows > 32 ? 64 : rows > 16 ? 32 : 16;
     prm.tt = prm.item_tok = form / prm.G;
-    const long long krows = static_cast<long long>(a.num_blocks) * a.block_size;
-    if (!gather && (!encode_rows_e4m3(&prm.tm_k, a.k_cache, a.Hkv, a.D, krows, R) ||
-                    !encode_rows_e4m3(&prm.tm_v, a.v_cache, a.Hkv, a.D, krows, R)))
-        return cudaErrorInvalidValue;
     prm.cu_q = a.cu_q;
     prm.ctx = a.ctx;
     prm.block_tables = a.block_tables;
@@ -935,6 +931,11 @@ cudaError_t launch_chunk_q8(const ChunkQ8Args &x, cudaStream_t stream) {
     prm.geom.block_size = a.block_size;
     prm.geom.shift = log2_if_pow2(a.block_size);
     prm.scale_log2 = a.scale * kLog2e;
+    if (rows > 64) return launch_chunk_q8_wide(prm, x, stream);
+    const long long krows = static_cast<long long>(a.num_blocks) * a.block_size;
+    if (!gather && (!encode_rows_e4m3(&prm.tm_k, a.k_cache, a.Hkv, a.D, krows, R) ||
+                    !encode_rows_e4m3(&prm.tm_v, a.v_cache, a.Hkv, a.D, krows, R)))
+        return cudaErrorInvalidValue;
     auto go = [&](auto e, auto hd) {
         using E = decltype(e);
         constexpr int HD = decltype(hd)::value;

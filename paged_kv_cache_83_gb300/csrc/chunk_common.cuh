@@ -110,11 +110,12 @@ struct Share {
     int s0;
 };
 
-// Every thread of the block calls this; sm: 12 words of shared memory, the result is in *out after the
+// Every thread of the block (kN of them) calls this; sm: kN / 32 words of shared memory, the result is in *out after the
 // next __syncthreads (in shared memory too: only the scheduler reads it).
+template <int kN = kThreads>
 __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, Share *out) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kW = kThreads / 32;
+    constexpr int kW = kN / 32;
     // the sum over the block so far, and the sum before this thread, of one value a thread
     auto scan = [&](long long v, long long &before) {
         long long incl = v;
@@ -139,10 +140,10 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
     Share r;
     long long v = tiles_of(tid), before;
     r.N = scan(v, before);
-    const long long first = r.N;  // of the first kThreads sequences
-    if (p.S > kThreads) {
+    const long long first = r.N;  // of the first kN sequences
+    if (p.S > kN) {
         long long more = 0, unused;
-        for (int s = tid + kThreads; s < p.S; s += kThreads) more += tiles_of(s);
+        for (int s = tid + kN; s < p.S; s += kN) more += tiles_of(s);
         r.N += scan(more, unused);
     }
     // CTAs 0 .. P - 1 take a share, at least one tile each (no piece of an item is then empty)
@@ -161,7 +162,7 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
     }
     if (r.b0 < r.b1) {
         long long base = 0, total = first;
-        for (int sb = 0;; sb += kThreads) {
+        for (int sb = 0;; sb += kN) {
             if (sb > 0) {
                 v = tiles_of(sb + tid);
                 total = scan(v, before);
@@ -178,7 +179,7 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
 }
 
 // Sequences whose lengths are outside the contract: an error bit and zero rows.
-template <class T, int HD>
+template <class T, int HD, int kN = kThreads>
 __device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p) {
     T *out = static_cast<T *>(p.out);
     for (int s = blockIdx.x; s < p.S; s += gridDim.x) {
@@ -187,7 +188,7 @@ __device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p) {
         if (threadIdx.x == 0) raise_err(p.err, PA_DEVERR_LENGTH);
         const int a = max(q.q0, 0), b = min(ld_index(p.cu_q + s + 1), p.total_q);
         for (long long i = static_cast<long long>(a) * p.Hq * HD + threadIdx.x; i < static_cast<long long>(b) * p.Hq * HD;
-             i += kThreads)
+             i += kN)
             out[i] = T(0.f);
     }
 }
@@ -286,6 +287,8 @@ __device__ __forceinline__ void zero_rows(unsigned char *tile, int z0, int z1) {
 
 }  // namespace chunk
 
+// chunk_attn_q8_wide.cu: over an 8-bit cache, items of two tiles of 128 query rows
+cudaError_t launch_chunk_q8_wide(const chunk::ChunkParams &prm, const ChunkQ8Args &a, cudaStream_t stream);
 // chunk_attn_narrow.cu: items of at most 64 query rows
 cudaError_t launch_chunk_narrow(const chunk::ChunkParams &prm, pa_dtype dtype, int D, bool gather, cudaStream_t stream);
 
