@@ -4,8 +4,8 @@
 // The mathematics is chunk_attn.cu's, with the scales of an 8-bit cache: x_j = ks_j (scale q.K8_j) + log2 vs_j, weights
 // 2^(x_j - m), O = sum 2^(x_j - m) V8_j, and the sum takes 2^(x_j - m) / vs_j.
 //
-// Bound by the softmax warps, as there. So the cache's e4m3 rows are widened to 16 bits, exactly, on their way to
-// shared memory, once for the 256 query rows of an item, and queries (of the storage type) and weights (fp16) stay whole operands (as sums of e4m3 pieces they
+// Bound by the softmax warps, as there. So the cache's e4m3 rows are widened to the storage type, exactly, on their way to
+// shared memory, once for the 256 query rows of an item, and queries and weights stay whole operands (as sums of e4m3 pieces they
 // cost the softmax three conversions a weight; that form of 64 rows an item took 955 us for two chunks of 2k tokens at 12-16k, 16/8
 // heads x 128). Four warps copy the rows ahead, any page size alike, widen them and write the swizzled
 // tile that the matrix instructions read; one buffer for K and one for V suffice, since a tile's K is wanted a
@@ -15,7 +15,7 @@
 //   warp 0        brings the queries of a segment by TMA
 //   warps 1, 2    one MMA issuer per row tile
 //   warps 4-11    softmax, a thread a query row
-//   warps 12-15   loaders: K tiles in the storage type, V tiles in fp16, and the three numbers of a key: scale * ks, log2 vs, 1 / vs
+//   warps 12-15   loaders: K and V tiles, and the three numbers of a key: scale * ks, log2 vs, 1 / vs
 #include <type_traits>
 
 #include "chunk_wide.cuh"
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
 
     // every role reads the segments in the same order: segment n sits in queue entry n % kQueue
     auto read_seg = [&](int n, SegInfo &it) -> bool {
-        if (!warp_wait(bar(W_IFULL + n % kQueue), (n / kQueue) & 1, abort_flag)) return false;
+        if (!short_wait(bar(W_IFULL + n % kQueue), (n / kQueue) & 1, abort_flag)) return false;
         it = items[n % kQueue];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(W_IEMPTY + n % kQueue));
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
             // ================================== scheduler ==================================
             int published = 0;
             const bool ok = walk_share(p, *share, [&](const SegInfo &it) {
-                if (!warp_wait(bar(W_IEMPTY + published % kQueue), ((published / kQueue) & 1) ^ 1, abort_flag)) return false;
+                if (!short_wait(bar(W_IEMPTY + published % kQueue), ((published / kQueue) & 1) ^ 1, abort_flag)) return false;
                 if (lane == 0) {
                     items[published % kQueue] = it;
                     mbar_arrive(bar(W_IFULL + published % kQueue));
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
             for (SegInfo cur{};; ++n) {
                 if (!(ok = read_seg(n, cur)) || cur.j0 == cur.j1) break;
                 // once both issuers are past the previous segment's last QK
-                if (n > 0 && !(ok = warp_wait(bar(W_QEMPTY), (n - 1) & 1, abort_flag))) break;
+                if (n > 0 && !(ok = short_wait(bar(W_QEMPTY), (n - 1) & 1, abort_flag))) break;
                 if (lane == 0) {
                     const int tiles = has_b(cur) ? 2 : 1;
                     const uint32_t half_bytes = static_cast<uint32_t>(p.tt) * p.G * 128;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
             // ============================ MMA issuer of one row tile =============================
             const int h = warp - 1;
             constexpr uint32_t IQK = idesc_f16(BM, BN, E::kIsBf16, false);
-            constexpr uint32_t IPV = idesc_f16(BM, HD, false, true);  // weights and values are fp16 in any case
+            constexpr uint32_t IPV = idesc_f16(BM, HD, E::kIsBf16, true);
             const uint64_t dq = smem_desc_sw128(sbase + (h ? Lay::OFF_QB : Lay::OFF_QA), 16, 1024);
             const uint64_t dp = smem_desc_sw128(sbase + (h ? Lay::OFF_PB : Lay::OFF_PA), 16, 1024);
             const uint64_t dk = smem_desc_sw128(sbase + Lay::OFF_K, 16, 1024);
@@ -230,15 +230,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
             for (int n = 0; ok; ++n) {
                 if (!(ok = read_seg(n, cur)) || cur.j0 == cur.j1) break;
                 const bool rows = h == 0 || has_b(cur);
-                if (!(ok = warp_wait(bar(W_QFULL), n & 1, abort_flag))) break;
+                if (!(ok = short_wait(bar(W_QFULL), n & 1, abort_flag))) break;
 #pragma unroll 1
                 for (int j = cur.j0 - 1; j < cur.j1; ++j) {  // the next tile's QK, then this one's PV
                     if (j + 1 < cur.j1) {
                         // S as soon as the softmax holds the one before in registers. Without rows in this row tile (B of a
                         // short chunk) a tile is only handed back.
                         const uint32_t before = t + (j >= cur.j0);  // S tiles issued
-                        if (rows && before > 0 && !(ok = warp_wait(bar(W_F + h), (before - 1) & 1, abort_flag))) break;
-                        if (!(ok = warp_wait(bar(W_KFULL), k_tiles & 1, abort_flag))) break;
+                        if (rows && before > 0 && !(ok = short_wait(bar(W_F + h), (before - 1) & 1, abort_flag))) break;
+                        if (!(ok = short_wait(bar(W_KFULL), k_tiles & 1, abort_flag))) break;
                         ++k_tiles;
                         tc_fence_after();
                         if (lane == 0) {
@@ -256,11 +256,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                         __syncwarp();
                     }
                     if (j < cur.j0) continue;
-                    if (!(ok = warp_wait(bar(W_VFULL), v_tiles & 1, abort_flag))) break;
+                    if (!(ok = short_wait(bar(W_VFULL), v_tiles & 1, abort_flag))) break;
                     ++v_tiles;
-                    if (rows && !(ok = warp_wait(bar(W_P + h), t & 1, abort_flag))) break;
+                    if (rows && !(ok = short_wait(bar(W_P + h), t & 1, abort_flag))) break;
                     // the previous segment's output must be out of TMEM before its O is overwritten
-                    if (rows && j == cur.j0 && done > 0 && !(ok = warp_wait(bar(W_OFREE + h), (done - 1) & 1, abort_flag))) break;
+                    if (rows && j == cur.j0 && done > 0 && !(ok = short_wait(bar(W_OFREE + h), (done - 1) & 1, abort_flag))) break;
                     tc_fence_after();
                     if (lane == 0) {
                         if (rows) {
@@ -288,149 +288,128 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
         regs_down<kRegsLoad>();
         // A warp has 32 keys of a tile, a lane 16 elements (one 16-byte piece) of every kStepKeys-th of them: kSteps pieces a tile,
         // which it copies to room of its own in shared memory, kUnit pieces (a unit) at a time and kUnits units ahead, and
-        // widens from there itself: nobody else waits for its copies. (Held in registers the loads left too few of them,
-        // and the unrolled code did not stay in the instruction cache: 1001 us for the two chunks.)
-        // Lane l looks up key l's place in the pool and loads its scales.
+        // widens from there itself: nobody else waits for its copies. Lane l looks up key l's place in the pool and loads its
+        // scales. One loop, one copy of the code: with the loads in registers, and with the loop's ends unrolled, it did not stay in
+        // the instruction cache beside the softmax's (1001 and 715 us for the two chunks).
         constexpr int kPieces = HD / 16, kStepKeys = 32 / kPieces, kSteps = 32 / kStepKeys;
         static_assert(kSteps % kUnit == 0);
         const int w = warp - 12, piece = lane % kPieces, key_of_lane = lane / kPieces;
         const uint32_t mine = sbase + Lay::OFF_STAGE + (tid - 384) * 16;  // pieces 2 KB apart
-        bool ok = true;
-        // ---- what is copied next: K of tile 0; K of tile i + 1 and V of tile i in turn; V of the last
+        // chunks 2 * piece and 2 * piece + 1 of a row; lanes of the second 64 columns write theirs in the other
+        // order, so that eight lanes meet eight different groups of banks
+        const int chunk = (2 * piece + (piece >= 4)) & 7;
+        const uint32_t stride = static_cast<uint32_t>(p.Hkv) * HD;
         SegInfo it{};
-        int n = 0, j = 0, id = 0;  // the tile whose K comes next; the table entry of this lane's key in it
+        int n = 0, j = 0, id = 0;  // the tile whose K is copied next; the table entry of this lane's key in it
         auto fetch = [&]() {
             const int pos = j * BN + w * 32 + lane;
             id = 0;
             if (it.j0 < it.j1 && pos >= it.n_lo && pos < it.n_end)
                 id = ld_index(p.block_tables + static_cast<size_t>(it.s) * p.max_blocks + p.geom.block_of(pos));
         };
-        int row = -1, g = 0;           // of the tile that is being copied: this lane's key's row of the pool (-1: zeros), kv head
-        int k_row = -1, k_g = 0;       // of the tile whose K was copied last
-        int v_row = -1, v_g = 0;       // of the tile whose V comes next
-        bool is_v = false, any = false, v_due = false, k_came = false;
-        int step = kSteps;             // of the tile that is being copied
-        float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};  // of this lane's key in the tile whose K was copied last, and the one before
-        uint32_t k_tiles = 0;          // whose copies have begun
-        bool v_next = false;
-        auto next_tile = [&]() {       // what is copied next; none at the end
-            step = 0;
-            any = false;
-            if (v_next) {  // V of the tile before the one whose K came last
-                v_next = false;
-                if (v_due) {
-                    row = v_row, g = v_g, is_v = any = true;
-                    return;
-                }
-            }
-            v_row = k_row, v_g = k_g, v_due = k_came;
-            k_came = ok && it.j0 < it.j1;
-            if (k_came) {
-                const int pos = j * BN + w * 32 + lane;
-                k_row = -1, k_g = it.g;
-                ks[1] = ks[0], vs[1] = vs[0];
-                ks[0] = vs[0] = 1.f;  // where no row sees the key: numbers that do no harm
-                if (pos >= it.n_lo && pos < it.n_end) {
-                    if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks)) {
-                        const int off = p.geom.offset_of(pos);
-                        k_row = id * p.geom.block_size + off;
-                        const size_t at = (static_cast<size_t>(id) * p.Hkv + it.g) * p.geom.block_size + off;
-                        ks[0] = __ldcg(p.k_scale + at);
-                        vs[0] = __ldcg(p.v_scale + at);
-                    } else {
-                        bad_seg[n & (kBadRing - 1)] = n + 1;
-                        raise_err(p.err, PA_DEVERR_TABLE);
-                    }
-                }
-                __syncwarp();
-                row = k_row, g = k_g, is_v = false, any = v_next = true;
-                ++k_tiles;
-                if (++j >= it.j1) {
-                    ok = read_seg(++n, it);
-                    j = it.j0;
-                    if (!ok) it.j1 = it.j0;
-                }
-                fetch();
-            } else if (v_due) {  // the last V
-                row = v_row, g = v_g, is_v = any = true;
-            }
-        };
-        uint32_t copied = 0;  // units
-        auto copy_unit = [&]() {
-            if (step == kSteps) next_tile();
-            if (any) {
-                const unsigned char *pool = static_cast<const unsigned char *>(is_v ? p.v_cache : p.k_cache) + g * HD + piece * 16;
-                const uint32_t dst = mine + (copied % kUnits) * (kUnit * 2048);
-                const size_t stride = static_cast<size_t>(p.Hkv) * HD;
-#pragma unroll
-                for (int i = 0; i < kUnit; ++i) {
-                    const int r = __shfl_sync(kFull, row, (step + i) * kStepKeys + key_of_lane);
-                    cp_async16(dst + i * 2048, pool + (r < 0 ? 0 : r) * stride, r < 0 ? 0 : 16);
-                }
-                ++copied;
-            }
-            step += kUnit;  // (of nothing, at the end)
-            cp_async_commit();
-        };
-        ok = read_seg(0, it);
+        bool ok = read_seg(0, it);
         if (!ok) it.j1 = it.j0;
         j = it.j0;
         fetch();
+        // Tiles are copied, and widened, in the order K 0, K 1, V 0, K 2, V 1, ...: K while it is less than two ahead of V.
+        uint32_t ck = 0, cv = 0;                         // copied
+        int row[2] = {-1, -1}, head[2] = {0, 0};         // of this lane's key, in the tiles whose K was copied last, and before it
+        float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+        int from = -1, from_head = 0, step = kSteps;     // of the tile that is being copied
+        const unsigned char *pool = nullptr;             // (nullptr: none is left)
+        uint32_t wk = 0, wv = 0;                         // widened
+        bool is_v = false;                               // the tile that is being widened
+        int done = kSteps;                               // of it
 #pragma unroll 1
-        for (int i = 0; i < kUnits; ++i) copy_unit();
-        // ---- what is widened: the same tiles
-        uint32_t used = 0;  // units
-        auto widen = [&](auto e, int off) {
-            using W = decltype(e);
-#pragma unroll 1
-            for (int s0 = 0; s0 < kSteps; s0 += kUnit) {
+        for (uint32_t u = 0; ok; ++u) {
+            if (u >= kUnits) {  // the unit that was copied kUnits steps ago
+                if (done == kSteps) {
+                    done = 0;
+                    is_v = !(wk < ck && wk - wv < 2);
+                    if (is_v && wv == wk) break;
+                    const uint32_t i = is_v ? wv : wk;
+                    if (!(ok = short_wait(bar(is_v ? W_VEMPTY : W_KEMPTY), (i & 1) ^ 1, abort_flag))) break;
+                    if (!is_v) {
+                        const bool before = ck == i + 2;  // the next tile's copies have begun
+                        const float key_vs = before ? vs[1] : vs[0];
+                        float *keys = reinterpret_cast<float *>(smem + Lay::OFF_KEYS) + (i % kKeyRing) * 3 * BN + w * 32 + lane;
+                        keys[0] = (before ? ks[1] : ks[0]) * p.scale_log2 * (E::kIsBf16 ? 1.f : 256.f);
+                        keys[BN] = __log2f(key_vs);
+                        keys[2 * BN] = __frcp_rn(key_vs) * (E::kIsBf16 ? 1.f : 0x1p-8f);
+                    }
+                }
                 cp_async_wait<kUnits - 1>();
-                const uint32_t src = mine + (used % kUnits) * (kUnit * 2048);
-                ++used;
+                const uint32_t src = mine + (u % kUnits) * (kUnit * 2048);
+                unsigned char *tile = smem + (is_v ? Lay::OFF_V : Lay::OFF_K) + (piece >> 2) * kHalf;
 #pragma unroll
                 for (int i = 0; i < kUnit; ++i) {
                     const uint4 x = lds128(src + i * 2048);
-                    const int k = w * 32 + (s0 + i) * kStepKeys + key_of_lane;
-                    const uint4 a = widen_e4m3x8<W>(x.x, x.y), b = widen_e4m3x8<W>(x.z, x.w);
-                    // chunks 2 * piece and 2 * piece + 1 of the row; lanes of the second 64 columns write theirs in the other
-                    // order, so that eight lanes meet eight different groups of banks
+                    const int k = w * 32 + (done + i) * kStepKeys + key_of_lane;
                     const bool other = piece >= 4;
-                    const int q = (2 * piece + other) & 7;
-                    unsigned char *at = smem + off + (piece >> 2) * kHalf + k * 128;
-                    *reinterpret_cast<uint4 *>(at + ((q ^ (k & 7)) << 4)) = other ? b : a;
-                    *reinterpret_cast<uint4 *>(at + (((q ^ 1) ^ (k & 7)) << 4)) = other ? a : b;
+                    const uint4 a = widen_e4m3x8<E>(other ? x.z : x.x, other ? x.w : x.y), b = widen_e4m3x8<E>(other ? x.x : x.z, other ? x.y : x.w);
+                    unsigned char *at = tile + k * 128 + ((chunk ^ (k & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(at) = a;
+                    *reinterpret_cast<uint4 *>(tile + k * 128 + ((chunk ^ 1 ^ (k & 7)) << 4)) = b;
                 }
-                copy_unit();
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
-#pragma unroll 1
-        for (uint32_t i = 0; ok; ++i) {  // K of tile i, V of tile i - 1
-            const bool k_there = i < k_tiles;
-            if (k_there) {
-                if (!(ok = warp_wait(bar(W_KEMPTY), (i & 1) ^ 1, abort_flag))) break;
-                float *keys = reinterpret_cast<float *>(smem + Lay::OFF_KEYS) + (i % kKeyRing) * 3 * BN + w * 32 + lane;
-                const bool before = k_tiles == i + 2;  // the next tile's copies have begun
-                const float key_vs = before ? vs[1] : vs[0];
-                keys[0] = (before ? ks[1] : ks[0]) * p.scale_log2 * (E::kIsBf16 ? 1.f : 256.f);
-                keys[BN] = __log2f(key_vs);
-                keys[2 * BN] = __frcp_rn(key_vs) * 0x1p-8f;
-                widen(E{}, Lay::OFF_K);
-                if (lane == 0) {
-                    mbar_arrive(bar(W_KEYS + i % kKeyRing));
-                    mbar_arrive(bar(W_KFULL));
+                done += kUnit;
+                if (done == kSteps) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (!is_v) mbar_arrive(bar(W_KEYS + wk % kKeyRing));
+                        mbar_arrive(bar(is_v ? W_VFULL : W_KFULL));
+                    }
+                    wk += !is_v, wv += is_v;
                 }
             }
-            if (i > 0) {
-                if (!warp_wait(bar(W_VEMPTY), i & 1, abort_flag)) {
-                    ok = false;
-                    break;
+            if (step == kSteps) {  // what is copied next
+                step = 0;
+                pool = nullptr;
+                if (it.j0 < it.j1 && ck - cv < 2) {
+                    row[1] = row[0], head[1] = head[0], ks[1] = ks[0], vs[1] = vs[0];
+                    const int pos = j * BN + w * 32 + lane;
+                    row[0] = -1, head[0] = it.g;
+                    ks[0] = vs[0] = 1.f;  // where no row sees the key: numbers that do no harm
+                    if (pos >= it.n_lo && pos < it.n_end) {
+                        if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks)) {
+                            const int off = p.geom.offset_of(pos);
+                            row[0] = id * p.geom.block_size + off;
+                            const size_t at = (static_cast<size_t>(id) * p.Hkv + it.g) * p.geom.block_size + off;
+                            ks[0] = __ldcg(p.k_scale + at);
+                            vs[0] = __ldcg(p.v_scale + at);
+                        } else {
+                            bad_seg[n & (kBadRing - 1)] = n + 1;
+                            raise_err(p.err, PA_DEVERR_TABLE);
+                        }
+                    }
+                    __syncwarp();
+                    from = row[0], from_head = head[0];
+                    pool = static_cast<const unsigned char *>(p.k_cache);
+                    ++ck;
+                    if (++j >= it.j1) {
+                        ok = read_seg(++n, it);
+                        j = it.j0;
+                        if (!ok) it.j1 = it.j0;
+                    }
+                    fetch();
+                } else if (cv < ck) {
+                    const bool before = ck == cv + 2;
+                    from = before ? row[1] : row[0], from_head = before ? head[1] : head[0];
+                    pool = static_cast<const unsigned char *>(p.v_cache);
+                    ++cv;
                 }
-                widen(F16{}, Lay::OFF_V);
-                if (lane == 0) mbar_arrive(bar(W_VFULL));
             }
-            if (!k_there) break;
+            if (pool) {
+                const unsigned char *base = pool + from_head * HD + piece * 16;
+                const uint32_t dst = mine + (u % kUnits) * (kUnit * 2048);
+#pragma unroll
+                for (int i = 0; i < kUnit; ++i) {
+                    const int r = __shfl_sync(kFull, from, (step + i) * kStepKeys + key_of_lane);
+                    cp_async16(dst + i * 2048, base + static_cast<uint64_t>(static_cast<uint32_t>(max(r, 0))) * stride, r < 0 ? 0 : 16);
+                }
+            }
+            step += kUnit;
+            cp_async_commit();
         }
         cp_async_wait<0>();
         if (!ok && lane == 0) give_up(p.err, abort_flag);
@@ -468,15 +447,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
             float m_use = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int j = it.j0; j < it.j1; ++j, ++t, ++tile) {
-                if (!(ok = warp_wait(s_full, t & 1, abort_flag))) break;
+                if (!(ok = short_wait(s_full, t & 1, abort_flag))) break;
                 if (!live) {
                     if (lane == 0) mbar_arrive(s_free);
                     // P's barrier counts tiles: not before the previous tile's PV has been issued
-                    if (t > 0 && !(ok = warp_wait(o_done, (t - 1) & 1, abort_flag))) break;
+                    if (t > 0 && !(ok = short_wait(o_done, (t - 1) & 1, abort_flag))) break;
                     if (lane == 0) mbar_arrive(p_full);
                     continue;
                 }
-                if (!(ok = warp_wait(bar(W_KEYS + tile % kKeyRing), (tile / kKeyRing) & 1, abort_flag))) break;
+                if (!(ok = short_wait(bar(W_KEYS + tile % kKeyRing), (tile / kKeyRing) & 1, abort_flag))) break;
                 const float4 *ks4 = reinterpret_cast<const float4 *>(smem + Lay::OFF_KEYS) + (tile % kKeyRing) * 3 * (BN / 4),
                              *lv4 = ks4 + BN / 4, *iv4 = lv4 + BN / 4;
                 tc_fence_after();
@@ -528,13 +507,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                     const float p0 = fast_exp2(f2_lo(xa)), p1 = fast_exp2(f2_hi(xa)), p2 = fast_exp2(f2_lo(xb)), p3 = fast_exp2(f2_hi(xb));
                     l2 = f2_fma(f2_pack(p0, p1), f2_pack(i4.x, i4.y), l2);
                     l2 = f2_fma(f2_pack(p2, p3), f2_pack(i4.z, i4.w), l2);
-                    // P is rounded to fp16 (the tensor cores' operand), the sum is not
-                    pk[e >> 1] = F16::pack2(p0, p1);
-                    pk[(e >> 1) + 1] = F16::pack2(p2, p3);
+                    // P is rounded to the storage type (the tensor cores' operand), the sum is not
+                    pk[e >> 1] = E::pack2(p0, p1);
+                    pk[(e >> 1) + 1] = E::pack2(p2, p3);
                 }
                 l = l * f + (f2_lo(l2) + f2_hi(l2));
                 if (t > 0) {  // the previous tile's PV has consumed P and completed O
-                    if (!(ok = warp_wait(o_done, (t - 1) & 1, abort_flag))) break;
+                    if (!(ok = short_wait(o_done, (t - 1) & 1, abort_flag))) break;
                     tc_fence_after();
                 }
                 if (!kPTmem && j == it.j0) {  // the warp's rows may still leave for the previous segment
@@ -570,7 +549,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
             }
-            if (ok) ok = warp_wait(o_done, (t - 1) & 1, abort_flag);
+            if (ok) ok = short_wait(o_done, (t - 1) & 1, abort_flag);
             if (!ok) break;
             if (!live) {
                 if (lane == 0) mbar_arrive(o_free);

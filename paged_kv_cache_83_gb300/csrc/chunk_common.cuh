@@ -55,6 +55,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     __syncwarp();
     return all;
 }
+// The same in few instructions, for kernels whose roles together hardly fit the instruction cache: it counts tries instead of
+// asking for the time (each suspends the thread for a time of the hardware's choosing, a microsecond or more: some seconds in all).
+constexpr uint32_t kWaitTries = 1u << 21;
+__device__ __forceinline__ bool short_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    bool ok = true;
+    for (uint32_t i = 0; !__all_sync(kFull, mbar_try_wait(bar, parity)); ++i)
+        if (i == kWaitTries || *abort_flag) {
+            ok = false;
+            break;
+        }
+    return __all_sync(kFull, ok);
+}
 __device__ __forceinline__ void give_up(int32_t *err, volatile int *abort_flag) {
     raise_err(err, PA_DEVERR_TIMEOUT);
     *abort_flag = 1;
