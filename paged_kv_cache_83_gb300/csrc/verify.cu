@@ -20,7 +20,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyThreads = 384, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyBlocks = 4;  // of an SM
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kResBits = 44;  // weights are multiples of 2^-44
 
@@ -36,6 +37,13 @@ struct VerifyParams {
     long long p_stride, q_stride;  // elements
     int S, V, total_q, slice;      // slice: weights of a warp, a multiple of 32 loads
 };
+
+// 16-byte load of what the grid before may have written (not the read-only path: this grid is launched beside that one)
+__device__ __forceinline__ uint4 ld_probs(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 
 template <class E>
 __device__ __forceinline__ void widen(const uint4 &w, float *f) {
@@ -53,7 +61,7 @@ __device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162flo
 template <class E, int kN>
 __device__ __forceinline__ void load_row(const typename E::T *row, int i, int V, bool wide, float (&f)[kN]) {
     if (wide && i >= 0 && i + kN <= V) {
-        widen<E>(ldg_stream(row + i), f);
+        widen<E>(ld_probs(row + i), f);
     } else {
 #pragma unroll
         for (int e = 0; e < kN; ++e) f[e] = i + e >= 0 && i + e < V ? widen1(row[i + e]) : 0.f;
@@ -96,7 +104,7 @@ __device__ __forceinline__ void weights_at(const Drawn<typename E::T> &d, int i,
 }
 
 template <class E>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(const __grid_constant__ VerifyParams p) {
     using T = typename E::T;
     constexpr int kN = 16 / sizeof(T);
     __shared__ long long warp_sum[2][kVerifyWarps], cta_sum[2];
@@ -106,6 +114,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
     const int s = blockIdx.x / ctas;
+    // launched beside what precedes it in the stream, whose results are read and written from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int a0 = p.cu_q[s], a1 = p.cu_q[s + 1];
     if (a0 < 0 || a1 < a0 || a1 > p.total_q || a1 == a0) {  // the same for every CTA of the cluster
         if (rank == 0 && tid == 0) {
@@ -268,19 +279,23 @@ template <class E>
 cudaError_t launch_verify_typed(const VerifyParams &in, cudaStream_t stream) {
     VerifyParams prm = in;
     constexpr int kN = 16 / sizeof(typename E::T);
-    // CTAs of a sequence: slices of at least 4096 numbers, eight CTAs (the portable cluster) at most
+    // CTAs of a sequence: slices of at least 4096 numbers, eight CTAs (the portable cluster) at most, and no more than leave
+    // all CTAs of the call on the SMs at once: each begins and ends with a chain of dependent loads and barriers.
     int ctas = 1;
-    while (ctas < 8 && prm.V > 4096 * ctas) ctas *= 2;
+    const long long room = static_cast<long long>(device_sm_count()) * kVerifyBlocks;
+    while (ctas < 8 && prm.V > 4096 * ctas && 2ll * ctas * prm.S <= room) ctas *= 2;
     const int per = 32 * kN, parts = ctas * kVerifyWarps;
     prm.slice = ((prm.V + kN + parts - 1) / parts + per - 1) / per * per;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cfg.gridDim = dim3(static_cast<unsigned>(prm.S) * ctas);
     cfg.blockDim = dim3(kVerifyThreads);
     return cudaLaunchKernelEx(&cfg, verify_kernel<E>, prm);
