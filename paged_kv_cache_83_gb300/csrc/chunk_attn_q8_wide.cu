@@ -341,15 +341,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                 cp_async_wait<kUnits - 1>();
                 const uint32_t src = mine + (u % kUnits) * (kUnit * 2048);
                 unsigned char *tile = smem + (is_v ? Lay::OFF_V : Lay::OFF_K) + (piece >> 2) * kHalf;
+                uint4 x[kUnit];  // all read before any is written: the order of reads and writes stays as it is here
+#pragma unroll
+                for (int i = 0; i < kUnit; ++i) x[i] = lds128(src + i * 2048);
 #pragma unroll
                 for (int i = 0; i < kUnit; ++i) {
-                    const uint4 x = lds128(src + i * 2048);
                     const int k = w * 32 + (done + i) * kStepKeys + key_of_lane;
                     const bool other = piece >= 4;
-                    const uint4 a = widen_e4m3x8<E>(other ? x.z : x.x, other ? x.w : x.y), b = widen_e4m3x8<E>(other ? x.x : x.z, other ? x.y : x.w);
-                    unsigned char *at = tile + k * 128 + ((chunk ^ (k & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(at) = a;
-                    *reinterpret_cast<uint4 *>(tile + k * 128 + ((chunk ^ 1 ^ (k & 7)) << 4)) = b;
+                    unsigned char *at = tile + k * 128;
+                    *reinterpret_cast<uint4 *>(at + ((chunk ^ (k & 7)) << 4)) =
+                        widen_e4m3x8<E>(other ? x[i].z : x[i].x, other ? x[i].w : x[i].y);
+                    *reinterpret_cast<uint4 *>(at + ((chunk ^ 1 ^ (k & 7)) << 4)) =
+                        widen_e4m3x8<E>(other ? x[i].x : x[i].z, other ? x[i].y : x[i].w);
                 }
                 done += kUnit;
                 if (done == kSteps) {
