@@ -603,9 +603,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             const int cnt = it.j1 - it.j0, rows = it.tok * p.G, par = n & 1;
             float *mx = fl + Lay::kMax + (par * 2 + h) * NT;
             const float *qs = fl + Lay::kQs + (n & 3) * Lay::kNC + col0;
-            // columns without a query row have a reference that leaves them no weight
-            if (wt < NT) mx[wt] = col0 + wt < rows ? kUnset : INFINITY;
-            if (!(ok = meet(false, any))) break;
             if (!(ok = wait_for(bar(Lay::B_QS + (n & 3)), (n >> 2) & 1, abort_flag))) break;  // the queries' scales
             float l[NT];
 #pragma unroll
@@ -689,10 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                     if (!(ok = meet(false, any))) break;
                     if (wt < NT) {
                         const float most = fmaxf(fmaxf(red[wt], red[NT + wt]), fmaxf(red[2 * NT + wt], red[3 * NT + wt]));
-                        const float old = mx[wt];
+                        // columns without a query row have a reference that leaves them no weight
+                        const float old = i > first ? mx[wt] : col0 + wt < rows ? kUnset : INFINITY;
                         const bool move = most > old + 8.f;  // never where old is +inf, or the largest -inf
                         fac[wt] = move ? fast_exp2(old - (most - 4.f)) : 1.f;
-                        if (move) mx[wt] = most - 4.f;
+                        mx[wt] = move ? most - 4.f : old;
                     }
                     if (!(ok = meet(false, any))) break;
 #pragma unroll
