@@ -88,19 +88,25 @@ __device__ __forceinline__ uint2 quantise8(const Eight &f, float inv) {
 }
 
 // A warp takes a token, or a part of it. It goes over the token's rows 32 / lanes at a time (a step): first queries and keys
-// side by side, then values. kAhead steps are loaded together before any is stored.
-template <class E, bool kPairs, bool kQ8>
+// side by side, then values. kAhead steps are loaded together before any is stored. kD: the head dim where whole rows of
+// that many elements are rotated in halves, 0: any (33,673 tokens of 16/8 heads x 128 into 8 bits: 89 us, with the general form 101).
+template <class E, bool kPairs, bool kQ8, int kD>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_kernel(const __grid_constant__ NormRopeParams p) {
+    constexpr bool kWhole = kD > 0;
+    const int D = kWhole ? kD : p.D, rot = kWhole ? kD : p.rot, lanes = kWhole ? kD / 16 : p.lanes;
+    const int lanes_log2 = kD == 64 ? 2 : kD == 128 ? 3 : p.lanes_log2;
     const int lane = threadIdx.x & 31;
     const unsigned warp = blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32;
     const int t = static_cast<int>(warp / static_cast<unsigned>(p.parts)), part = static_cast<int>(warp) - t * p.parts;
-    const int u = lane & (p.lanes - 1), row_of_lane = lane >> p.lanes_log2;
-    const int n8 = p.rot / 16;  // units that hold rotated pairs
+    const int u = lane & (lanes - 1), row_of_lane = lane >> lanes_log2;
+    const int n8 = rot / 16;  // units that hold rotated pairs
+    const bool turns = kWhole || u < n8;
     const int n_qk = p.Hq + p.Hkv;
     // The unit's two chunks of 8 elements in a head row of q or k, and of v. The last unit of a row may have one only.
-    const int e0 = u < n8 ? kPairs ? u * 16 : u * 8 : p.rot + (u - n8) * 16;
-    const int e1 = u < n8 && !kPairs ? p.rot / 2 + u * 8 : e0 + 8;
-    const bool there0 = u < p.units && e0 < p.D, there1 = u < p.units && e1 < p.D;
+    const int e0 = turns ? kPairs ? u * 16 : u * 8 : rot + (u - n8) * 16;
+    const int e1 = turns && !kPairs ? rot / 2 + u * 8 : e0 + 8;
+    const bool there0 = kWhole || (u < p.units && e0 < D), there1 = kWhole || (u < p.units && e1 < D);
+    const bool v_there0 = kWhole || u * 16 < D, v_there1 = kWhole || u * 16 + 8 < D;
     // launched beside what precedes it in the stream, whose results are read and written from here on
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");  // the attention's set-up may run beside this grid
@@ -108,14 +114,14 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
     // slot and positions side by side; the axes that are not there hold the first's position
     const int slot = *(p.slot_mapping + t);
     int pos[4] = {0, 0, 0, 0};
-    if (p.rot > 0) {
+    if (rot > 0) {
 #pragma unroll
         for (int a = 0; a < 4; ++a) pos[a] = a == 0 || a < p.n_axes ? *(p.positions + static_cast<size_t>(a) * p.T + t) : pos[0];
     }
     if (slot < 0) return;  // padding: none of this token's rows is read or written
     const unsigned top = max(max(static_cast<unsigned>(pos[0]), static_cast<unsigned>(pos[1])),
                              max(static_cast<unsigned>(pos[2]), static_cast<unsigned>(pos[3])));
-    const bool bad_pos = p.rot > 0 && top >= static_cast<unsigned>(p.max_pos);
+    const bool bad_pos = rot > 0 && top >= static_cast<unsigned>(p.max_pos);
     if (slot >= p.num_slots || bad_pos) {
         if (part == 0 && lane == 0)
             raise_err(p.err, (slot >= p.num_slots ? PA_DEVERR_SLOT : 0) | (bad_pos ? PA_DEVERR_POSITION : 0));
@@ -125,13 +131,13 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
     uint64_t c[4], s[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[e] = f2_pack(1.f, 1.f), s[e] = f2_pack(0.f, 0.f);
-    if (u < n8) {
+    if (turns) {
         const uint32_t axes = p.axis[u];
-        const int half = p.rot / 2;
+        const int half = rot / 2;
         const auto pos_of = [&](uint32_t a) { return a & 2u ? a & 1u ? pos[3] : pos[2] : a & 1u ? pos[1] : pos[0]; };
         if (axes == (axes & 15u) * 0x11111111u) {
             // one position for the unit: four 16-byte loads
-            const float *row = p.cos_sin + static_cast<size_t>(pos_of(axes & 3u)) * p.rot + u * 8;
+            const float *row = p.cos_sin + static_cast<size_t>(pos_of(axes & 3u)) * rot + u * 8;
             const float4 c0 = *reinterpret_cast<const float4 *>(row), c1 = *reinterpret_cast<const float4 *>(row + 4),
                          s0 = *reinterpret_cast<const float4 *>(row + half), s1 = *reinterpret_cast<const float4 *>(row + half + 4);
             c[0] = f2_pack(c0.x, c0.y), c[1] = f2_pack(c0.z, c0.w), c[2] = f2_pack(c1.x, c1.y), c[3] = f2_pack(c1.z, c1.w);
@@ -139,8 +145,8 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float *x = p.cos_sin + static_cast<size_t>(pos_of((axes >> (8 * e)) & 3u)) * p.rot + u * 8 + 2 * e;
-                const float *y = p.cos_sin + static_cast<size_t>(pos_of((axes >> (8 * e + 4)) & 3u)) * p.rot + u * 8 + 2 * e + 1;
+                const float *x = p.cos_sin + static_cast<size_t>(pos_of((axes >> (8 * e)) & 3u)) * rot + u * 8 + 2 * e;
+                const float *y = p.cos_sin + static_cast<size_t>(pos_of((axes >> (8 * e + 4)) & 3u)) * rot + u * 8 + 2 * e + 1;
                 c[e] = f2_pack(*x, *y);
                 s[e] = f2_pack(x[half], y[half]);
             }
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
     }
     const unsigned char *const q_row = p.q + t * p.q_stride + e0 * 2, *const k_row = p.k + t * p.k_stride + e0 * 2,
                         *const v_row = p.v + t * p.v_stride + u * 32;
-    const int row_bytes = p.D * 2, next = (e1 - e0) * 2, per_step = 32 >> p.lanes_log2;
+    const int row_bytes = D * 2, next = (e1 - e0) * 2, per_step = 32 >> lanes_log2;
     const size_t cache_row = static_cast<size_t>(slot) * p.Hkv;
     size_t scale_row = 0;  // index of the slot's scale of kv head 0
     if constexpr (kQ8) scale_row = static_cast<size_t>(p.geom.block_of(slot)) * p.Hkv * p.geom.block_size + p.geom.offset_of(slot);
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
         float most = largest(g, largest(f, 0.f));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1)
-            if (o < p.lanes) most = max_nan3(most, most, __shfl_xor_sync(0xffffffffu, most, o));
+            if (o < lanes) most = max_nan3(most, most, __shfl_xor_sync(0xffffffffu, most, o));
         float scale = __fdiv_rn(most, 448.f);
         if (scale < 0x1p-90f) scale = 0x1p-90f;
         const float inv = __frcp_rn(scale);
@@ -180,8 +186,8 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
                 const int r = (step + i - p.qk_steps) * per_step + row_of_lane;
                 const unsigned char *src = v_row + r * row_bytes;
                 const bool mine = step + i < end && r < p.Hkv;
-                if (mine && u * 16 < p.D) x0[i] = ld_row(src);
-                if (mine && u * 16 + 8 < p.D) x1[i] = ld_row(src + 16);
+                if (mine && v_there0) x0[i] = ld_row(src);
+                if (mine && v_there1) x1[i] = ld_row(src + 16);
             }
         }
 #pragma unroll
@@ -189,9 +195,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
             if (step + i >= end) break;
             if (step + i >= p.qk_steps) {
                 const int r = (step + i - p.qk_steps) * per_step + row_of_lane;
-                const bool on0 = r < p.Hkv && u * 16 < p.D, on1 = r < p.Hkv && u * 16 + 8 < p.D;
+                const bool on0 = r < p.Hkv && v_there0, on1 = r < p.Hkv && v_there1;
                 if constexpr (kQ8) {
-                    store8(widen8<E>(x0[i]), widen8<E>(x1[i]), p.v_cache + (cache_row + r) * p.D + u * 16, p.v_scale, r, on0, on1, 8);
+                    store8(widen8<E>(x0[i]), widen8<E>(x1[i]), p.v_cache + (cache_row + r) * D + u * 16, p.v_scale, r, on0, on1, 8);
                 } else {
                     unsigned char *dst = p.v_cache + (cache_row + r) * row_bytes + u * 32;  // values are bit copies
                     if (on0) stg128(dst, x0[i]);
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
                 float squares = f2_lo(sum) + f2_hi(sum);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1)
-                    if (o < p.lanes) squares += __shfl_xor_sync(0xffffffffu, squares, o);
+                    if (o < lanes) squares += __shfl_xor_sync(0xffffffffu, squares, o);
                 const unsigned char *w = is_q ? p.q_weight : p.k_weight;
                 if (w) {
                     const float m1 = rsqrtf(fmaf(squares, p.inv_d, p.eps));
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
                     }
                 }
             }
-            if (u < n8) {
+            if (turns) {
                 if constexpr (kPairs) {
                     // pairs lie side by side: (x0, x1) c + (-x1, x0) s, the latter product rounded (as in the rotation without norms)
 #pragma unroll
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
             if constexpr (kQ8) {
                 // (steps of queries alone have nothing for the cache)
                 if ((step + i + 1) * per_step > p.Hq)
-                    store8(f, g, p.k_cache + (cache_row + (r - p.Hq)) * p.D + e0, p.k_scale, r - p.Hq, on0 && !is_q, on1 && !is_q, e1 - e0);
+                    store8(f, g, p.k_cache + (cache_row + (r - p.Hq)) * D + e0, p.k_scale, r - p.Hq, on0 && !is_q, on1 && !is_q, e1 - e0);
             }
         }
     }
@@ -273,8 +279,10 @@ cudaError_t launch_norm_typed(const NormRopeParams &prm, bool pairs, unsigned gr
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kNormThreads);
-    return pairs ? cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, true, kQ8>, prm)
-                 : cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, false, kQ8>, prm);
+    if (pairs) return cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, true, kQ8, 0>, prm);
+    if (prm.rot == 64 && prm.D == 64) return cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, false, kQ8, 64>, prm);
+    if (prm.rot == 128 && prm.D == 128) return cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, false, kQ8, 128>, prm);
+    return cudaLaunchKernelEx(&cfg, norm_rope_store_kv_kernel<E, false, kQ8, 0>, prm);
 }
 
 }  // namespace
