@@ -931,8 +931,8 @@ cudaError_t launch_chunk_q8(const ChunkQ8Args &x, cudaStream_t stream) {
     prm.scale_log2 = a.scale * kLog2e;
     if (rows > 64) return launch_chunk_q8_wide(prm, x, stream);
     const long long krows = static_cast<long long>(a.num_blocks) * a.block_size;
-    if (!gather && (!encode_rows_e4m3(&prm.tm_k, a.k_cache, a.Hkv, a.D, krows, R) ||
-                    !encode_rows_e4m3(&prm.tm_v, a.v_cache, a.Hkv, a.D, krows, R)))
+    if (!gather && (!encode_rows_e4m3(&prm.tm_k, a.k_cache, a.Hkv, a.D, krows, R, true) ||
+                    !encode_rows_e4m3(&prm.tm_v, a.v_cache, a.Hkv, a.D, krows, R, true)))
         return cudaErrorInvalidValue;
     auto go = [&](auto e, auto hd) {
         using E = decltype(e);

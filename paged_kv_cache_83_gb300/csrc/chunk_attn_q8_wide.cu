@@ -1,21 +1,26 @@
 // chunk_attn_q8_wide.cu: pa_chunk_attn_q8 for chunks of more than 64 query rows a kv head (tokens x group), such as pieces of
 // long prompts.
 //
-// The mathematics is chunk_attn.cu's, with the scales of an 8-bit cache: x_j = ks_j (scale q.K8_j) + log2 vs_j, weights
-// 2^(x_j - m), O = sum 2^(x_j - m) V8_j, and the sum takes 2^(x_j - m) / vs_j.
+// The mathematics is chunk_attn.cu's, with the scales of an 8-bit cache: scores ks_j (scale q.K8_j), weights p_j,
+// O = sum (vs_j p_j) V8_j. In bf16 the weights are multiplied by vs_j before they are rounded; fp16 has not the range for that
+// and takes vs_j into the exponent, w_j = 2^(x_j - m) with x_j = s_j + log2 vs_j, and the sum is of w_j / vs_j.
 //
-// Bound by the softmax warps, as there. So the cache's e4m3 rows are widened to the storage type, exactly, on their way to
-// shared memory, once for the 256 query rows of an item, and queries and weights stay whole operands (as sums of e4m3 pieces they
-// cost the softmax three conversions a weight; that form of 64 rows an item took 955 us for two chunks of 2k tokens at 12-16k, 16/8
-// heads x 128). Four warps copy the rows ahead, any page size alike, widen them and write the swizzled
-// tile that the matrix instructions read; one buffer for K and one for V suffice, since a tile's K is wanted a
-// whole softmax before its V.
+// The cache's e4m3 rows are widened to the storage type, exactly, on their way to shared memory, once for the 256 query rows of
+// an item, and queries and weights stay whole operands. (As sums of e4m3 pieces beside rows that are used as they lie, the
+// weights cost the softmax three conversions each: that form, of 64 rows an item, took 955 us where this one takes 550: two
+// chunks of 2k tokens at contexts of 12-16k, 16/8 heads x 128, bf16.) A producer brings halves of tiles by TMA and four warps
+// widen them into the swizzled tile that the matrix instructions read (loaders that copied for themselves: 675 us). One buffer
+// for K and one for V suffice, since a tile's K is wanted a whole softmax before its V.
 //
-//   warp 3        scheduler, as in chunk_attn.cu
-//   warp 0        brings the queries of a segment by TMA
+// Bound by the softmax warps, as there: at that shape 0.78 PFLOP/s, 0.41 of the burst peak, and 5500 clocks a key tile of both
+// row tiles. Against the 16-bit cache's kernel they read two numbers a key from shared memory and multiply twice more a
+// weight; with log2 vs in the exponent and 1 / vs in the sum for bf16 as well it was 587 us.
+//
+//   warp 3        scheduler, as in chunk_attn.cu; brings the queries of a segment by TMA
+//   warp 0        producer: halves of K and V tiles as they lie in the cache, and the scales of their keys
 //   warps 1, 2    one MMA issuer per row tile
 //   warps 4-11    softmax, a thread a query row
-//   warps 12-15   loaders: K and V tiles, and the three numbers of a key: scale * ks, log2 vs, 1 / vs
+//   warps 12-15   loaders: K and V tiles, and the numbers of a key: scale * ks, and vs, or log2 vs and 1 / vs
 #include <type_traits>
 
 #include "chunk_wide.cuh"
@@ -28,14 +33,13 @@ namespace {
 using namespace chunk;
 
 constexpr int kWideThreads = 512;
-constexpr int kWideReaders = 15;  // roles that read the queue of segments, by warp
+constexpr int kWideReaders = 15;  // roles that read the queue of segments, by warp: all but the scheduler
 constexpr int kKeyRing = 4;       // key tiles whose numbers are held
-// Segments in the queue. The loaders look two tiles ahead of the products, which may be two segments: they wait for segment
-// n + 2 to be published, before they bring the V of n - 1, and so for all roles to have read n + 2 - kQueue.
-constexpr int kQueue = 4;
-constexpr int kUnit = 4, kUnits = 3;  // pieces of a loader's unit, units in flight
-// registers of a thread by warpgroup: 88 + 2 * 168 + 88 = 4 * 128
-constexpr int kRegsSmall = 88, kRegsSoftmax = 168, kRegsLoad = 88;
+constexpr int kQueue = 4;         // segments
+constexpr int kStages = 3;        // halves of tiles (64 keys) that are under way as they lie in the cache
+constexpr int kHalfKeys = BN / 2;
+// registers of a thread by warpgroup: 72 + 2 * 176 + 88 = 4 * 128
+constexpr int kRegsSmall = 72, kRegsSoftmax = 176, kRegsLoad = 88;
 
 struct WideParams : ChunkParams {
     const float *k_scale, *v_scale;  // [num_blocks, Hkv, block_size]
@@ -48,7 +52,9 @@ enum {
     W_KEMPTY,               // both issuers' QKs are done with it
     W_VFULL,                // a V tile is written
     W_VEMPTY,               // both issuers' PVs are done with it
-    W_KEYS,                 // + tile % kKeyRing: the keys' numbers are written (4 arrivals)
+    W_SFULL,                // + half tile % kStages: it landed, with its keys' scales if it is of K (the tile, and 32 lanes' copies)
+    W_SEMPTY = W_SFULL + kStages,  // the loaders have read it (4 arrivals)
+    W_KEYS = W_SEMPTY + kStages,   // + tile % kKeyRing: the keys' numbers are written (4 arrivals)
     W_S = W_KEYS + kKeyRing,  // + h: S is in TMEM
     W_F = W_S + 2,          // + h: the softmax has read S (4 arrivals)
     W_P = W_F + 2,          // + h: P is written (4 arrivals)
@@ -64,8 +70,8 @@ struct LayWide {
     static constexpr int kHalves = HD / 64;
     static constexpr int kQ = BM * HD * 2, kKV = BN * HD * 2, kP = BM * BN * 2;
     static constexpr int OFF_QA = 0, OFF_QB = kQ, OFF_PA = 2 * kQ, OFF_PB = OFF_PA + kP, OFF_K = OFF_PB + kP, OFF_V = OFF_K + kKV,
-                         OFF_STAGE = OFF_V + kKV,  // the loaders' units: 16 bytes a thread and piece
-                         OFF_KEYS = OFF_STAGE + kUnits * kUnit * 2048;  // per tile of the ring: scale * ks [BN], log2 vs [BN], 1 / vs [BN]
+                         OFF_STAGE = OFF_V + kKV, OFF_SCALE = OFF_STAGE + kStages * kHalfKeys * HD,  // of K, then of V
+                         OFF_KEYS = OFF_SCALE + kStages * 2 * kHalfKeys * 4;  // per tile of the ring: scale * ks [BN], vs or log2 vs [BN], 1 / vs [BN]
     static constexpr int OFF_BAR = OFF_KEYS + kKeyRing * 3 * BN * 4;
     static constexpr int OFF_ITEMS = OFF_BAR + W_BARS * 8;
     static constexpr int OFF_BAD = OFF_ITEMS + kQueue * static_cast<int>(sizeof(SegInfo));
@@ -100,7 +106,7 @@ __device__ __forceinline__ uint4 widen_e4m3x8(uint32_t a, uint32_t b) {
                       widen_e4m3x2<E>(__byte_perm(b, 0, 0x1404)), widen_e4m3x2<E>(__byte_perm(b, 0, 0x3424)));
 }
 
-template <class E, int HD>
+template <class E, int HD, bool kGather>
 __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __grid_constant__ WideParams p) {
     using T = typename E::T;
     using Lay = LayWide<HD>;
@@ -122,7 +128,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
     if (tid < W_BARS) {
         uint32_t count = 1;
         if (tid == W_QEMPTY || tid == W_KEMPTY || tid == W_VEMPTY) count = 2;
-        if (tid == W_KFULL || tid == W_VFULL || (tid >= W_KEYS && tid < W_S)) count = 4;
+        if (tid == W_KFULL || tid == W_VFULL || (tid >= W_SEMPTY && tid < W_S)) count = 4;  // W_SEMPTY, W_KEYS
+        if (tid >= W_SFULL && tid < W_SEMPTY) count = 1 + 32;
         if ((tid >= W_F && tid < W_O) || (tid >= W_OFREE && tid < W_END)) count = 4;
         if (tid >= W_IEMPTY) count = kWideReaders;
         mbar_init(bar(tid), count);
@@ -157,42 +164,147 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
     if (warp < 4) {
         regs_down<kRegsSmall>();
         if (warp == 3) {
-            // ================================== scheduler ==================================
-            int published = 0;
-            const bool ok = walk_share(p, *share, [&](const SegInfo &it) {
-                if (!short_wait(bar(W_IEMPTY + published % kQueue), ((published / kQueue) & 1) ^ 1, abort_flag)) return false;
+            // =========================== scheduler, and the queries ===========================
+            prefetch_tmap(&p.tm_q);
+            int n = 0;  // segments published
+            bool ok = walk_share(p, *share, [&](const SegInfo &it) {
+                if (!short_wait(bar(W_IEMPTY + n % kQueue), ((n / kQueue) & 1) ^ 1, abort_flag)) return false;
                 if (lane == 0) {
-                    items[published % kQueue] = it;
-                    mbar_arrive(bar(W_IFULL + published % kQueue));
+                    items[n % kQueue] = it;
+                    mbar_arrive(bar(W_IFULL + n % kQueue));
                 }
                 __syncwarp();
-                ++published;
-                return true;
-            });
-            if (!ok && lane == 0) give_up(p.err, abort_flag);
-        } else if (warp == 0) {
-            // =================================== queries ===================================
-            prefetch_tmap(&p.tm_q);
-            int n = 0;
-            bool ok = true;
-            for (SegInfo cur{};; ++n) {
-                if (!(ok = read_seg(n, cur)) || cur.j0 == cur.j1) break;
-                // once both issuers are past the previous segment's last QK
-                if (n > 0 && !(ok = short_wait(bar(W_QEMPTY), (n - 1) & 1, abort_flag))) break;
+                if (it.j0 == it.j1) return true;
+                // its queries, once both issuers are past the previous segment's last QK
+                if (n > 0 && !short_wait(bar(W_QEMPTY), (n - 1) & 1, abort_flag)) return false;
                 if (lane == 0) {
-                    const int tiles = has_b(cur) ? 2 : 1;
+                    const int tiles = has_b(it) ? 2 : 1;
                     const uint32_t half_bytes = static_cast<uint32_t>(p.tt) * p.G * 128;
                     mbar_arrive_expect_tx(bar(W_QFULL), tiles * kHalves * half_bytes);
                     for (int h = 0; h < tiles; ++h)
                         for (int half = 0; half < kHalves; ++half)
-                            tma_load_3d(sbase + (h ? Lay::OFF_QB : Lay::OFF_QA) + half * kHalf, &p.tm_q, half * 64, cur.g * p.G,
-                                        cur.tok0 + h * p.tt, bar(W_QFULL));
+                            tma_load_3d(sbase + (h ? Lay::OFF_QB : Lay::OFF_QA) + half * kHalf, &p.tm_q, half * 64, it.g * p.G,
+                                        it.tok0 + h * p.tt, bar(W_QFULL));
                 }
                 __syncwarp();
-            }
+                ++n;
+                return true;
+            });
             if (!ok && lane == 0) give_up(p.err, abort_flag);
             // no copy may still be in flight at exit
             if (lane == 0 && n > 0 && !mbar_wait(bar(W_QFULL), (n - 1) & 1)) give_up(p.err, abort_flag);
+            __syncwarp();
+        } else if (warp == 0) {
+            // =================================== producer ===================================
+            // Halves of K and V tiles as they lie in the cache, in the order K 0, K 1, V 0, K 2, V 1, ..., with the scales of their keys
+            // with K; boxes of R rows by TMA, or (blocks of fewer than 8 aligned rows) row by row.
+            if constexpr (!kGather) {
+                prefetch_tmap(&p.tm_k);
+                prefetch_tmap(&p.tm_v);
+            }
+            constexpr int kRowsLane = kGather ? BN / 32 : 1;
+            const int R = p.box_rows, nbox = BN / R;
+            struct Tile {
+                int r[kRowsLane], id[kRowsLane];  // pool rows of the lane's boxes (keys), -1: not read; their blocks
+                int g;
+            };
+            int next_id[kRowsLane];  // the table entries of the next tile, fetched ahead
+            bool next_needed[kRowsLane];
+            auto pos_of = [&](int j, int i) { return j * BN + (kGather ? lane + 32 * i : lane * R); };
+            auto fetch = [&](const SegInfo &it, int j) {
+                const int32_t *row = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks;
+#pragma unroll
+                for (int i = 0; i < kRowsLane; ++i) {
+                    const int pos = pos_of(j, i);
+                    next_needed[i] = (kGather || lane < nbox) && pos < it.n_end && pos + (kGather ? 0 : R - 1) >= it.n_lo;
+                    next_id[i] = next_needed[i] ? ld_index(row + p.geom.block_of(pos)) : 0;
+                }
+            };
+            auto scale_at = [&](int r, int id, int g) {
+                return r + (static_cast<long long>(id) * (p.Hkv - 1) + g) * p.geom.block_size;
+            };
+            // of the four keys whose scales this lane copies (lanes 0-15 those of K, 16-31 of V), in a tile's first half
+            const int key4 = (lane & 15) * 4, box4 = key4 / R, in_box4 = key4 - box4 * R, boxes_half = kGather ? 0 : kHalfKeys / R;
+            uint32_t u = 0;  // halves loaded
+            auto load = [&](const Tile &t, bool is_v) -> bool {
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf, ++u) {
+                    const uint32_t slot = u % kStages, full = bar(W_SFULL) + 8 * slot;
+                    if (!short_wait(bar(W_SEMPTY) + 8 * slot, ((u / kStages) & 1) ^ 1, abort_flag)) return false;
+                    const uint32_t dst = sbase + Lay::OFF_STAGE + slot * kHalfKeys * HD, sc = sbase + Lay::OFF_SCALE + slot * 2 * kHalfKeys * 4;
+                    if constexpr (kGather) {
+                        if (lane == 0) mbar_arrive(full);
+                        const unsigned char *pool = static_cast<const unsigned char *>(is_v ? p.v_cache : p.k_cache);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = hf ? t.r[2 + e] : t.r[e], id = hf ? t.id[2 + e] : t.id[e], k = lane + 32 * e;
+                            if (r < 0) continue;
+                            const unsigned char *src = pool + (static_cast<size_t>(r) * p.Hkv + t.g) * HD;
+#pragma unroll
+                            for (int c = 0; c < HD / 16; ++c) cp_async16(dst + k * HD + c * 16, src + c * 16, 16);
+                            if (!is_v) {
+                                const long long from = scale_at(r, id, t.g);
+                                cp_async4(sc + k * 4, p.k_scale + from);
+                                cp_async4(sc + (kHalfKeys + k) * 4, p.v_scale + from);
+                            }
+                        }
+                    } else {
+                        const int b = lane - hf * boxes_half;
+                        const bool mine = b >= 0 && b < boxes_half && t.r[0] >= 0;
+                        const uint32_t boxes = __popc(__ballot_sync(kFull, mine));
+                        if (lane == 0) mbar_arrive_expect_tx(full, boxes * static_cast<uint32_t>(R) * HD);
+                        __syncwarp();
+                        if (mine) tma_load_3d(dst + b * R * HD, is_v ? &p.tm_v : &p.tm_k, 0, t.g, t.r[0], full);
+                        if (!is_v) {
+                            const int r = __shfl_sync(kFull, t.r[0], box4 + hf * boxes_half), id = __shfl_sync(kFull, t.id[0], box4 + hf * boxes_half);
+                            if (r >= 0)
+                                cp_async16(sc + lane * 16, (lane < 16 ? p.k_scale : p.v_scale) + scale_at(r, id, t.g) + in_box4, 16);
+                        }
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+                }
+                return true;
+            };
+            SegInfo cur{};
+            Tile last{};        // whose V is still to come
+            bool owed = false;
+            bool ok = read_seg(0, cur);
+            if (ok && cur.j0 < cur.j1) fetch(cur, cur.j0);
+            int n = 0, j = cur.j0;
+#pragma unroll 1
+            while (ok && (cur.j0 < cur.j1 || owed)) {
+                Tile t{};
+                const bool there = cur.j0 < cur.j1;
+                if (there) {
+                    t.g = cur.g;
+#pragma unroll
+                    for (int i = 0; i < kRowsLane; ++i) {
+                        t.id[i] = next_id[i];
+                        t.r[i] = next_needed[i] ? next_id[i] * p.geom.block_size + p.geom.offset_of(pos_of(j, i)) : -1;
+                        if (next_needed[i] && static_cast<unsigned>(next_id[i]) >= static_cast<unsigned>(p.num_blocks)) {
+                            t.r[i] = -1;
+                            bad_seg[n & (kBadRing - 1)] = n + 1;
+                            raise_err(p.err, PA_DEVERR_TABLE);
+                        }
+                    }
+                    if (j + 1 < cur.j1) fetch(cur, j + 1);  // in flight while this tile is loaded
+                    ok = load(t, false);
+                }
+                if (ok && owed) ok = load(last, true);
+                last = t;
+                owed = there;
+                if (ok && there && ++j == cur.j1) {
+                    ok = read_seg(++n, cur);
+                    if (!ok) break;
+                    j = cur.j0;
+                    if (cur.j0 < cur.j1) fetch(cur, j);
+                }
+            }
+            if (!ok && lane == 0) give_up(p.err, abort_flag);
+            // no copy may still be in flight at exit
+            if (lane == 0)
+                for (uint32_t i = u > kStages ? u - kStages : 0; i < u; ++i)
+                    if (!mbar_wait(bar(W_SFULL) + 8 * (i % kStages), (i / kStages) & 1)) give_up(p.err, abort_flag);
             __syncwarp();
         } else {
             // ============================ MMA issuer of one row tile =============================
@@ -286,135 +398,91 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
     } else if (warp >= 12) {
         // =================================== loaders ===================================
         regs_down<kRegsLoad>();
-        // A warp has 32 keys of a tile, a lane 16 elements (one 16-byte piece) of every kStepKeys-th of them: kSteps pieces a tile,
-        // which it copies to room of its own in shared memory, kUnit pieces (a unit) at a time and kUnits units ahead, and
-        // widens from there itself: nobody else waits for its copies. Lane l looks up key l's place in the pool and loads its
-        // scales. One loop, one copy of the code: with the loads in registers, and with the loop's ends unrolled, it did not stay in
-        // the instruction cache beside the softmax's (1001 and 715 us for the two chunks).
-        constexpr int kPieces = HD / 16, kStepKeys = 32 / kPieces, kSteps = 32 / kStepKeys;
-        static_assert(kSteps % kUnit == 0);
-        const int w = warp - 12, piece = lane % kPieces, key_of_lane = lane / kPieces;
-        const uint32_t mine = sbase + Lay::OFF_STAGE + (tid - 384) * 16;  // pieces 2 KB apart
+        // They widen the halves that landed into the tile that the matrix instructions read, in the order in which they come: K
+        // while it is less than two tiles ahead of V. A warp has 16 keys of a half, a lane 16 elements (one 16-byte piece) of every
+        // kStepKeys-th of them.
+        constexpr int kPieces = HD / 16, kStepKeys = 32 / kPieces, kSteps = 16 / kStepKeys;
+        const int w = warp - 12, piece = lane % kPieces, row0 = w * 16 + lane / kPieces;
         // chunks 2 * piece and 2 * piece + 1 of a row; lanes of the second 64 columns write theirs in the other
         // order, so that eight lanes meet eight different groups of banks
-        const int chunk = (2 * piece + (piece >= 4)) & 7;
-        const uint32_t stride = static_cast<uint32_t>(p.Hkv) * HD;
+        const bool other = piece >= 4;
+        const int chunk = (2 * piece + other) & 7;
         SegInfo it{};
-        int n = 0, j = 0, id = 0;  // the tile whose K is copied next; the table entry of this lane's key in it
-        auto fetch = [&]() {
-            const int pos = j * BN + w * 32 + lane;
-            id = 0;
-            if (it.j0 < it.j1 && pos >= it.n_lo && pos < it.n_end)
-                id = ld_index(p.block_tables + static_cast<size_t>(it.s) * p.max_blocks + p.geom.block_of(pos));
-        };
-        bool ok = read_seg(0, it);
-        if (!ok) it.j1 = it.j0;
-        j = it.j0;
-        fetch();
-        // Tiles are copied, and widened, in the order K 0, K 1, V 0, K 2, V 1, ...: K while it is less than two ahead of V.
-        uint32_t ck = 0, cv = 0;                         // copied
-        int row[2] = {-1, -1}, head[2] = {0, 0};         // of this lane's key, in the tiles whose K was copied last, and before it
-        float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
-        int from = -1, from_head = 0, step = kSteps;     // of the tile that is being copied
-        const unsigned char *pool = nullptr;             // (nullptr: none is left)
-        uint32_t wk = 0, wv = 0;                         // widened
-        bool is_v = false;                               // the tile that is being widened
-        int done = kSteps;                               // of it
+        bool ok = read_seg(0, it), end = !ok || it.j0 == it.j1;
+        int n = 0, j = it.j0;
+        uint32_t wk = 0, wv = 0, u = 0;      // tiles of K and V widened, halves used
+        int lo[2] = {0, 0}, hi[2] = {0, 0};  // the keys that some row sees, in the tiles whose K was widened last, and before it
 #pragma unroll 1
-        for (uint32_t u = 0; ok; ++u) {
-            if (u >= kUnits) {  // the unit that was copied kUnits steps ago
-                if (done == kSteps) {
-                    done = 0;
-                    is_v = !(wk < ck && wk - wv < 2);
-                    if (is_v && wv == wk) break;
-                    const uint32_t i = is_v ? wv : wk;
-                    if (!(ok = short_wait(bar(is_v ? W_VEMPTY : W_KEMPTY), (i & 1) ^ 1, abort_flag))) break;
-                    if (!is_v) {
-                        const bool before = ck == i + 2;  // the next tile's copies have begun
-                        const float key_vs = before ? vs[1] : vs[0];
-                        float *keys = reinterpret_cast<float *>(smem + Lay::OFF_KEYS) + (i % kKeyRing) * 3 * BN + w * 32 + lane;
-                        keys[0] = (before ? ks[1] : ks[0]) * p.scale_log2 * (E::kIsBf16 ? 1.f : 256.f);
-                        keys[BN] = __log2f(key_vs);
-                        keys[2 * BN] = __frcp_rn(key_vs) * (E::kIsBf16 ? 1.f : 0x1p-8f);
+        while (ok) {
+            if (!end && wk - wv < 2 && j == it.j1) {
+                ok = read_seg(++n, it);
+                if (!ok) break;
+                j = it.j0;
+                end = it.j0 == it.j1;
+            }
+            const bool is_v = end || wk - wv == 2;
+            if (is_v && wv == wk) break;
+            if (!is_v) {
+                lo[1] = lo[0], hi[1] = hi[0];
+                lo[0] = it.n_lo - j * BN, hi[0] = it.n_end - j * BN;
+                ++j;
+            }
+            const bool before = is_v && wk - wv == 2;
+            const int z0 = before ? lo[1] : lo[0], z1 = before ? hi[1] : hi[0];
+            const uint32_t i = is_v ? wv : wk;
+            if (!(ok = short_wait(bar(is_v ? W_VEMPTY : W_KEMPTY), (i & 1) ^ 1, abort_flag))) break;
+            unsigned char *tile = smem + (is_v ? Lay::OFF_V : Lay::OFF_K) + (piece >> 2) * kHalf;
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf, ++u) {
+                const uint32_t slot = u % kStages;
+                if (!(ok = short_wait(bar(W_SFULL) + 8 * slot, (u / kStages) & 1, abort_flag))) break;
+                const uint32_t src = sbase + Lay::OFF_STAGE + slot * kHalfKeys * HD + row0 * HD + piece * 16;
+                uint4 x[kSteps];  // all read before any is written: the order of reads and writes stays as it is here
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) x[e] = lds128(src + e * kStepKeys * HD);
+                if (!is_v && lane < 16) {
+                    const int k = hf * kHalfKeys + w * 16 + lane;
+                    const float *sc = reinterpret_cast<const float *>(smem + Lay::OFF_SCALE) + slot * 2 * kHalfKeys + w * 16 + lane;
+                    float ks = sc[0], vs = sc[kHalfKeys];
+                    if (k < z0 || k >= z1) ks = vs = 1.f;  // no row sees it: numbers that do no harm, whatever lies there
+                    float *keys = reinterpret_cast<float *>(smem + Lay::OFF_KEYS) + (i % kKeyRing) * 3 * BN + k;
+                    if constexpr (E::kIsBf16) {
+                        keys[0] = ks * p.scale_log2;
+                        keys[BN] = vs;
+                    } else {  // (the widened rows are 2^-8 of what they stand for)
+                        keys[0] = ks * p.scale_log2 * 256.f;
+                        keys[BN] = __log2f(vs);
+                        keys[2 * BN] = __frcp_rn(vs) * 0x1p-8f;
                     }
                 }
-                cp_async_wait<kUnits - 1>();
-                const uint32_t src = mine + (u % kUnits) * (kUnit * 2048);
-                unsigned char *tile = smem + (is_v ? Lay::OFF_V : Lay::OFF_K) + (piece >> 2) * kHalf;
-                uint4 x[kUnit];  // all read before any is written: the order of reads and writes stays as it is here
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(W_SEMPTY) + 8 * slot);
+                if (z0 > hf * kHalfKeys || z1 < (hf + 1) * kHalfKeys) {  // keys that no row sees are zeros, whatever lies there
 #pragma unroll
-                for (int i = 0; i < kUnit; ++i) x[i] = lds128(src + i * 2048);
+                    for (int e = 0; e < kSteps; ++e) {
+                        const int k = hf * kHalfKeys + row0 + e * kStepKeys;
+                        if (k < z0 || k >= z1) x[e] = make_uint4(0, 0, 0, 0);
+                    }
+                }
 #pragma unroll
-                for (int i = 0; i < kUnit; ++i) {
-                    const int k = w * 32 + (done + i) * kStepKeys + key_of_lane;
-                    const bool other = piece >= 4;
+                for (int e = 0; e < kSteps; ++e) {
+                    const int k = hf * kHalfKeys + row0 + e * kStepKeys;
                     unsigned char *at = tile + k * 128;
                     *reinterpret_cast<uint4 *>(at + ((chunk ^ (k & 7)) << 4)) =
-                        widen_e4m3x8<E>(other ? x[i].z : x[i].x, other ? x[i].w : x[i].y);
+                        widen_e4m3x8<E>(other ? x[e].z : x[e].x, other ? x[e].w : x[e].y);
                     *reinterpret_cast<uint4 *>(at + ((chunk ^ 1 ^ (k & 7)) << 4)) =
-                        widen_e4m3x8<E>(other ? x[i].x : x[i].z, other ? x[i].y : x[i].w);
-                }
-                done += kUnit;
-                if (done == kSteps) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (!is_v) mbar_arrive(bar(W_KEYS + wk % kKeyRing));
-                        mbar_arrive(bar(is_v ? W_VFULL : W_KFULL));
-                    }
-                    wk += !is_v, wv += is_v;
+                        widen_e4m3x8<E>(other ? x[e].x : x[e].z, other ? x[e].y : x[e].w);
                 }
             }
-            if (step == kSteps) {  // what is copied next
-                step = 0;
-                pool = nullptr;
-                if (it.j0 < it.j1 && ck - cv < 2) {
-                    row[1] = row[0], head[1] = head[0], ks[1] = ks[0], vs[1] = vs[0];
-                    const int pos = j * BN + w * 32 + lane;
-                    row[0] = -1, head[0] = it.g;
-                    ks[0] = vs[0] = 1.f;  // where no row sees the key: numbers that do no harm
-                    if (pos >= it.n_lo && pos < it.n_end) {
-                        if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks)) {
-                            const int off = p.geom.offset_of(pos);
-                            row[0] = id * p.geom.block_size + off;
-                            const size_t at = (static_cast<size_t>(id) * p.Hkv + it.g) * p.geom.block_size + off;
-                            ks[0] = __ldcg(p.k_scale + at);
-                            vs[0] = __ldcg(p.v_scale + at);
-                        } else {
-                            bad_seg[n & (kBadRing - 1)] = n + 1;
-                            raise_err(p.err, PA_DEVERR_TABLE);
-                        }
-                    }
-                    __syncwarp();
-                    from = row[0], from_head = head[0];
-                    pool = static_cast<const unsigned char *>(p.k_cache);
-                    ++ck;
-                    if (++j >= it.j1) {
-                        ok = read_seg(++n, it);
-                        j = it.j0;
-                        if (!ok) it.j1 = it.j0;
-                    }
-                    fetch();
-                } else if (cv < ck) {
-                    const bool before = ck == cv + 2;
-                    from = before ? row[1] : row[0], from_head = before ? head[1] : head[0];
-                    pool = static_cast<const unsigned char *>(p.v_cache);
-                    ++cv;
-                }
+            if (!ok) break;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (!is_v) mbar_arrive(bar(W_KEYS + wk % kKeyRing));
+                mbar_arrive(bar(is_v ? W_VFULL : W_KFULL));
             }
-            if (pool) {
-                const unsigned char *base = pool + from_head * HD + piece * 16;
-                const uint32_t dst = mine + (u % kUnits) * (kUnit * 2048);
-#pragma unroll
-                for (int i = 0; i < kUnit; ++i) {
-                    const int r = __shfl_sync(kFull, from, (step + i) * kStepKeys + key_of_lane);
-                    cp_async16(dst + i * 2048, base + static_cast<uint64_t>(static_cast<uint32_t>(max(r, 0))) * stride, r < 0 ? 0 : 16);
-                }
-            }
-            step += kUnit;
-            cp_async_commit();
+            wk += !is_v, wv += is_v;
         }
-        cp_async_wait<0>();
         if (!ok && lane == 0) give_up(p.err, abort_flag);
         __syncwarp();
     } else {
@@ -460,7 +528,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                 }
                 if (!(ok = short_wait(bar(W_KEYS + tile % kKeyRing), (tile / kKeyRing) & 1, abort_flag))) break;
                 const float4 *ks4 = reinterpret_cast<const float4 *>(smem + Lay::OFF_KEYS) + (tile % kKeyRing) * 3 * (BN / 4),
-                             *lv4 = ks4 + BN / 4, *iv4 = lv4 + BN / 4;
+                             *v4 = ks4 + BN / 4, *iv4 = v4 + BN / 4;
                 tc_fence_after();
                 uint32_t sv[128];
 #pragma unroll
@@ -473,12 +541,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free);
                 const int n0 = j * BN;
-                // x = log2 of the weight before the reference
+                // x = log2 of the weight (fp16: times its value's scale) before the reference
 #pragma unroll
                 for (int e = 0; e < 128; e += 4) {
-                    const float4 k4 = ks4[e >> 2], l4 = lv4[e >> 2];
-                    const uint64_t a = f2_fma(u2_pack(sv[e], sv[e + 1]), f2_pack(k4.x, k4.y), f2_pack(l4.x, l4.y)),
-                                   b = f2_fma(u2_pack(sv[e + 2], sv[e + 3]), f2_pack(k4.z, k4.w), f2_pack(l4.z, l4.w));
+                    const float4 k4 = ks4[e >> 2];
+                    uint64_t a = f2_mul(u2_pack(sv[e], sv[e + 1]), f2_pack(k4.x, k4.y)), b = f2_mul(u2_pack(sv[e + 2], sv[e + 3]), f2_pack(k4.z, k4.w));
+                    if constexpr (!E::kIsBf16) {
+                        const float4 l4 = v4[e >> 2];
+                        a = f2_add(a, f2_pack(l4.x, l4.y)), b = f2_add(b, f2_pack(l4.z, l4.w));
+                    }
                     sv[e] = __float_as_uint(f2_lo(a)), sv[e + 1] = __float_as_uint(f2_hi(a));
                     sv[e + 2] = __float_as_uint(f2_lo(b)), sv[e + 3] = __float_as_uint(f2_hi(b));
                 }
@@ -505,14 +576,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                 uint32_t pk[64];
 #pragma unroll
                 for (int e = 0; e < 128; e += 4) {
-                    const float4 i4 = iv4[e >> 2];
+                    const float4 i4 = E::kIsBf16 ? v4[e >> 2] : iv4[e >> 2];
                     const uint64_t xa = f2_add(u2_pack(sv[e], sv[e + 1]), nm2), xb = f2_add(u2_pack(sv[e + 2], sv[e + 3]), nm2);
                     const float p0 = fast_exp2(f2_lo(xa)), p1 = fast_exp2(f2_hi(xa)), p2 = fast_exp2(f2_lo(xb)), p3 = fast_exp2(f2_hi(xb));
-                    l2 = f2_fma(f2_pack(p0, p1), f2_pack(i4.x, i4.y), l2);
-                    l2 = f2_fma(f2_pack(p2, p3), f2_pack(i4.z, i4.w), l2);
+                    uint64_t wa = f2_pack(p0, p1), wb = f2_pack(p2, p3);
+                    if constexpr (E::kIsBf16) {
+                        l2 = f2_add(f2_add(l2, wa), wb);
+                        wa = f2_mul(wa, f2_pack(i4.x, i4.y)), wb = f2_mul(wb, f2_pack(i4.z, i4.w));
+                    } else {
+                        l2 = f2_fma(wa, f2_pack(i4.x, i4.y), l2);
+                        l2 = f2_fma(wb, f2_pack(i4.z, i4.w), l2);
+                    }
                     // P is rounded to the storage type (the tensor cores' operand), the sum is not
-                    pk[e >> 1] = E::pack2(p0, p1);
-                    pk[(e >> 1) + 1] = E::pack2(p2, p3);
+                    pk[e >> 1] = E::pack2(f2_lo(wa), f2_hi(wa));
+                    pk[(e >> 1) + 1] = E::pack2(f2_lo(wb), f2_hi(wb));
                 }
                 l = l * f + (f2_lo(l2) + f2_hi(l2));
                 if (t > 0) {  // the previous tile's PV has consumed P and completed O
@@ -641,9 +718,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
     }
 }
 
-template <class E, int HD>
+template <class E, int HD, bool kGather>
 cudaError_t launch_wide(const WideParams &prm, cudaStream_t stream) {
-    auto kern = chunk_q8_wide_kernel<E, HD>;
+    auto kern = chunk_q8_wide_kernel<E, HD, kGather>;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -691,8 +768,21 @@ cudaError_t launch_chunk_q8_wide(const chunk::ChunkParams &common, const ChunkQ8
     // a warp's 32 output rows as one box, where they are whole tokens
     prm.store_tok = 32 % prm.G == 0 && BM % prm.G == 0 ? 32 / prm.G : 0;
     if (prm.store_tok > 0 && !encode(&prm.tm_o, a.out, prm.store_tok)) return cudaErrorInvalidValue;
-    if (a.dtype == PA_BF16) return a.D == 64 ? launch_wide<BF16, 64>(prm, stream) : launch_wide<BF16, 128>(prm, stream);
-    return a.D == 64 ? launch_wide<F16, 64>(prm, stream) : launch_wide<F16, 128>(prm, stream);
+    const bool gather = prm.box_rows < 8;
+    if (prm.box_rows > kHalfKeys) prm.box_rows = kHalfKeys;
+    const long long rows = static_cast<long long>(a.num_blocks) * a.block_size;
+    if (!gather && (!encode_rows_e4m3(&prm.tm_k, a.k_cache, a.Hkv, a.D, rows, prm.box_rows, false) ||
+                    !encode_rows_e4m3(&prm.tm_v, a.v_cache, a.Hkv, a.D, rows, prm.box_rows, false)))
+        return cudaErrorInvalidValue;
+    auto go = [&](auto e, auto hd) {
+        using E = decltype(e);
+        constexpr int HD = decltype(hd)::value;
+        return gather ? launch_wide<E, HD, true>(prm, stream) : launch_wide<E, HD, false>(prm, stream);
+    };
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    if (a.dtype == PA_BF16) return a.D == 64 ? go(BF16{}, I64{}) : go(BF16{}, I128{});
+    return a.D == 64 ? go(F16{}, I64{}) : go(F16{}, I128{});
 }
 
 }  // namespace pa

@@ -53,10 +53,11 @@ static bool encode_elements_3d(CUtensorMap *m, const void *base, CUtensorMapData
                               heads, hd, rows, box_heads, box_rows, box_cols, swizzle, fill);
 }
 
-// of e4m3 elements, whole rows of 64 or 128 bytes of one head, swizzled over as many bytes
-[[maybe_unused]] static bool encode_rows_e4m3(CUtensorMap *m, const void *base, int heads, int hd, long long rows, int box_rows) {
+// of e4m3 elements, whole rows of 64 or 128 bytes of one head, one after the other or swizzled over as many bytes
+[[maybe_unused]] static bool encode_rows_e4m3(CUtensorMap *m, const void *base, int heads, int hd, long long rows, int box_rows,
+                                              bool swizzled) {
     return encode_elements_3d(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, heads, hd, rows, 1, box_rows, hd,
-                              hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
