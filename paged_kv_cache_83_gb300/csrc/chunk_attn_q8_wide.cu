@@ -512,8 +512,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
             }
             const int rows = min(tok, p.tt) * p.G;
             const bool live = quarter * 32 < rows;  // this warp holds rows
-            const int pos = it.p0 + h * p.tt + row_tok;
-            const int lim = r < rows ? pos + 1 : 0;  // the keys this row sees: [lo, lim)
+            // The keys this row sees: [lo, lim). Rows without a token take the last one's, and nobody reads what comes of them:
+            // with bounds of their own their warp would mask every tile (66 rows of 128: 92 us where 128 rows take 68).
+            const int pos = it.p0 + h * p.tt + min(row_tok, tok - 1), lim = pos + 1;
             const int lo = p.window > 0 ? pos - p.window + 1 : 0;
             float m_use = -INFINITY, l = 0.f;
 #pragma unroll 1
