@@ -17,11 +17,13 @@
 // 4 below the largest x of the first tile and moves when some x exceeds it by more than 8: a w is at most 256,
 // below e4m3's 448, and what is smaller than 2^-16 (2^-21) beside a largest w of 16 counts for nothing.
 //
-// Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. The loads run ahead in rings of tiles; two streams of softmax
-// warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a
-// segment. With more than 32 query rows a kv head an item is at most 64 of them, and the streams take half of the columns
-// each, of every key tile: a long chunk is many items, whose keys come from L2, and is bound by the softmax (exponentials
-// and conversions).
+// Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. 256 single tokens over 100-4096 keys, 16/8 heads x 128,
+// block 256: 209-221 us by box, 5.3-5.6 TB/s, 0.80-0.84 of a copy. The loads run ahead in rings of tiles; two streams of softmax
+// warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a segment. On
+// the way to that: 305 us before the code of all roles stayed in the instruction cache, the scales came by cp.async and table
+// entries a tile ahead (229), 224 with packed arithmetic on the scores and three K tiles a stream, 212 with a meeting of the
+// streams at a segment's start. With more than 32 query rows a kv head the streams take half of the columns each, of every key
+// tile; chunks of more than 64 go to chunk_attn_q8_wide.cu.
 //
 //   warp 3      scheduler, as in chunk_attn.cu; splits each segment's queries into pieces
 //   warp 0      producer: K and V tiles of the streams in turn, the scales with the K tile
@@ -929,6 +931,8 @@ cudaError_t launch_chunk_q8(const ChunkQ8Args &x, cudaStream_t stream) {
     prm.geom.block_size = a.block_size;
     prm.geom.shift = log2_if_pow2(a.block_size);
     prm.scale_log2 = a.scale * kLog2e;
+    // Items of 256 rows from 65 rows a kv head on. 8 sequences of 6000 keys, 16/8 heads x 128, bf16: 34 rows 51 us here, 64 rows
+    // 63.5 (there 65.5), 66 rows 65.5 there; at 64 rows and head dim 64 (32 sequences of 4000) 65.5 here, 71.6 there.
     if (rows > 64) return launch_chunk_q8_wide(prm, x, stream);
     const long long krows = static_cast<long long>(a.num_blocks) * a.block_size;
     if (!gather && (!encode_rows_e4m3(&prm.tm_k, a.k_cache, a.Hkv, a.D, krows, R, true) ||

@@ -7,14 +7,17 @@
 //
 // The cache's e4m3 rows are widened to the storage type, exactly, on their way to shared memory, once for the 256 query rows of
 // an item, and queries and weights stay whole operands. (As sums of e4m3 pieces beside rows that are used as they lie, the
-// weights cost the softmax three conversions each: that form, of 64 rows an item, took 955 us where this one takes 550: two
+// weights cost the softmax three conversions each: that form, of 64 rows an item, took 955 us where this one takes 533: two
 // chunks of 2k tokens at contexts of 12-16k, 16/8 heads x 128, bf16.) A producer brings halves of tiles by TMA and four warps
-// widen them into the swizzled tile that the matrix instructions read (loaders that copied for themselves: 675 us). One buffer
-// for K and one for V suffice, since a tile's K is wanted a whole softmax before its V.
+// widen them into the swizzled tile that the matrix instructions read (loaders that copied for themselves: 675 us). There is
+// room for one buffer of K and one of V; a tile's K is wanted a whole softmax before its V.
 //
-// Bound by the softmax warps, as there: at that shape 0.78 PFLOP/s, 0.41 of the burst peak, and 5500 clocks a key tile of both
-// row tiles. Against the 16-bit cache's kernel they read two numbers a key from shared memory and multiply twice more a
-// weight; with log2 vs in the exponent and 1 / vs in the sum for bf16 as well it was 587 us.
+// Bound by shared memory and by the softmax and loader warps together: at that shape 0.80 PFLOP/s, 0.42 of the burst peak, a key
+// tile of both row tiles every 5250 clocks, of which the operands, P, the rows' way through the stage and the numbers of the keys
+// keep shared memory busy for some 4000. Without the widening it would be 468 us, without the numbers of the keys 516, without
+// both 382. Measured and not kept: P in the columns of its S, the next QK behind this PV, and two buffers of K and V
+// in P's place (584); sixteen softmax warps, half of a row's keys each (568, registers spill); V widened with its scales
+// (550); 184 registers for the softmax (537); for bf16, too, log2 vs in the exponent and 1 / vs in the sum (587).
 //
 //   warp 3        scheduler, as in chunk_attn.cu; brings the queries of a segment by TMA
 //   warp 0        producer: halves of K and V tiles as they lie in the cache, and the scales of their keys

