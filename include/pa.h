@@ -154,7 +154,7 @@ pa_status pa_rope_store_kv(void *q_out, int64_t q_out_stride, const void *q, int
  *           then rotated as in pa_rope_store_kv (rot_dim == 0: not)
  *       q_out[t] = y of q[t];  k_cache row s = y of k[t];  v_cache row s = v[t]
  *   with cache_dtype == PA_E4M3 each row z of keys (y) and values (v) of a slot and kv head has a scale of its own:
- *       scale = max(max |z| / 448, 2^-90),   cache row = z / scale, rounded to the nearest e4m3 (ties to even)
+ *       scale = max(max |z| / 448, 2^-90),   cache row = z * (1 / scale), rounded to the nearest e4m3 (ties to even)
  *   which reads back as scale * cache row. A row that holds a NaN or an infinity reads back as NaN throughout (its
  *   scale is NaN or infinite).
  *
@@ -420,20 +420,26 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
  *   K_j = k_scale_j * (k_cache row j),  V_j = v_scale_j * (v_cache row j) of the sequence and kv head, each with its own scale;
  *   everything else as pa_chunk_attn.
  *
- * The e4m3 rows are operands of the tensor cores as they lie there; queries and softmax weights meet them as sums of e4m3 numbers.
- * Scores, references, sums and accumulators are fp32. A query's element is exact where its magnitude is above 2^-14 of the
- * largest of its row, below that to 2^-24 of the largest; a weight (times its value's scale) is rounded to within 2^-8 (bf16) or 2^-11 (fp16) of itself, and
- * to within 2^-19 (2^-24) of the largest that was seen when the first keys of a piece were; the output is rounded once.
+ * Scores, references, sums and accumulators are fp32; the output is rounded once. What is rounded to fewer bits before:
+ *   up to 64 query rows a kv head (tokens * Hq / Hkv) the e4m3 rows are operands of the tensor cores as they lie there, and
+ *     queries and softmax weights meet them as sums of e4m3 numbers. A query's element is exact where its magnitude is above
+ *     2^-14 of the largest of its row, below that to 2^-24 of the largest; a weight (times its value's scale) is rounded to
+ *     within 2^-8 (bf16) or 2^-11 (fp16) of itself, and to within 2^-19 (2^-24) of the largest that was seen when the first
+ *     keys of a piece were;
+ *   beyond that the rows are widened to the storage type, exactly, and a weight times its value's scale is rounded to it.
  *
- * k_cache, v_cache  e4m3 pools [num_blocks, block_size, Hkv, D].
- * k_scale, v_scale  fp32 [num_blocks, Hkv, block_size], 16-byte aligned. Positive; k_scale from 2^-126, v_scale from 2^-90 to 2^60. A
- *               NaN or an infinity (a row that held one) makes the output of what sees it NaN.
+ * k_cache, v_cache  e4m3 pools [num_blocks, block_size, Hkv, D]. The pattern of a NaN counts as one in rows whose scale is NaN,
+ *               as pa_norm_rope_store_kv writes them; with a finite scale it is not looked for.
+ * k_scale, v_scale  fp32 [num_blocks, Hkv, block_size], 16-byte aligned. Positive; k_scale from 2^-126, v_scale from 2^-90 to
+ *               2^60, those of a sequence and kv head at most 2^100 apart; scale * k_scale * 369 finite. A NaN or an infinity
+ *               (a row that held one) makes the output of what sees it NaN, and may make that of the call's other rows of that
+ *               sequence and kv head NaN too (cf. pa_chunk_attn: keys that some rows see and others do not).
  * q, out, dtype fp16 or bf16; out may be q itself.
- * max_seqlen_q  chooses the kernel for the whole call: up to 16 query rows a kv head (tokens * Hq / Hkv), up to 32, or
- *               items of 64 of them.
- * workspace     device scratch of at least pa_chunk_attn_q8_workspace_size(S, Hq, Hkv, D) bytes (10 MB on a GB300 at D = 128, 5 MB at
- *               64). Its contents on entry do not matter; calls that share a workspace must not overlap on the GPU.
- * A bad table entry leaves zero rows for up to 64 / (Hq / Hkv) tokens (cf. pa_chunk_attn). All else as pa_chunk_attn.
+ * max_seqlen_q  chooses the kernel for the whole call: up to 16 query rows a kv head, up to 32, up to 64, or items of 256.
+ * workspace     device scratch of at least pa_chunk_attn_q8_workspace_size(S, Hq, Hkv, D) bytes (41 MB on a GB300 at D = 128,
+ *               21 MB at 64). Its contents on entry do not matter; calls that share a workspace must not overlap on the GPU.
+ * A bad table entry leaves zero rows for up to 64 / (Hq / Hkv) tokens, with items of 256 rows 256 / (Hq / Hkv) (cf. pa_chunk_attn).
+ * All else as pa_chunk_attn.
  */
 size_t pa_chunk_attn_q8_workspace_size(int S, int Hq, int Hkv, int D);
 pa_status pa_chunk_attn_q8(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -506,8 +512,8 @@ pa_status pa_sample(int32_t *tokens, const void *logits, int64_t row_stride, int
  * accepted      int32 [S], written; 0 for a sequence without rows.
  * tokens        int32 [total_q], the chunks.
  * probs, draft_probs  [total_q, V] fp16, bf16 or fp32 (`dtype`, of both), rows probs_stride and draft_stride elements apart, at
- *               least V; any alignment that the element type has. A row's numbers sum to about 1; NaN and negative ones count as
- *               0, larger ones as 1 (in the test: a p that is NaN refuses, as does a q). The last row of a sequence in
+ *               least V; any alignment that the element type has. A row's numbers sum to about 1; a weight r_j that is NaN or
+ *               negative counts as 0, a larger one than 1 as 1 (in the test: a p that is NaN refuses, as does a q). The last row of a sequence in
  *               draft_probs is not read, nor is any row behind the one that decides.
  * cu_seqlens_q  int32 [S+1], non-decreasing, from >= 0 to <= total_q; a span outside that sets PA_DEVERR_LENGTH, and the
  *               sequence's accepted is 0 and its rows are left as they were.

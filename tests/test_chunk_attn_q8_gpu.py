@@ -348,3 +348,57 @@ def test_against_the_16_bit_cache():
     pa.pa_chunk_attn(other, c.q, kc.to(c.dt), vc.to(c.dt), c.bt, c.cu, c.ctx, c.max_q, c.scale, workspace=ws)
     # each is within 2^-8 of the norm
     assert float((other.double() - c.out.double()).norm()) <= 2.0 ** -7 * float(c.out.double().norm())
+
+
+# chunks of more than 64 query rows a kv head: items of two row tiles of 128, loaders that widen the cache's rows
+
+
+@pytest.mark.parametrize("D,bs,dt", [(64, 16, "bf16"), (128, 4, "bf16"), (128, 256, "f16")])
+def test_wide_many_short_sequences(D, bs, dt):
+    # segments of one key tile, some without rows in the second row tile, and sequences without new tokens between them
+    r = np.random.default_rng(1)
+    lens = [(int(a), int(a + b)) for a, b in zip(r.integers(0, 70, 400), r.integers(0, 60, 400))]
+    assert int(Case(lens, 4, 2, D, bs, dt, max_q=70, pad=1, lead=1).check().err) == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,q", [(1, 1, 65), (1, 1, 127), (1, 1, 128), (1, 1, 129), (1, 1, 255), (1, 1, 256), (1, 1, 257), (3, 1, 43),
+                                      (3, 1, 85), (5, 1, 26), (6, 1, 22), (7, 1, 18), (7, 1, 19), (7, 1, 37), (8, 1, 16), (8, 1, 33)])
+@pytest.mark.parametrize("D,dt", [(64, "f16"), (128, "bf16")])
+def test_wide_rows(Hq, Hkv, q, D, dt):
+    Case([(q, q), (1, 1), (q - 1, 127 + q), (q, 1500)], Hq, Hkv, D, 16, dt).check()
+
+
+@pytest.mark.parametrize("D,dt", [(64, "bf16"), (128, "bf16"), (128, "f16")])
+def test_wide_scales_of_every_size(D, dt):
+    Case([(100, 700), (40, 2000)], 4, 2, D, 16, dt, sizes=4.0).check()
+    c = Case([(100, 300)], 4, 2, D, 16, dt)
+    if dt == "bf16":  # (fp16 outputs hold no such numbers)
+        c.vs *= 2.0 ** 40
+        c.check()
+        c.vs *= 2.0 ** -40
+    # rows of zeros have the least scale and take their weight
+    c.vc.view(torch.uint8)[int(c.bt[0, 0])] = 0
+    c.vs[int(c.bt[0, 0])] = 2.0 ** -90
+    c.check()
+
+
+def test_wide_captured_with_other_lengths_at_replay():
+    c = Case([(80, 900), (1, 2000), (70, 300)], 4, 2, 128, 64, "bf16")
+    c.run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run()
+    c.lens = [(1, 700), (70, 1999), (80, 280)]
+    c.cu.copy_(torch.tensor([0, 1, 71, 151], dtype=torch.int32))
+    c.ctx.copy_(torch.tensor([n for _, n in c.lens], dtype=torch.int32))
+    for _ in range(2):
+        graph.replay()
+    c.check(run=False)
+
+
+@pytest.mark.parametrize("D,dt", [(64, "f16"), (128, "bf16")])
+def test_wide_lengths_outside_the_contract(D, dt):
+    c = Case([(200, 500), (100, 400), (90, 300), (130, 600)], 4, 2, D, 16, dt)
+    c.ctx[0], c.ctx[2] = 199, 1 << 20
+    c.check(zero=(0, 2))
+    assert int(c.err) == pa.PA_DEVERR_LENGTH
