@@ -12,7 +12,7 @@
 // Bound by HBM where there are many sequences (one row of p and one of q each), by the chain of dependent loads where there are
 // few. So a sequence belongs to a cluster of CTAs: each finds the number of accepted drafts by itself (a few
 // gathered numbers), sums the weights of its slice of the one row that matters, and all learn each other's sums through
-// distributed shared memory; the CTA whose slice holds the token reads one warp's twelfth of it again, from L2. One launch, no
+// distributed shared memory; the CTA whose slice holds the token reads one warp's part of it again, from L2. One launch, no
 // workspace. 256 sequences, 151,936 fp32 numbers in p and in q: 51 us, 0.71 of a copy (one CTA a sequence: 78 us); one
 // sequence with a draft of four tokens and a drafter without probabilities, bf16: 7.0 us (8.9 in smaller clusters).
 #include "pa_internal.h"
@@ -21,10 +21,9 @@ namespace pa {
 
 namespace {
 
-constexpr int kVerifyThreads = 384, kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyBlocks = 4;  // of an SM
+constexpr int kVerifySm = 1536;  // threads of an SM, in CTAs of 384 or 512
+constexpr int kMostCtas = 8;     // of a sequence: the portable cluster
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kResBits = 44;  // weights are multiples of 2^-44
 
 struct F32 {
     using T = float;
@@ -104,11 +103,11 @@ __device__ __forceinline__ void weights_at(const Drawn<typename E::T> &d, int i,
         if (i + e == d.bare) r[e] = 0.f;
 }
 
-template <class E>
-__global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(const __grid_constant__ VerifyParams p) {
+template <class E, int kThreads>
+__global__ void __launch_bounds__(kThreads, kVerifySm / kThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
     using T = typename E::T;
-    constexpr int kN = 16 / sizeof(T);
-    __shared__ long long warp_sum[2][kVerifyWarps], cta_sum[2];
+    constexpr int kN = 16 / sizeof(T), kWarps = kThreads / 32;
+    __shared__ long long warp_sum[2][kWarps], cta_sum[2];
     __shared__ int taken, ended;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t rank, ctas;
@@ -165,13 +164,13 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
     d.shift = static_cast<int>(reinterpret_cast<uintptr_t>(d.p) % 16 / sizeof(T));
     d.same = d.diff && reinterpret_cast<uintptr_t>(d.q) % 16 == reinterpret_cast<uintptr_t>(d.p) % 16;
     if (rank == 0) {
-        for (int r = tid; r <= n; r += kVerifyThreads)
+        for (int r = tid; r <= n; r += kThreads)
             if (r != a) p.next_tokens[a0 + r] = r < a ? p.tokens[a0 + r + 1] : -1;
         if (tid == 0) p.accepted[s] = a;
     }
     const float uf = p.u[a1 - 1];
     const uint32_t u31 = uf > 0.f ? uf < 1.f ? static_cast<uint32_t>(uf * 0x1p31f) : 0x7fffffffu : 0u;
-    const int first = (static_cast<int>(rank) * kVerifyWarps + warp) * p.slice - d.shift;  // of this warp's slice
+    const int first = (static_cast<int>(rank) * kWarps + warp) * p.slice - d.shift;  // of this warp's slice
     for (int attempt = 0;; ++attempt) {
         // ---- the sums of the slices
         int hi = 0, lo = 0;
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
         if (lane == 0) warp_sum[attempt][warp] = sum;
         __syncthreads();
         if (warp == 0) {
-            long long v = lane < kVerifyWarps ? warp_sum[attempt][lane] : 0;
+            long long v = lane < kWarps ? warp_sum[attempt][lane] : 0;
 #pragma unroll
             for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
             if (lane == 0) cta_sum[attempt] = v;
@@ -225,10 +224,10 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
             long long left = border - before;  // in this CTA's slice
             int w = 0;
             while (left >= warp_sum[attempt][w]) left -= warp_sum[attempt][w++];
-            const int begin = (static_cast<int>(rank) * kVerifyWarps + w) * p.slice - d.shift;
+            const int begin = (static_cast<int>(rank) * kWarps + w) * p.slice - d.shift;
             // the block takes the warp's slice, a few numbers a thread
-            __shared__ long long step_sum[kVerifyWarps];
-            for (int at = begin; at < begin + p.slice; at += kVerifyThreads * kN) {
+            __shared__ long long step_sum[kWarps];
+            for (int at = begin; at < begin + p.slice; at += kThreads * kN) {
                 const int i = at + tid * kN;
                 float r[kN];
                 long long v = 0;
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
                 if (lane == 31) step_sum[warp] = upto;
                 __syncthreads();
                 long long ahead = upto - v, step = 0;
-                for (int k = 0; k < kVerifyWarps; ++k) {
+                for (int k = 0; k < kWarps; ++k) {
                     if (k < warp) ahead += step_sum[k];
                     step += step_sum[k];
                 }
@@ -276,16 +275,34 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <class E>
-cudaError_t launch_verify_typed(const VerifyParams &in, cudaStream_t stream) {
-    VerifyParams prm = in;
+// Clusters of 1 .. kMostCtas CTAs that are on the SMs at once (asked for once for each kernel and device)
+template <class E, int kThreads>
+cudaError_t active_clusters(int dev, const int *&most) {
+    static int table[64][kMostCtas + 1];  // [0]: filled
+    if (!table[dev][0]) {
+        for (int ctas = 1; ctas <= kMostCtas; ++ctas) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = ctas;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg{};
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(ctas);
+            cfg.blockDim = dim3(kThreads);
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&table[dev][ctas], verify_kernel<E, kThreads>, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        table[dev][0] = 1;
+    }
+    most = table[dev];
+    return cudaSuccess;
+}
+
+template <class E, int kThreads>
+cudaError_t launch_verify_as(VerifyParams &prm, int ctas, cudaStream_t stream) {
     constexpr int kN = 16 / sizeof(typename E::T);
-    // CTAs of a sequence: slices of at least 4096 numbers, eight CTAs (the portable cluster) at most, and no more than leave
-    // all CTAs of the call on the SMs at once: each begins and ends with a chain of dependent loads and barriers.
-    int ctas = 1;
-    const long long room = static_cast<long long>(device_sm_count()) * kVerifyBlocks;
-    while (ctas < 8 && prm.V > 4096 * ctas && 2ll * ctas * prm.S <= room) ctas *= 2;
-    const int per = 32 * kN, parts = ctas * kVerifyWarps;
+    const int per = 32 * kN, parts = ctas * (kThreads / 32);
     prm.slice = ((prm.V + kN + parts - 1) / parts + per - 1) / per * per;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -298,8 +315,32 @@ cudaError_t launch_verify_typed(const VerifyParams &in, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(static_cast<unsigned>(prm.S) * ctas);
-    cfg.blockDim = dim3(kVerifyThreads);
-    return cudaLaunchKernelEx(&cfg, verify_kernel<E>, prm);
+    cfg.blockDim = dim3(kThreads);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<E, kThreads>, prm);
+}
+
+template <class E>
+cudaError_t launch_verify_typed(const VerifyParams &in, cudaStream_t stream) {
+    VerifyParams prm = in;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const int *most_384, *most_512;
+    if ((e = active_clusters<E, 384>(dev, most_384)) != cudaSuccess || (e = active_clusters<E, 512>(dev, most_512)) != cudaSuccess) return e;
+    // CTAs of a sequence: slices of at least 4096 numbers, and no more CTAs than are on the SMs at once: each begins and ends
+    // with a chain of dependent loads and barriers. Of the two sizes of CTA the one that leaves more threads (p and q in fp32, us,
+    // powers of two of 384 threads before, this rule after: 4 sequences 18.4, 16.6; 76: 36.0, 26.7; 152: 51.0, 38.8; 256: 54.9,
+    // 54.8; 400: 89.1, 78.0).
+    const auto ctas_of = [&](const int *most) {
+        int ctas = 1;
+        for (int c = 2; c <= kMostCtas; ++c)
+            if (prm.V > 4096 * (c - 1) && prm.S <= most[c]) ctas = c;
+        return ctas;
+    };
+    const int c384 = ctas_of(most_384), c512 = ctas_of(most_512);
+    return prm.S <= most_512[c512] && 512 * c512 > 384 * c384 ? launch_verify_as<E, 512>(prm, c512, stream)
+                                                              : launch_verify_as<E, 384>(prm, c384, stream);
 }
 
 }  // namespace
