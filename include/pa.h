@@ -1,6 +1,7 @@
 /*
- * pa.h: C ABI of the paged KV-cache hot path (store, paged decode, varlen prefill) for one
- * NVIDIA GB300 (sm_103a).
+ * pa.h: C ABI of the paged KV-cache hot path (store, paged decode, varlen prefill, and the steps around
+ * them: rotation and norms, chunks of new tokens over a 16- or 8-bit cache, sampling, verification) for
+ * one NVIDIA GB300 (sm_103a).
  *
  * The three operations are the attention layer's GPU work in the engines that the
  * "nano-vLLM Part 4" page (section 3, the prefill/decode table and the per-rank tensor list)
@@ -14,7 +15,8 @@
  *   buffer. The library allocates nothing that outlives a call. Nothing is freed by the library.
  * - Every call is asynchronous on `stream`; it returns after the launch. Errors that the host
  *   can see are returned before anything is launched, and nothing is written then.
- * - Element types: `pa_dtype` selects fp16 or bf16 for q, k, v, the pools and the output.
+ * - Element types: `pa_dtype` selects fp16 or bf16 for q, k, v, the pools and the output (8-bit
+ *   pools have calls of their own).
  *   Scores, softmax and accumulation run in fp32; the output is rounded once (to nearest even).
  * - Pools: `k_cache` and `v_cache` are each [num_blocks, block_size, Hkv, D], contiguous.
  *   Token slot `s` (0 <= s < num_blocks * block_size) is block `s / block_size`, offset

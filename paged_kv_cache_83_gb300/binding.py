@@ -25,7 +25,8 @@ PA_F16, PA_BF16, PA_F32, PA_E4M3 = 0, 1, 2, 3
 PA_DEVERR_SLOT, PA_DEVERR_TABLE, PA_DEVERR_LENGTH, PA_DEVERR_TIMEOUT, PA_DEVERR_POSITION, PA_DEVERR_ROW = 1, 2, 4, 8, 16, 32
 EXPORTS = ("pa_store_kv", "pa_rope_store_kv", "pa_decode_workspace_size", "pa_decode", "pa_store_decode",
            "pa_store_decode_host", "pa_store_decode_host_workspace_size", "pa_store_decode_host_layout",
-           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample", "pa_norm_rope_store_kv", "pa_verify", "pa_chunk_attn_q8",
+           "pa_prefill_varlen", "pa_chunk_attn", "pa_chunk_attn_workspace_size", "pa_sample",
+           "pa_norm_rope_store_kv", "pa_verify", "pa_chunk_attn_q8",
            "pa_chunk_attn_q8_workspace_size", "pa_decode_noalloc",
            "pa_decode_debug_tail_units", "pa_status_string", "pa_bm_create",
            "pa_bm_destroy", "pa_bm_allocate", "pa_bm_can_allocate", "pa_bm_append",

@@ -121,7 +121,7 @@ def build(verbose: bool = False, force: bool = False) -> Path:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
     if lacking:
-        warnings.warn(f"the binding's calls for rotation, chunk attention and sampling were not built: {lacking}", RuntimeWarning,
+        warnings.warn(f"the binding's calls for rotation, chunk attention, sampling and verification were not built: {lacking}", RuntimeWarning,
                       stacklevel=2)
     return LIB
 
