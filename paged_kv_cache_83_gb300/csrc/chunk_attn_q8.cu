@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
     // there: no block holds tensor memory while it waits for another grid, whose blocks on this SM may want some.
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), Lay::kTmem);
     if (tid == 0) p.recs[blockIdx.x].valid = 0;
-    plan_share(p, plan, share);
+    plan_share<kThreads, true>(p, plan, share);
     zero_bad_sequences<T, HD>(p);
     tc_fence_before();
     __syncthreads();
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
             }
             return true;
         };
-        const bool ok = walk_share(p, *share, [&](const SegInfo &it) {
+        const bool ok = walk_share<true>(p, *share, [&](const SegInfo &it) {
             if (!wait_for(bar(Lay::B_IEMPTY + (published & 3)), ((published >> 2) & 1) ^ 1, abort_flag)) return false;
             if (lane == 0) {
                 items[published & 3] = it;

@@ -115,16 +115,18 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     return v;
 }
 
-// A CTA's share [b0, b1) of the line of (item, key tile) pairs; N of them on P CTAs. Sequence s0, which
-// starts at place base0 of the line, holds b0.
+// A CTA's share [b0, b1) of the line of (item, key tile) pairs; N of them on P CTAs. Sequence s0 (by head: of kv head g0), which
+// starts at place base0 of the line, holds b0. The line goes by sequence, kv head, item; or by head: kv head, sequence, item.
+// By head, CTAs far apart on the line read the heads of one block at about the same time, by sequence one CTA does, head
+// after head, each time 128 or 256 bytes of a row of the pool.
 struct Share {
     long long N, P, b0, b1, base0;
-    int s0;
+    int s0, g0;
 };
 
 // Every thread of the block (kN of them) calls this; sm: kN / 32 words of shared memory, the result is in *out after the
 // next __syncthreads (in shared memory too: only the scheduler reads it).
-template <int kN = kThreads>
+template <int kN = kThreads, bool kByHead = false>
 __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, Share *out) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kW = kN / 32;
@@ -148,7 +150,7 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
         }
         return total;
     };
-    auto tiles_of = [&](int s) { return s < p.S ? head_tiles(p, seq_shape(p, s)) * p.Hkv : 0; };
+    auto tiles_of = [&](int s) { return s < p.S ? head_tiles(p, seq_shape(p, s)) * (kByHead ? 1 : p.Hkv) : 0; };
     Share r;
     long long v = tiles_of(tid), before;
     r.N = scan(v, before);
@@ -158,6 +160,8 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
         for (int s = tid + kN; s < p.S; s += kN) more += tiles_of(s);
         r.N += scan(more, unused);
     }
+    const long long line = r.N;  // by head: of one
+    if constexpr (kByHead) r.N *= p.Hkv;
     // CTAs 0 .. P - 1 take a share, at least one tile each (no piece of an item is then empty)
     r.P = min(static_cast<long long>(gridDim.x), r.N);
     const long long me = blockIdx.x;
@@ -173,18 +177,22 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
         }
     }
     if (r.b0 < r.b1) {
-        long long base = 0, total = first;
+        long long base = 0, total = first, place = r.b0;
+        int g0 = 0;
+        if constexpr (kByHead)
+            for (; place >= line; ++g0) place -= line;
         for (int sb = 0;; sb += kN) {
             if (sb > 0) {
                 v = tiles_of(sb + tid);
                 total = scan(v, before);
             }
-            if (base + before <= r.b0 && r.b0 < base + before + v) {  // one thread of the block, once
+            if (base + before <= place && place < base + before + v) {  // one thread of the block, once
                 out->s0 = sb + tid;
-                out->base0 = base + before;
+                out->g0 = g0;
+                out->base0 = g0 * line + base + before;
             }
             base += total;
-            if (r.b0 < base) break;  // the same for every thread
+            if (place < base) break;  // the same for every thread
         }
     }
     if (tid == 0) out->N = r.N, out->P = r.P, out->b0 = r.b0, out->b1 = r.b1;
@@ -207,23 +215,25 @@ __device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p) {
 
 // One warp walks the CTA's share and hands each of its segments to publish (false: stop); the record
 // of an item that starts in this share and ends in another's goes to the joining kernel.
-template <class F>
+template <bool kByHead = false, class F>
 __device__ __forceinline__ bool walk_share(const ChunkParams &p, const Share sh, F publish) {
     const int lane = threadIdx.x & 31;
-    int s = sh.s0;
+    int s = sh.s0, g = sh.g0;
     long long at = sh.b0, off = sh.b0 - sh.base0;  // places on the line, and in the sequence
     while (at < sh.b1) {
         const SeqShape q = seq_shape(p, s);
         const long long per_head = head_tiles(p, q);
-        // order within a sequence: kv head, then item: a CTA's next item reads the same keys
-        int g = per_head > 0 ? 0 : p.Hkv;
-        while (off > 0 && off >= per_head) off -= per_head, ++g;
+        if constexpr (!kByHead) {
+            // order within a sequence: kv head, then item: a CTA's next item reads the same keys
+            g = per_head > 0 ? 0 : p.Hkv;
+            while (off > 0 && off >= per_head) off -= per_head, ++g;
+        }
         long long in_head = off;
         int i = 0;
-        if (g < p.Hkv)
+        if (g < p.Hkv && (!kByHead || per_head > 0))
             for (int n; in_head >= (n = item_tiles(p, q, i)); ++i) in_head -= n;
-        for (; g < p.Hkv && at < sh.b1; ++g, i = 0)
-            for (; i * p.item_tok < q.ql && at < sh.b1; ++i) {
+        for (; g < p.Hkv && at < sh.b1; ++g, i = 0) {
+            for (; i * p.item_tok < q.ql && at < sh.b1 && (!kByHead || per_head > 0); ++i) {
                 const int n = item_tiles(p, q, i), t0 = i * p.item_tok;
                 const int first = static_cast<int>(in_head);
                 const int last = static_cast<int>(min(static_cast<long long>(n), first + (sh.b1 - at)));
@@ -246,8 +256,12 @@ __device__ __forceinline__ bool walk_share(const ChunkParams &p, const Share sh,
                 }
                 at += last - first;
             }
+            if constexpr (kByHead) break;  // the next sequence of this head
+        }
         ++s;
         off = 0;
+        if constexpr (kByHead)
+            if (s == p.S) s = 0, ++g;
     }
     return publish(SegInfo{});  // the end marker
 }
