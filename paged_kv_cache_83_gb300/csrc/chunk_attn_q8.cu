@@ -18,12 +18,14 @@
 // below e4m3's 448, and what is smaller than 2^-16 (2^-21) beside a largest w of 16 counts for nothing.
 //
 // Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. 256 single tokens over 100-4096 keys, 16/8 heads x 128,
-// block 256: 209-221 us by box, 5.3-5.6 TB/s, 0.80-0.84 of a copy. The loads run ahead in rings of tiles; two streams of softmax
+// block 256: 196-201 us by box, 5.9-6.0 TB/s, 0.88-0.90 of a copy. The loads run ahead in rings of tiles; two streams of softmax
 // warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a segment. On
 // the way to that: 305 us before the code of all roles stayed in the instruction cache, the scales came by cp.async and table
-// entries a tile ahead (229), 224 with packed arithmetic on the scores and three K tiles a stream, 212 with a meeting of the
-// streams at a segment's start. With more than 32 query rows a kv head the streams take half of the columns each, of every key
-// tile; chunks of more than 64 go to chunk_attn_q8_wide.cu.
+// entries a tile ahead (229), 224 with packed arithmetic on the scores and three K tiles a stream, 209 without a meeting of
+// the streams at a segment's start; on a box where that took 222, 201 with the line of work by head (see Share). A segment's end
+// costs about 1 us that the rings cover in part: one segment a CTA (19 sequences of 28k) reads 6.0-6.1 TB/s from cold caches.
+// With more than 32 query rows a kv head the streams take half of the columns each, of every key tile; chunks of more than 64
+// go to chunk_attn_q8_wide.cu.
 //
 //   warp 3      scheduler, as in chunk_attn.cu; splits each segment's queries into pieces
 //   warp 0      producer: K and V tiles of the streams in turn, the scales with the K tile
