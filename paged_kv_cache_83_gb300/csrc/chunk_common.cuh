@@ -179,8 +179,10 @@ __device__ __forceinline__ void plan_share(const ChunkParams &p, long long *sm, 
     if (r.b0 < r.b1) {
         long long base = 0, total = first, place = r.b0;
         int g0 = 0;
-        if constexpr (kByHead)
-            for (; place >= line; ++g0) place -= line;
+        if constexpr (kByHead) {  // r.N > 0: there is work, and so is on each head's line
+            g0 = r.N <= 0xffffffffll ? static_cast<uint32_t>(place) / static_cast<uint32_t>(line) : static_cast<int>(place / line);
+            place -= g0 * line;
+        }
         for (int sb = 0;; sb += kN) {
             if (sb > 0) {
                 v = tiles_of(sb + tid);

@@ -258,6 +258,14 @@ def test_many_sequences():
     Case(lens, 4, 2, 64, 16, "bf16").check()
 
 
+@pytest.mark.parametrize("Hq,Hkv,window", [(320, 320, 0), (96, 48, 0), (33, 11, 50)])
+def test_many_heads(Hq, Hkv, window):
+    # more heads than CTAs, and shares that begin and end inside of a head's sequences; some sequences without work
+    c = Case([(1, 300), (0, 40), (2, 129), (3, 60), (1, 5)], Hq, Hkv, 64, 16, "bf16", window=window, max_q=2)
+    c.check(zero=(3,))  # longer than max_seqlen_q
+    assert int(c.err) == pa.PA_DEVERR_LENGTH
+
+
 def test_repeated_calls_are_equal_and_out_may_be_q():
     c = Case([(2, 4000), (1, 100), (70, 900)], 16, 8, 128, 64, "bf16", seed=3)
     c.run()
