@@ -437,7 +437,7 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
  *               (a row that held one) makes the output of what sees it NaN, and may make that of the call's other rows of that
  *               sequence and kv head NaN too (cf. pa_chunk_attn: keys that some rows see and others do not).
  * q, out, dtype fp16 or bf16; out may be q itself.
- * max_seqlen_q  chooses the kernel for the whole call: up to 16 query rows a kv head, up to 32, up to 64, or items of 256.
+ * max_seqlen_q  chooses the kernel for the whole call: up to 8 query rows a kv head (bf16), 16, 32, 64, or items of 256.
  * workspace     device scratch of at least pa_chunk_attn_q8_workspace_size(S, Hq, Hkv, D) bytes (41 MB on a GB300 at D = 128,
  *               21 MB at 64). Its contents on entry do not matter; calls that share a workspace must not overlap on the GPU.
  * A bad table entry leaves zero rows for up to 64 / (Hq / Hkv) tokens, with items of 256 rows 256 / (Hq / Hkv) (cf. pa_chunk_attn).

@@ -18,12 +18,13 @@
 // below e4m3's 448, and what is smaller than 2^-16 (2^-21) beside a largest w of 16 counts for nothing.
 //
 // Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. 256 single tokens over 100-4096 keys, 16/8 heads x 128,
-// block 256: 196-201 us by box, 5.9-6.0 TB/s, 0.88-0.90 of a copy. The loads run ahead in rings of tiles; two streams of softmax
+// block 256: 190 us, 6.2 TB/s, 0.93 of a copy. The loads run ahead in rings of tiles; two streams of softmax
 // warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a segment. On
 // the way to that: 305 us before the code of all roles stayed in the instruction cache, the scales came by cp.async and table
 // entries a tile ahead (229), 224 with packed arithmetic on the scores and three K tiles a stream, 209 without a meeting of
-// the streams at a segment's start; on a box where that took 222, 201 with the line of work by head (see Share). A segment's end
-// costs about 1 us that the rings cover in part: one segment a CTA (19 sequences of 28k) reads 6.0-6.1 TB/s from cold caches.
+// the streams at a segment's start; on a box where that took 222, 201 with the line of work by head (see Share), 190 (another
+// box: 197 before) with a form of eight columns. A segment's end costs about 1 us that the rings cover in part: one segment a CTA
+// (19 sequences of 28k) reads 6.1 TB/s from cold caches, 16 segments of 1760 keys 5.8.
 // With more than 32 query rows a kv head the streams take half of the columns each, of every key tile; chunks of more than 64
 // go to chunk_attn_q8_wide.cu.
 //
@@ -59,7 +60,7 @@ struct LayQ8 {
     static constexpr int kQ = kNC * QP * HD;
     static constexpr int kP = BN * 128;                     // W^T: a 128-byte row a key, PP * NT of it used
     static constexpr int kTiles = HD == 128 ? 4 : 8;        // V tiles held; of K half as many more where there is room
-    static constexpr bool kMoreK = !kCols && (NT == 16 || QP == 2);
+    static constexpr bool kMoreK = !kCols && (NT <= 16 || QP == 2);
     static constexpr int kVSlots = kTiles, kKSlots = kMoreK ? kTiles * 3 / 2 : kTiles;
     static constexpr int kVD = kCols ? kVSlots : kVSlots / 2, kKD = kCols ? kKSlots : kKSlots / 2;  // of a ring
     static constexpr int kQf = 4;                           // segments whose queries' scales are held
@@ -581,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         const uint32_t s_row = tmem + lane_off + h * Lay::kS, o_row = tmem + lane_off + 2 * Lay::kS + h * Lay::kO;
         unsigned char *prow = smem + Lay::OFF_P + h * Lay::kP + wt * 128;
         const int ring = kCols ? 0 : h * Lay::kKD;
+        constexpr int kC = NT < 16 ? NT : 16;    // columns that are taken at a time
         const int first = kCols ? 0 : h;         // the stream's first key tile of a segment
         const int col0 = kCols ? h * NT : 0;     // the query row of its first column
         float *red = fl + Lay::kRed + h * 4 * NT, *fac = fl + Lay::kFac + h * NT;
@@ -636,24 +638,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 // x = log2 of the weights, less `less` (the references, or 0); the largest
                 auto read_s = [&](const float *less) {
 #pragma unroll
-                    for (int c = 0; c < NT; c += 16) {
-                        uint32_t s0[16], s1[16];
-                        tmem_ld<16>(s_row + c, s0);
-                        tmem_ld<16>(s_row + NT + c, s1);
+                    for (int c = 0; c < NT; c += kC) {
+                        uint32_t s0[kC], s1[kC];
+                        tmem_ld<kC>(s_row + c, s0);
+                        tmem_ld<kC>(s_row + NT + c, s1);
                         tmem_wait_ld();
-                        uint64_t y[8];
+                        uint64_t y[kC / 2];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < kC / 2; ++e)
                             y[e] = f2_fma(u2_pack(s1[2 * e], s1[2 * e + 1]), f2_pack(0x1p-5f, 0x1p-5f), u2_pack(s0[2 * e], s0[2 * e + 1]));
                         if constexpr (QP == 3) {
-                            tmem_ld<16>(s_row + 2 * NT + c, s0);
+                            tmem_ld<kC>(s_row + 2 * NT + c, s0);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
+                            for (int e = 0; e < kC / 2; ++e)
                                 y[e] = f2_fma(u2_pack(s0[2 * e], s0[2 * e + 1]), f2_pack(0x1p-10f, 0x1p-10f), y[e]);
                         }
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
+                        for (int e = 0; e < kC; e += 4) {
                             const float4 f4 = *reinterpret_cast<const float4 *>(qs + c + e), m4 = *reinterpret_cast<const float4 *>(less + c + e);
                             const uint64_t a = f2_fma(f2_mul(y[e >> 1], f2_pack(f4.x, f4.y)), ks2, lv2),
                                            b = f2_fma(f2_mul(y[(e >> 1) + 1], f2_pack(f4.z, f4.w)), ks2, lv2);
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                             tmem_ld<16>(o_row + c, ov);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * fac[c % NT + e]);
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * fac[(c + e) % NT]);
                             tmem_st16(o_row + c, ov);
                         }
                         tmem_wait_st();
@@ -726,11 +728,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 // the stream's previous PV has read W
                 if (t > 0 && !(ok = wait_for(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
 #pragma unroll
-                for (int q = 0; q < NT / 16; ++q) {
-                    uint32_t piece[Lay::PP][4];
+                for (int q = 0; q < NT / kC; ++q) {
+                    uint32_t piece[Lay::PP][kC / 4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int c = q * 16 + e * 2;
+                    for (int e = 0; e < kC / 2; ++e) {
+                        const int c = q * kC + e * 2;
                         const float w0 = fast_exp2(x[c]), w1 = fast_exp2(x[c + 1]);
                         l[c] = fmaf(w0, inv_vs, l[c]);
                         l[c + 1] = fmaf(w1, inv_vs, l[c + 1]);
@@ -745,10 +747,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                         }
                     }
                     // 16-byte chunk c of a key's row sits at c ^ (key % 8)
+                    if constexpr (kC == 8) {  // both pieces in one chunk
+                        static_assert(Lay::PP == 2);
+                        *reinterpret_cast<uint4 *>(prow + ((wt & 7) << 4)) = make_uint4(piece[0][0], piece[0][1], piece[1][0], piece[1][1]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < Lay::PP; ++i)
-                        *reinterpret_cast<uint4 *>(prow + (((i * (NT / 16) + q) ^ (wt & 7)) << 4)) =
-                            make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+                        for (int i = 0; i < Lay::PP; ++i)
+                            *reinterpret_cast<uint4 *>(prow + (((i * (NT / 16) + q) ^ (wt & 7)) << 4)) =
+                                make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -772,14 +779,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 if (!(ok = wait_for(bar(Lay::B_BOTH), n & 1, abort_flag))) break;
             }
             tc_fence_after();
-            // this stream writes the query rows [c_lo, c_lo + kMine): its own, or half of the streams' common ones
-            constexpr int kMine = kCols ? NT : NT / 2;
+            // this stream writes the query rows [c_lo, c_lo + kMine): its own, or half of the streams' common ones (A all of eight)
+            constexpr int kMine = kCols || NT == 8 ? NT : NT / 2;
             const int c_lo = h * kMine, acc = kCols ? h : 0;  // the stream whose state counts as A's
             const bool bad = bad_seg[n & (kBadRing - 1)] == n + 1;  // a table entry of the segment was bad
             float *piece = it.part < 0 ? nullptr
                                        : p.pieces + (static_cast<size_t>(blockIdx.x) * 2 + it.part) * Lay::kPieceFloats;
             float *wa = fl + Lay::kWgt + par * 2 * NT, *wb = wa + NT;
-            if (wt < kMine) {
+            if (wt < kMine && c_lo < Lay::kNC) {
                 const int c = c_lo + wt, ca = c - (kCols ? col0 : 0);  // its column in the stream
                 const float *sa = fl + Lay::kSum + (par * 2 + acc) * 4 * NT + ca, *sb = fl + Lay::kSum + (par * 2 + 1) * 4 * NT + ca;
                 const float ma = fl[Lay::kMax + (par * 2 + acc) * NT + ca], mb = cnt_b > 0 ? fl[Lay::kMax + (par * 2 + 1) * NT + ca] : kUnset;
@@ -910,8 +917,10 @@ cudaError_t launch_chunk_q8(const ChunkQ8Args &x, cudaStream_t stream) {
     prm.G = a.Hq / a.Hkv;
     prm.inv_g = (65536 + prm.G - 1) / prm.G;
     const long long rows = static_cast<long long>(a.max_seqlen_q) * prm.G;
+    // Up to eight rows (bf16, whose two pieces of eight columns are the least N of the instruction) a form of their own halves the
+    // softmax: 256 single tokens 197 -> 190 us.
     // gathered keys are bound by the one warp that copies them, whatever the columns: one form for all
-    const int form = gather || rows > 32 ? 64 : rows > 16 ? 32 : 16;
+    const int form = gather || rows > 32 ? 64 : rows > 16 ? 32 : rows > 8 || a.dtype != PA_BF16 ? 16 : 8;
     prm.tt = prm.item_tok = form / prm.G;
     prm.cu_q = a.cu_q;
     prm.ctx = a.ctx;
@@ -944,6 +953,9 @@ cudaError_t launch_chunk_q8(const ChunkQ8Args &x, cudaStream_t stream) {
         using E = decltype(e);
         constexpr int HD = decltype(hd)::value;
         if (gather) return launch_typed<E, HD, 32, true, true>(prm, stream);
+        if constexpr (E::kIsBf16) {
+            if (form == 8) return launch_typed<E, HD, 8, false, false>(prm, stream);
+        }
         if (form == 16) return launch_typed<E, HD, 16, false, false>(prm, stream);
         if (form == 32) return launch_typed<E, HD, 32, false, false>(prm, stream);
         return launch_typed<E, HD, 32, true, false>(prm, stream);

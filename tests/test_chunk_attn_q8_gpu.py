@@ -258,6 +258,17 @@ def test_many_sequences():
     Case(lens, 4, 2, 64, 16, "bf16").check()
 
 
+@pytest.mark.parametrize("Hq,Hkv,q", [(8, 1, 1), (7, 1, 1), (14, 2, 1), (3, 1, 2), (4, 1, 2), (2, 1, 4), (6, 6, 8), (5, 5, 7)])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 256), (128, 8)])
+def test_up_to_eight_rows(Hq, Hkv, q, D, bs):
+    c = Case([(q, 2000), (max(q - 1, 1), 129), (q, q), (q, 700)], Hq, Hkv, D, bs, "bf16", window=0 if D == 64 else 300)
+    c.check()
+    for s, (_, n) in enumerate(c.lens):  # scores that grow along the keys: references move
+        j = torch.arange(max(0, n - q - 299) if c.window else 0, n, device="cuda")
+        c.ks[c.bt[s].long()[j // bs], :, j % bs] *= (1 + j[:, None] / 40.0)
+    c.check()
+
+
 @pytest.mark.parametrize("Hq,Hkv,window", [(320, 320, 0), (96, 48, 0), (33, 11, 50)])
 def test_many_heads(Hq, Hkv, window):
     # more heads than CTAs, and shares that begin and end inside of a head's sequences; some sequences without work
