@@ -18,7 +18,7 @@
 // below e4m3's 448, and what is smaller than 2^-16 (2^-21) beside a largest w of 16 counts for nothing.
 //
 // Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. 256 single tokens over 100-4096 keys, 16/8 heads x 128,
-// block 256: 190 us, 6.2 TB/s, 0.93 of a copy. The loads run ahead in rings of tiles; two streams of softmax
+// block 256: 190-195 us by box, 6.1-6.2 TB/s, 0.91-0.93 of a copy. The loads run ahead in rings of tiles; two streams of softmax
 // warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a segment. On
 // the way to that: 305 us before the code of all roles stayed in the instruction cache, the scales came by cp.async and table
 // entries a tile ahead (229), 224 with packed arithmetic on the scores and three K tiles a stream, 209 without a meeting of
