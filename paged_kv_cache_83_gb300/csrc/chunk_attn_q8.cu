@@ -7,15 +7,19 @@
 // to the tensor cores as they lie in the cache, without a conversion: keys are the 128 rows, query rows the
 // columns, as in chunk_attn_narrow.cu,
 //   S^T = K8 Q^T,   O^T += V8^T W^T,
-// and what meets them is split into e4m3 pieces, side by side as further columns of the same instruction:
-//   q = 2^e (q0 + q1 / 32 [+ q2 / 1024]): two pieces hold a bf16 number (8 bits) exactly, three an fp16 number (11 bits),
-//     where its magnitude is above 2^-14 of its row's largest; below that the error is at most 2^-24 (2^-29) of the largest;
-//   w = w0 + w1 / 32 [+ w2 / 1024], a weight of the softmax, with an error of at most 2^-8 (2^-12) of itself, where bf16's (fp16's)
-//     is 2^-9 (2^-12), and 2^-16 (2^-21) absolute.
+// and what meets them is split into pieces of 8 bits, side by side as further columns of the same instruction:
+//   q = 2^e (q0 + q1 / 32 [+ q2 / 1024]) in e4m3: two pieces hold a bf16 number (8 bits) exactly, three an fp16 number (11 bits),
+//     where its magnitude is above 2^-14 of its row's largest; below that the error is at most 2^-22 (2^-27) of the largest;
+//   w, a weight of the softmax. In fp16 w0 + w1 / 32 + w2 / 1024 in e4m3: off by at most 2^-11 of itself, as an fp16 number is, or
+//     2^-20. In bf16 w0 + (w1 + w2) / 8 in e5m2, whose 3 bits each reach down to 2^-16: off by at most 2^-8 of itself, as a
+//     bf16 number is, or 2^-19, which is 2^-30 of a largest w of 2^11. (As two e4m3 pieces what lay below 2^-19 of the largest
+//     counted in the sum but not in the output: behind one heavy key a tail of 20,000 such keys was lost. The third piece costs
+//     0.2 to 9 % more time, most at 17 to 32 query rows; an e5m2 number is the upper byte of an fp16 one, so that it takes no
+//     conversions.)
 // A softmax thread owns one key, so that both scales are one number a thread. The values' scale goes into the
 // exponent: x_j = s_j + log2 vs_j, w_j = 2^(x_j - m), O = sum w_j V8_j, and the sum takes w_j / vs_j = 2^(s_j - m). The reference m is
-// 4 below the largest x of the first tile and moves when some x exceeds it by more than 8: a w is at most 256,
-// below e4m3's 448, and what is smaller than 2^-16 (2^-21) beside a largest w of 16 counts for nothing.
+// 4 (bf16: 11) below the largest x of the first tile and moves when some x exceeds it by more than 8 (15): a w is at most
+// 2^8 (2^15), below e4m3's (e5m2's) largest number.
 //
 // Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. 256 single tokens over 100-4096 keys, 16/8 heads x 128,
 // block 256: 190-195 us by box, 6.1-6.2 TB/s, 0.91-0.93 of a copy. The loads run ahead in rings of tiles; two streams of softmax
@@ -55,7 +59,7 @@ struct Q8Params : ChunkParams {
 template <int HD, int NT, int QP, bool kCols>
 struct LayQ8 {
     static constexpr int kNC = kCols ? 2 * NT : NT;         // query rows
-    static constexpr int PP = QP;                           // pieces of a weight
+    static constexpr int PP = 3;                            // pieces of a weight
     static constexpr int kKV = BN * HD;                     // bytes of a tile
     static constexpr int kQ = kNC * QP * HD;
     static constexpr int kP = BN * 128;                     // W^T: a 128-byte row a key, PP * NT of it used
@@ -85,7 +89,7 @@ struct LayQ8 {
     static constexpr int kSmem = OFF_MISC + 16 + 1024;
     static_assert(kSmem <= 232448, "shared memory per CTA");
     static_assert(kQ % 1024 == 0 && kKV % 1024 == 0 && OFF_BAR % 8 == 0);
-    static constexpr int kS = QP * NT, kO = PP * NT;        // columns of a stream's S and O
+    static constexpr int kS = QP * NT, kO = (PP * NT + 15) / 16 * 16;  // columns of a stream's S and O (a multiple of 16 for an instruction of 128 rows)
     static constexpr int kNeed = 2 * (kS + kO);
     static constexpr int kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
     static constexpr size_t kPieceFloats = piece_floats(kNC, HD);
@@ -139,6 +143,20 @@ __device__ __forceinline__ __half2 left_of(__half2 v, uint32_t piece) {
     const __half2 k = __float2half2_rn(32.f);
     return __hfma2(from_e4m3x2(piece), __hneg2(k), __hmul2(v, k));
 }
+
+// Two fp16 numbers of at most 2^15 in e5m2, the upper bytes of the halves: the nearest (half-way cases away from zero), or the next towards
+// zero; and what that leaves of them, exact, times 8 if asked for. (Of a NaN comes any number: the sum of the weights keeps it.)
+__device__ __forceinline__ uint32_t to_e5m2x2(__half2 v, bool nearest) { return *reinterpret_cast<uint32_t *>(&v) + (nearest ? 0x00800080u : 0u); }
+__device__ __forceinline__ __half2 left_of_e5m2(__half2 v, uint32_t piece, bool times8) {
+    piece &= 0xff00ff00u;
+    const __half2 r = __hsub2(v, *reinterpret_cast<__half2 *>(&piece));
+    return times8 ? __hmul2(r, __float2half2_rn(8.f)) : r;
+}
+// where the reference lies below the largest x that sets it, and how far above it an x may be before it moves
+template <bool kBf16>
+constexpr float kBelow = kBf16 ? 11.f : 4.f;
+template <bool kBf16>
+constexpr float kAbove = kBf16 ? 15.f : 8.f;
 
 __device__ __forceinline__ float max_of(float a, float b, float c) {
     float d;
@@ -489,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
         // ============================ MMA issuer of one stream =============================
         const int h = warp - 1;
         constexpr uint32_t IQK = idesc_e4m3(BM, Lay::kS, false);             // A = K rows, B = Q pieces, both K-major
-        constexpr uint32_t IPV = idesc_a_mn(idesc_e4m3(BM, Lay::kO, true));  // A = V^T, B = W^T pieces, both MN-major
+        // A = V^T, B = W^T pieces, both MN-major; B's type 0 is e4m3, 1 e5m2
+        constexpr uint32_t IPV = idesc_a_mn(idesc_e4m3(BM, Lay::kO, true)) | (E::kIsBf16 ? 1u << 10 : 0u);
         const int k_ring = kCols ? 0 : h * Lay::kKD, v_ring = kCols ? 0 : h * Lay::kVD;  // the stream's first slots
         const int first = kCols ? 0 : h;                                      // and key tile
         const uint64_t dq0 = desc_rows<HD>(sbase + Lay::OFF_Q + (kCols ? h * Lay::kS * HD : 0), 16);
@@ -659,8 +678,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                             const float4 f4 = *reinterpret_cast<const float4 *>(qs + c + e), m4 = *reinterpret_cast<const float4 *>(less + c + e);
                             const uint64_t a = f2_fma(f2_mul(y[e >> 1], f2_pack(f4.x, f4.y)), ks2, lv2),
                                            b = f2_fma(f2_mul(y[(e >> 1) + 1], f2_pack(f4.z, f4.w)), ks2, lv2);
-                            x[c + e] = f2_lo(a) - m4.x, x[c + e + 1] = f2_hi(a) - m4.y;
-                            x[c + e + 2] = f2_lo(b) - m4.z, x[c + e + 3] = f2_hi(b) - m4.w;
+                            if constexpr (E::kIsBf16) {  // (packed, which gains 2 % there; in fp16 it costs as much at 63 rows)
+                                const uint64_t neg = f2_pack(-1.f, -1.f);
+                                const uint64_t xa = f2_fma(f2_pack(m4.x, m4.y), neg, a), xb = f2_fma(f2_pack(m4.z, m4.w), neg, b);
+                                x[c + e] = f2_lo(xa), x[c + e + 1] = f2_hi(xa), x[c + e + 2] = f2_lo(xb), x[c + e + 3] = f2_hi(xb);
+                            } else {
+                                x[c + e] = f2_lo(a) - m4.x, x[c + e + 1] = f2_hi(a) - m4.y;
+                                x[c + e + 2] = f2_lo(b) - m4.z, x[c + e + 3] = f2_hi(b) - m4.w;
+                            }
                         }
                     }
                     if (masked) {
@@ -673,15 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                     for (int c = 0; c < NT; c += 2) most = max_of(most, x[c], x[c + 1]);
                     return most;
                 };
-                // A reference moves when some x exceeds it by more than 8: the sum uses the same
-                // reference, so the result is exact, and the weights stay at most 2^8. The segment's first tile sets the
+                // A reference moves when some x exceeds it by more than kAbove: the sum uses the same
+                // reference, so the result is exact, and the weights stay at most 2^kAbove. The segment's first tile sets the
                 // references. (Where they move the scores are read once more, by the same code.)
                 any = i == first;
 #pragma unroll 1
                 for (bool set = false;;) {
                     const float most = read_s(any ? fl + Lay::kZero : mx);
                     if (!any) {
-                        if (set || !(ok = meet(most > 8.f, any)) || !any) break;
+                        if (set || !(ok = meet(most > kAbove<E::kIsBf16>, any)) || !any) break;
                         continue;
                     }
 #pragma unroll
@@ -694,9 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                         const float most = fmaxf(fmaxf(red[wt], red[NT + wt]), fmaxf(red[2 * NT + wt], red[3 * NT + wt]));
                         // columns without a query row have a reference that leaves them no weight
                         const float old = i > first ? mx[wt] : col0 + wt < rows ? kUnset : INFINITY;
-                        const bool move = most > old + 8.f;  // never where old is +inf, or the largest -inf
-                        fac[wt] = move ? fast_exp2(old - (most - 4.f)) : 1.f;
-                        mx[wt] = move ? most - 4.f : old;
+                        const bool move = most > old + kAbove<E::kIsBf16>;  // never where old is +inf, or the largest -inf
+                        fac[wt] = move ? fast_exp2(old - (most - kBelow<E::kIsBf16>)) : 1.f;
+                        mx[wt] = move ? most - kBelow<E::kIsBf16> : old;
                     }
                     if (!(ok = meet(false, any))) break;
 #pragma unroll
@@ -727,29 +752,45 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 if (lane == 0) mbar_arrive(bar(Lay::B_F + h));  // S has been read
                 // the stream's previous PV has read W
                 if (t > 0 && !(ok = wait_for(bar(Lay::B_O + h), (t - 1) & 1, abort_flag))) break;
+                // the weights as the tensor cores take them, three pieces each; the sum is of the weights themselves
+                const uint64_t inv2 = f2_pack(inv_vs, inv_vs);
 #pragma unroll
                 for (int q = 0; q < NT / kC; ++q) {
                     uint32_t piece[Lay::PP][kC / 4];
 #pragma unroll
-                    for (int e = 0; e < kC / 2; ++e) {
-                        const int c = q * kC + e * 2;
-                        const float w0 = fast_exp2(x[c]), w1 = fast_exp2(x[c + 1]);
-                        l[c] = fmaf(w0, inv_vs, l[c]);
-                        l[c + 1] = fmaf(w1, inv_vs, l[c + 1]);
-                        // the weights as the tensor cores take them, two or three e4m3 numbers each; the sum is of the weights
-                        // themselves
-                        __half2 w = __floats2half2_rn(w0, w1);
+                    for (int e = 0; e < kC / 4; ++e) {
+                        const int c = q * kC + e * 4;
+                        __half2 w[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float w0 = fast_exp2(x[c + 2 * i]), w1 = fast_exp2(x[c + 2 * i + 1]);
+                            if constexpr (E::kIsBf16) {
+                                const uint64_t sum = f2_fma(f2_pack(w0, w1), inv2, f2_pack(l[c + 2 * i], l[c + 2 * i + 1]));
+                                l[c + 2 * i] = f2_lo(sum), l[c + 2 * i + 1] = f2_hi(sum);
+                            } else {
+                                l[c + 2 * i] = fmaf(w0, inv_vs, l[c + 2 * i]);
+                                l[c + 2 * i + 1] = fmaf(w1, inv_vs, l[c + 2 * i + 1]);
+                            }
+                            w[i] = __floats2half2_rn(w0, w1);
+                        }
 #pragma unroll
                         for (int i = 0; i < Lay::PP; ++i) {
-                            const uint32_t a = to_e4m3x2(w);
-                            if (i + 1 < Lay::PP) w = left_of(w, a);
-                            piece[i][e >> 1] = e & 1 ? piece[i][e >> 1] | a << 16 : a;
+                            if constexpr (E::kIsBf16) {
+                                const bool last = i + 1 == Lay::PP;
+                                const uint32_t a = to_e5m2x2(w[0], !last), b = to_e5m2x2(w[1], !last);
+                                piece[i][e] = __byte_perm(a, b, 0x7531);
+                                if (!last) w[0] = left_of_e5m2(w[0], a, i == 0), w[1] = left_of_e5m2(w[1], b, i == 0);
+                            } else {
+                                const uint32_t a = to_e4m3x2(w[0]), b = to_e4m3x2(w[1]);
+                                piece[i][e] = a | b << 16;
+                                if (i + 1 < Lay::PP) w[0] = left_of(w[0], a), w[1] = left_of(w[1], b);
+                            }
                         }
                     }
                     // 16-byte chunk c of a key's row sits at c ^ (key % 8)
-                    if constexpr (kC == 8) {  // both pieces in one chunk
-                        static_assert(Lay::PP == 2);
+                    if constexpr (kC == 8) {  // two pieces in a chunk
                         *reinterpret_cast<uint4 *>(prow + ((wt & 7) << 4)) = make_uint4(piece[0][0], piece[0][1], piece[1][0], piece[1][1]);
+                        *reinterpret_cast<uint4 *>(prow + ((1 ^ (wt & 7)) << 4)) = make_uint4(piece[2][0], piece[2][1], 0u, 0u);
                     } else {
 #pragma unroll
                         for (int i = 0; i < Lay::PP; ++i)
@@ -821,7 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                     for (int e = 0; e < W; ++e) {
                         v[e] = __uint_as_float(part[Lay::PP - 1][e]);
 #pragma unroll
-                        for (int i = Lay::PP - 2; i >= 0; --i) v[e] = fmaf(v[e], 0x1p-5f, __uint_as_float(part[i][e]));
+                        for (int i = Lay::PP - 2; i >= 0; --i)
+                            v[e] = fmaf(v[e], !E::kIsBf16 ? 0x1p-5f : i == 0 ? 0x1p-3f : 1.f, __uint_as_float(part[i][e]));
                     }
                 };
                 read_o(oa, o);
