@@ -430,11 +430,11 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
  *     first keys of a piece were;
  *   beyond that the rows are widened to the storage type, exactly, and a weight times its value's scale is rounded to it.
  *
- * k_cache, v_cache  e4m3 pools [num_blocks, block_size, Hkv, D]. The pattern of a NaN counts as one in rows whose scale is NaN,
- *               as pa_norm_rope_store_kv writes them; with a finite scale it is not looked for.
+ * k_cache, v_cache  e4m3 pools [num_blocks, block_size, Hkv, D]. The pattern of a NaN counts as one in rows whose scale is NaN or
+ *               infinite, as pa_norm_rope_store_kv writes them; with a finite scale it is not looked for.
  * k_scale, v_scale  fp32 [num_blocks, Hkv, block_size], 16-byte aligned. Positive; k_scale from 2^-126, v_scale from 2^-90 to
  *               2^60, those of a sequence and kv head at most 2^100 apart; scale * k_scale * 369 finite. A NaN or an infinity
- *               (a row that held one) makes the output of what sees it NaN, and may make that of the call's other rows of that
+ *               (a row that held one) makes the output of what sees it NaN whatever the row's numbers, and may make that of the call's other rows of that
  *               sequence and kv head NaN too (cf. pa_chunk_attn: keys that some rows see and others do not).
  * q, out, dtype fp16 or bf16; out may be q itself.
  * max_seqlen_q  chooses the kernel for the whole call: up to 8 query rows a kv head (bf16), 16, 32, 64, or items of 256.

@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_q8_kernel(const __grid_cons
                 const int slot = ring + static_cast<int>(t % Lay::kKD);
                 if (!(ok = wait_for(bar(Lay::B_KFULL + slot), (t / Lay::kKD) & 1, abort_flag))) break;
                 const float *sc = reinterpret_cast<const float *>(smem + Lay::OFF_SCALE + slot * 2 * BN * 4);
-                float ks = sc[wt], vs = sc[BN + wt];
+                float ks = finite_or_nan(sc[wt]), vs = finite_or_nan(sc[BN + wt]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(Lay::B_KEMPTY + slot));  // the scales have been read
                 if (key < it.n_lo || key >= it.n_end) ks = vs = 1.f;    // no row sees it: whatever lies there

@@ -95,7 +95,7 @@ __device__ __forceinline__ void regs_up() {
 // Two e4m3 numbers in the upper bytes of x's halves, in 16 bits, exactly. The fields move as they are, which leaves the value
 // times 2^(bias - 7): fp16 keeps its 2^-8 (the keys' numbers make up for it), bf16's 2^-120 is multiplied away. (With the
 // conversion instructions e4m3 -> fp16 (-> fp32 -> bf16) the loaders took 1130 clocks for what takes them 500 so.) The pattern
-// of a NaN becomes +-480: a row that held a NaN has a NaN scale.
+// of a NaN becomes +-480: a row that held a NaN or an infinity has a scale that is not finite, which makes NaN of it.
 template <class E>
 __device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t x) {
     if constexpr (!E::kIsBf16) return ((x >> 1) & 0x3f803f80u) | (x & 0x80008000u);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) chunk_q8_wide_kernel(const __
                 if (!is_v && lane < 16) {
                     const int k = hf * kHalfKeys + w * 16 + lane;
                     const float *sc = reinterpret_cast<const float *>(smem + Lay::OFF_SCALE) + slot * 2 * kHalfKeys + w * 16 + lane;
-                    float ks = sc[0], vs = sc[kHalfKeys];
+                    float ks = finite_or_nan(sc[0]), vs = finite_or_nan(sc[kHalfKeys]);
                     if (k < z0 || k >= z1) ks = vs = 1.f;  // no row sees it: numbers that do no harm, whatever lies there
                     float *keys = reinterpret_cast<float *>(smem + Lay::OFF_KEYS) + (i % kKeyRing) * 3 * BN + k;
                     if constexpr (E::kIsBf16) {

@@ -76,6 +76,10 @@ __device__ __forceinline__ void give_up(int32_t *err, volatile int *abort_flag) 
 // the shares
 // ------------------------------------------------------------------------------------------
 
+// The scale of a row of an 8-bit cache. An infinite one becomes NaN (the row held an infinity, and times the numbers that stand for it the
+// scale could give either infinity, or a weight of zero), any other stays: s + 0 s.
+__device__ __forceinline__ float finite_or_nan(float s) { return __fmaf_rn(s, 0.f, s); }
+
 // A length or a table entry. The kernels are launched beside what precedes them, which may still write these: they are
 // read after the wait, by plain loads (the read-only path asks for data that is constant from the kernel's start
 // on, and its loads may be moved before the wait). Past L1, with __ldcg, they cost 0.4 us of a small draft's 8.2.
