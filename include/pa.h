@@ -504,8 +504,8 @@ pa_status pa_sample(int32_t *tokens, const void *logits, int64_t row_stride, int
  *           the vocabulary, exceeds floor(W * floor(u[b-1] * 2^31) / 2^31)
  *       accepted[s] = k;  next_tokens[a .. b) = the k drafts, t, and -1 from there on
  *
- * So the number of new tokens is accepted + 1. Products of the tests and sums of the weights are exact, the
- * differences p - q are fp32 (subnormal ones count as 0): the tokens do not depend on how the work is divided.
+ * So the number of new tokens is accepted + 1. Products of the tests and sums of the weights are exact (subnormal numbers
+ * count as what they are), the differences p - q are fp32: the tokens do not depend on how the work is divided.
  * A draft outside [0, V) ends the drafts before it, as if the sequence had no more (k == n): a captured step
  * pads shorter drafts with -1.
  *

@@ -5,7 +5,8 @@
 // min(1, p(x) / q(x)), the token after the last one taken comes from max(p - q, 0), so that the tokens have
 // the target's distribution p whatever the drafter's q.
 //
-// The mathematics: the tests u q(x) < p(x) are exact, being products of two fp32 numbers in 64 bits. A weight is the whole
+// The mathematics: the tests u q(x) < p(x) are exact, being products of two fp32 numbers in 64 bits (and this file is compiled without
+// the fast mathematics that takes subnormal numbers for 0). A weight is the whole
 // number rint(r 2^44), r in [0, 1]; whole numbers add up to the same sum in any order, so that the token does not depend
 // on how the row is divided.
 //
