@@ -88,7 +88,9 @@ __device__ __forceinline__ void weight(float r, int &hi, int &lo) {
     hi = __float_as_int(h) - __float_as_int(2.f);
     lo = __float_as_int(__fadd_rn(rest, 0x1.8p-21f)) - __float_as_int(0x1.8p-21f);
 }
-__device__ __forceinline__ long long whole(int hi, int lo) { return (static_cast<long long>(hi) << 22) + lo; }
+// Sums of hi and lo of up to kLaneMost weights, each at most 2^22 and 2^21 in magnitude, whatever the row holds
+constexpr int kLaneMost = 1023;
+__device__ __forceinline__ long long whole(uint32_t hi, int lo) { return (static_cast<long long>(hi) << 22) + lo; }
 
 template <class E, int kN>
 __device__ __forceinline__ void weights_at(const Drawn<typename E::T> &d, int i, int V, float (&r)[kN]) {
@@ -174,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, kVerifySm / kThreads) verify_kernel(
     const int first = (static_cast<int>(rank) * kWarps + warp) * p.slice - d.shift;  // of this warp's slice
     for (int attempt = 0;; ++attempt) {
         // ---- the sums of the slices
-        int hi = 0, lo = 0;
+        uint32_t hi = 0;
+        int lo = 0;
 #pragma unroll 2
         for (int i = first + lane * kN; i < first + p.slice && i < p.V; i += 32 * kN) {
             float r[kN];
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, kVerifySm / kThreads) verify_kernel(
             for (int e = 0; e < kN; ++e) {
                 int h, l;
                 weight(r[e], h, l);
-                hi += h, lo += l;
+                hi += static_cast<uint32_t>(h), lo += l;
             }
         }
         long long sum = whole(hi, lo);
@@ -303,8 +306,10 @@ cudaError_t active_clusters(int dev, const int *&most) {
 template <class E, int kThreads>
 cudaError_t launch_verify_as(VerifyParams &prm, int ctas, cudaStream_t stream) {
     constexpr int kN = 16 / sizeof(typename E::T);
-    const int per = 32 * kN, parts = ctas * (kThreads / 32);
-    prm.slice = ((prm.V + kN + parts - 1) / parts + per - 1) / per * per;
+    constexpr int per = 32 * kN;
+    const auto slice_of = [](int V, int parts) constexpr { return ((V + kN + parts - 1) / parts + per - 1) / per * per; };
+    static_assert(slice_of(kSampleMaxVocab, kThreads / 32) / 32 <= kLaneMost, "a lane's sums");
+    prm.slice = slice_of(prm.V, ctas * (kThreads / 32));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;

@@ -33,3 +33,16 @@ def test_subnormal_numbers_in_a_test_are_what_they_are(dtype, certain):
         assert float(d.p[2 * s, 40 + s]) == p and (certain or float(d.q[2 * s, 40 + s]) == q) and float(d.u[2 * s]) == u
         stands.append(int(u * q < p))  # exact in 64 bits
     assert d.check() == stands and 0 < sum(stands) < len(stands)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [1, 400])
+@pytest.mark.parametrize("V", [9000, 262144])
+def test_rows_of_ones(V, S, dtype):
+    # each number counts as 1 (larger ones do too): their sum is far from 1, and the token that of the definition. With 400 sequences a
+    # sequence has one CTA, and a lane up to 704 of these numbers.
+    d = Drafts([1] * S, V, dtype, certain=True)
+    d.p[:] = 1
+    d.p[:, V // 3:V // 2] = 2
+    d.u[:] = torch.linspace(0, 1 - 2.0 ** -24, S, device="cuda") if S > 1 else 0.7
+    d.check()
