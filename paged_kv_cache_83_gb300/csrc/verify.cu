@@ -16,6 +16,8 @@
 // distributed shared memory; the CTA whose slice holds the token reads one warp's part of it again, from L2. One launch, no
 // workspace. 256 sequences, 151,936 fp32 numbers in p and in q: 51 us, 0.71 of a copy (one CTA a sequence: 78 us); one
 // sequence with a draft of four tokens and a drafter without probabilities, bf16: 7.0 us (8.9 in smaller clusters).
+#include <atomic>
+
 #include "pa_internal.h"
 
 namespace pa {
@@ -279,11 +281,12 @@ __global__ void __launch_bounds__(kThreads, kVerifySm / kThreads) verify_kernel(
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Clusters of 1 .. kMostCtas CTAs that are on the SMs at once (asked for once for each kernel and device)
+// Clusters of 1 .. kMostCtas CTAs that are on the SMs at once (asked for once for each kernel and device; threads that ask at the
+// same time write the same numbers, and whoever sees the mark of a full table sees them)
 template <class E, int kThreads>
-cudaError_t active_clusters(int dev, const int *&most) {
-    static int table[64][kMostCtas + 1];  // [0]: filled
-    if (!table[dev][0]) {
+cudaError_t active_clusters(int dev, int (&most)[kMostCtas + 1]) {
+    static std::atomic<int> table[64][kMostCtas + 1];  // [0]: filled
+    if (!table[dev][0].load(std::memory_order_acquire)) {
         for (int ctas = 1; ctas <= kMostCtas; ++ctas) {
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -294,12 +297,14 @@ cudaError_t active_clusters(int dev, const int *&most) {
             cfg.numAttrs = 1;
             cfg.gridDim = dim3(ctas);
             cfg.blockDim = dim3(kThreads);
-            const cudaError_t e = cudaOccupancyMaxActiveClusters(&table[dev][ctas], verify_kernel<E, kThreads>, &cfg);
+            int clusters = 0;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<E, kThreads>, &cfg);
             if (e != cudaSuccess) return e;
+            table[dev][ctas].store(clusters, std::memory_order_relaxed);
         }
-        table[dev][0] = 1;
+        table[dev][0].store(1, std::memory_order_release);
     }
-    most = table[dev];
+    for (int ctas = 1; ctas <= kMostCtas; ++ctas) most[ctas] = table[dev][ctas].load(std::memory_order_relaxed);
     return cudaSuccess;
 }
 
@@ -332,7 +337,7 @@ cudaError_t launch_verify_typed(const VerifyParams &in, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const int *most_384, *most_512;
+    int most_384[kMostCtas + 1], most_512[kMostCtas + 1];
     if ((e = active_clusters<E, 384>(dev, most_384)) != cudaSuccess || (e = active_clusters<E, 512>(dev, most_512)) != cudaSuccess) return e;
     // CTAs of a sequence: slices of at least 4096 numbers, and no more CTAs than are on the SMs at once: each begins and ends
     // with a chain of dependent loads and barriers. Of the two sizes of CTA the one that leaves more threads (p and q in fp32, us,
