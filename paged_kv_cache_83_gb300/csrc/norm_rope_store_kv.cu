@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) norm_rope_store_kv_
             if (step + i < p.qk_steps) {
                 const int r = (step + i) * per_step + row_of_lane;
                 const unsigned char *src = r < p.Hq ? q_row + r * row_bytes : k_row + (r - p.Hq) * row_bytes;
-                if (there0 && r < n_qk) x0[i] = ld_row(src);
-                if (there1 && r < n_qk) x1[i] = ld_row(src + next);
+                const bool mine = step + i < end && r < n_qk;  // a step behind the part's last is another warp's, which may store it in place
+                if (mine && there0) x0[i] = ld_row(src);
+                if (mine && there1) x1[i] = ld_row(src + next);
             } else {
                 const int r = (step + i - p.qk_steps) * per_step + row_of_lane;
                 const unsigned char *src = v_row + r * row_bytes;
