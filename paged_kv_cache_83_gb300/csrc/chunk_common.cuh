@@ -56,8 +56,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return all;
 }
 // The same in few instructions, for kernels whose roles together hardly fit the instruction cache: it counts tries instead of
-// asking for the time (each suspends the thread for a time of the hardware's choosing, a microsecond or more: some seconds in all).
-constexpr uint32_t kWaitTries = 1u << 21;
+// asking for the time. A try that fails suspends the warp for a time of the hardware's choosing, 1.34 us as measured: half a second in
+// all, as kWaitLimitNs. (With the time itself in the loop a window of 1024 over 12 chunks took 208 us instead of 180.)
+constexpr uint32_t kWaitTries = 400000;
 __device__ __forceinline__ bool short_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     bool ok = true;
     for (uint32_t i = 0; !__all_sync(kFull, mbar_try_wait(bar, parity)); ++i)

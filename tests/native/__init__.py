@@ -9,13 +9,13 @@ HERE = Path(__file__).resolve().parent
 BUILD = HERE / "_build"
 
 
-def build_wait_probe() -> Path:
-    """Compile wait_probe.cu (sm_103a, -DPA_TEST_HOOKS) into its own shared library."""
+def build_wait_probe(name: str = "wait_probe") -> Path:
+    """Compile wait_probe.cu or short_wait_probe.cu (sm_103a, -DPA_TEST_HOOKS) into its own shared library."""
     from paged_kv_cache_83_gb300 import build as lib_build
 
-    src = HERE / "wait_probe.cu"
-    out = BUILD / "libwait_probe.so"
-    deps = [src, lib_build.CSRC / "pa_common.cuh", lib_build.ROOT / "include" / "pa.h"]
+    src = HERE / f"{name}.cu"
+    out = BUILD / f"lib{name}.so"
+    deps = [src, lib_build.CSRC / "pa_common.cuh", lib_build.CSRC / "chunk_common.cuh", lib_build.ROOT / "include" / "pa.h"]
     if out.exists() and all(d.stat().st_mtime <= out.stat().st_mtime for d in deps):
         return out
     BUILD.mkdir(parents=True, exist_ok=True)
