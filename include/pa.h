@@ -425,8 +425,8 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
  * Scores, references, sums and accumulators are fp32; the output is rounded once. What is rounded to fewer bits before:
  *   up to 64 query rows a kv head (tokens * Hq / Hkv) the e4m3 rows are operands of the tensor cores as they lie there, and
  *     queries and softmax weights meet them as sums of 8-bit numbers. A query's element is exact where its magnitude is above
- *     2^-14 of the largest of its row, below that to 2^-22 (bf16) or 2^-27 (fp16) of the largest; a weight (times its value's
- *     scale) is rounded to within 2^-8 (2^-11) of itself, or to within 2^-30 (2^-24) of the largest that was seen when the
+ *     2^-14 of the largest of its row, below that to about 2^-22 (bf16) or 2^-27 (fp16) of the largest; a weight (times its value's
+ *     scale) is rounded to within 2^-8 (2^-11) of itself, or to within about 2^-30 (2^-24) of the largest that was seen when the
  *     first keys of a piece were;
  *   beyond that the rows are widened to the storage type, exactly, and a weight times its value's scale is rounded to it.
  *
