@@ -437,7 +437,11 @@ pa_status pa_chunk_attn(void *out, const void *q, const void *k_cache, const voi
  *               (a row that held one) makes the output of what sees it NaN whatever the row's numbers, and may make that of the call's other rows of that
  *               sequence and kv head NaN too (cf. pa_chunk_attn: keys that some rows see and others do not).
  * q, out, dtype fp16 or bf16; out may be q itself.
- * max_seqlen_q  chooses the kernel for the whole call: up to 8 query rows a kv head (bf16), 16, 32, 64, or items of 256.
+ * max_seqlen_q  chooses the kernel for the whole call: up to 8 query rows a kv head (bf16), 16, 32, 64, or items of 256, which
+ *               cost single tokens several times as much: long chunks and single tokens want a call each (250 single tokens and
+ *               two chunks of 2k tokens at 13-14k: 1174 us in one call, 718 in two). Above 64 rows the call takes 1.15 to 1.7
+ *               times what pa_chunk_attn does over 16 bits (two such chunks 528 us against 315, a window of 1024 over 12 chunks
+ *               of 20-700 tokens 191 against 135): the cache of 8 bits is for decoding and drafts.
  * workspace     device scratch of at least pa_chunk_attn_q8_workspace_size(S, Hq, Hkv, D) bytes (41 MB on a GB300 at D = 128,
  *               21 MB at 64). Its contents on entry do not matter; calls that share a workspace must not overlap on the GPU.
  * A bad table entry leaves zero rows for up to 64 / (Hq / Hkv) tokens, with items of 256 rows 256 / (Hq / Hkv) (cf. pa_chunk_attn).

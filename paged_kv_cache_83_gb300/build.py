@@ -5,7 +5,7 @@ library that exports the C ABI of ``include/pa.h``. The runtime is linked shared
 that already loaded PyTorch's CUDA runtime uses that one instance. The binding's argument checks
 (``csrc/args.cpp``) become an extension module for the installed PyTorch and Python. That needs a C++
 compiler and the headers of both; where they are missing the library is built all the same, with a warning,
-and the calls that go through the module (rotation, chunk attention, sampling) raise.
+and the calls that go through the module (rotation, chunk attention, sampling, verification) raise.
 """
 from __future__ import annotations
 

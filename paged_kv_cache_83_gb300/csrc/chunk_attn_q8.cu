@@ -22,7 +22,7 @@
 // 2^8 (2^15), below e4m3's (e5m2's) largest number.
 //
 // Bound by HBM for few query rows: (2 D + 8) bytes a key and kv head. 256 single tokens over 100-4096 keys, 16/8 heads x 128,
-// block 256: 190-195 us by box, 6.1-6.2 TB/s, 0.91-0.93 of a copy. The loads run ahead in rings of tiles; two streams of softmax
+// block 256: 190-195 us by box, 6.1-6.2 TB/s, 0.90-0.93 of a copy (fp16, in sixteen columns, 202-206). The loads run ahead in rings of tiles; two streams of softmax
 // warps take the key tiles in turn, each with its own reference, sum and accumulator, and join at the end of a segment. On
 // the way to that: 305 us before the code of all roles stayed in the instruction cache, the scales came by cp.async and table
 // entries a tile ahead (229), 224 with packed arithmetic on the scores and three K tiles a stream, 209 without a meeting of
@@ -36,7 +36,8 @@
 //   warp 0      producer: K and V tiles of the streams in turn, the scales with the K tile
 //   warps 1, 2  one MMA issuer per stream
 //   warps 4-7   softmax of stream A (tiles 0, 2, ... of a segment), warps 8-11 of stream B (1, 3, ...)
-//   TMEM columns: S_A, S_B (NT for each piece), O_A, O_B (likewise); lanes are keys in S and head elements in O.
+//   TMEM columns: S_A, S_B (NT for each piece of a query), O_A, O_B (NT for each piece of a weight); lanes are keys in S and
+//   head elements in O.
 #include <type_traits>
 
 #include "chunk_narrow.cuh"

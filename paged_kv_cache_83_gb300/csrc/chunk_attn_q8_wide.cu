@@ -19,6 +19,8 @@
 // in P's place (584); sixteen softmax warps, half of a row's keys each (568, registers spill); V widened with its scales
 // (550); 184 registers for the softmax (537); for bf16, too, log2 vs in the exponent and 1 / vs in the sum (587).
 //
+// The softmax spills a little at its 176 registers (head dim 128: bf16 20 bytes stored and 28 loaded, fp16 94 and 120; 64: bf16 4 and 20).
+//
 //   warp 3        scheduler, as in chunk_attn.cu; brings the queries of a segment by TMA
 //   warp 0        producer: halves of K and V tiles as they lie in the cache, and the scales of their keys
 //   warps 1, 2    one MMA issuer per row tile

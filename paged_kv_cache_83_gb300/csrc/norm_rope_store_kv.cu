@@ -14,8 +14,9 @@
 // rotation without norms, a thread takes the same elements of several rows of its token, whose cosines and sines
 // it loads once. The weights come from L1. 33,673 tokens of 16/8 heads x 128 in bf16, into the 8-bit cache: 89 us, 0.84 of a copy
 // (101 without a form for whole rows of 64 or 128 elements, 182 before a warp took a token, 16 elements a lane); 9001 tokens of
-// 14/2 x 64 with three axes into the cache of the storage type: 12.1 us, 0.51; a step of 256 tokens 3.5 us, of 4 tokens 4.1:
-// launch latency.
+// 14/2 x 64 with three axes into the cache of the storage type: 12.3 us, 0.51, in 1.85 waves of blocks (64 registers a thread hold eight of
+// them on an SM; the general forms spill 40 to 90 bytes there, those of whole rows none or 8 to 16); a step of 256 tokens 3.6 us, of 4
+// tokens 3.2: the call's host side.
 #include "pa_internal.h"
 
 namespace pa {
@@ -325,8 +326,9 @@ cudaError_t launch_norm_rope_store_kv(const NormRopeStoreArgs &n, cudaStream_t s
     const int per_step = 32 >> prm.lanes_log2;
     prm.qk_steps = (a.Hq + a.Hkv + per_step - 1) / per_step;
     prm.steps = prm.qk_steps + (a.Hkv + per_step - 1) / per_step;
-    // A warp a token where that leaves the SMs full, else a step each: the time is then one chain of dependent loads (1500
-    // tokens of 14/2 heads x 64: 4.3 us, a warp a token 5.2; 9001: 19.6 and 14.5; 5000 of 16/8 heads x 128: 28.7 and 21.2).
+    // A warp a token where that leaves the SMs full, else a step each: the time is then one chain of dependent loads (a step
+    // each, and a warp a token, us: 14/2 heads x 64 with three axes, cache of the storage type: 1500 tokens 4.2, 4.9; 2400: 6.3, 5.6;
+    // 9001: 17.3, 12.2; 16/8 heads x 128 into 8 bits: 256: 3.7, 7.6; 1500: 9.0, 9.2; 2400: 12.6, 10.2; 5000: 27.4, 20.3).
     prm.part_steps = a.T > device_sm_count() * kFullWarps ? prm.steps : 1;
     prm.parts = (prm.steps + prm.part_steps - 1) / prm.part_steps;
     const long long warps = static_cast<long long>(a.T) * prm.parts;
